@@ -8,6 +8,12 @@
  *   spec_verify_tokenwise  - token-by-token speculative sampling
  *   spec_verify_block      - block verification
  *   adaptive_pick_k        - confidence head + the controller that picks how many drafts to verify
+ * Four more serve the pass whose logits are verified, over a paged key-value cache:
+ *   spec_paged_attention   - the attention of every stream's block (its drafts and the token
+ *                            before them) over the cached context
+ *   spec_cache_append      - the block's keys and values written into their pages
+ *   spec_cache_resize      - pages reserved before a block, and given back after its verify
+ *   spec_cache_fork        - a stream's pages shared with another stream
  * Sources (web pages, cited by title and section):
  *   [P1] "MTP, DSpark and Block Verification, Explained: Six Tokens per Step" (al-engr.com)
  *   [P2] "MTP Heads and Confidence Heads: Linking Three Self-Drafting Routes into One Chain"
@@ -76,10 +82,18 @@ extern "C" {
                                      earlier stream is negative or above kmax */
 #define SPEC_ST_TIMEOUT 6         /* a bounded device wait gave up, or the workspace was not zero-filled */
 #define SPEC_ST_NUMERIC 7         /* the distribution to draw from has zero or non-finite mass */
+/* ... and by the cache calls */
+#define SPEC_ST_NO_PAGES 8        /* the pool has too few free pages for the stream's room */
+#define SPEC_ST_BAD_LENGTH 9      /* a length, advance or room outside the stream's pages or its table row */
+#define SPEC_ST_BAD_PAGE 10       /* a needed page-table entry is not a page of the pool */
+#define SPEC_ST_BAD_STREAM 11     /* a fork's source or destination cannot be used */
 
 /* limits */
 #define SPEC_MAX_KMAX 32          /* drafts per stream */
 #define SPEC_MAX_V 16777216       /* vocabulary size */
+#define SPEC_MAX_STREAMS 65535    /* streams of a cache call */
+#define SPEC_MAX_HEAD 256         /* elements of an attention head */
+#define SPEC_MAX_PAGE 256         /* tokens of a page */
 
 /* columns of the optional diag output (one row per target row) */
 #define SPEC_DIAG_COLS 8
@@ -423,6 +437,164 @@ int spec_cost_curve_observe(void* curve, int32_t num_tokens, float ms);
 int spec_cost_curve_table(void* curve, float* out, int64_t* counters);
 int spec_cost_curve_upload(void* curve, float* device_table, void* stream);
 void spec_cost_curve_destroy(void* curve);
+
+/*
+ * The paged key-value cache.  A verify step scores N_b + 1 slots per stream in one pass of the
+ * target ([P1] §3 "One pass, N slots"): the block of stream b is the last emitted token and its
+ * N_b drafts, at positions length[b] .. length[b] + N_b.  The pass writes the block's keys and
+ * values behind the stream's cached ones (spec_cache_append) and attends over all of them
+ * (spec_paged_attention), layer by layer; the verify call then keeps the first n_emitted[b] of
+ * the block, and spec_cache_resize drops the rest.
+ *   - Pool: K and V [layers, num_pages, Hkv, page_size, D] (dtype), 16-byte aligned.  The
+ *     attention and append calls take one layer's [num_pages, Hkv, page_size, D].
+ *   - page_table [B, max_pages] int32: entry j of stream b is the page with its positions
+ *     j * page_size .. + page_size - 1, the same page of every layer; -1 past the pages it holds.
+ *   - held [B] int32: pages that the stream holds (table entries 0 .. held - 1).
+ *   - length [B] int32: tokens whose keys and values are kept.
+ *   - ref_count [num_pages] int32: streams that hold a page; a page with none is free.  There is
+ *     no other free list.
+ *   - page_size is a power of two from 8 to SPEC_MAX_PAGE; D a multiple of 8 up to SPEC_MAX_HEAD.
+ *   - Blocks are packed as in the verify calls: row cu_drafts[b] + b + i is token i of stream b,
+ *     i <= N_b = cu_drafts[b + 1] - cu_drafts[b] <= kmax.  cu_drafts NULL means N_b = kmax for all
+ *     (kmax = 0: one new token per stream).
+ */
+
+/*
+ * spec_paged_attention - softmax attention of every block row over its stream's cached context.
+ * Row (b, i) stands at position p = length[b] + i; query head h reads key head h / (Hq / Hkv):
+ *   out[row, h] = sum_j e_j v_j / sum_j e_j,   e_j = exp(scale q[row, h] . k_j)
+ * over the visible positions j: j <= p, and with window > 0 only j > p - window or j < sinks (the
+ * first tokens of a stream stay visible).  window = 0 sees everything.  The keys and values of
+ * positions length[b] .. length[b] + N_b must be in the cache (spec_cache_append).  Pages that hold no
+ * visible position are not read, and their table entries may be -1.
+ * q [rows, Hq, D] with q_row_stride elements from row to row (a slice of a wider projection),
+ * out [rows, Hq, D] dense, both in the cache's dtype.  status [B]: SPEC_ST_OK, BAD_OFFSETS (rows not
+ * written), BAD_LENGTH (length < 0 or the block ends past max_pages * page_size: rows are NaN),
+ * BAD_PAGE (entries outside [0, num_pages) at visible positions, whose keys and values read as
+ * zeros), TIMEOUT (every stream's rows undefined).
+ * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before
+ * they meet the values, and the same rounded weights are summed.  A value that is not finite at a
+ * position that one row of a block sees may reach the block's earlier rows; one that no row sees
+ * reaches none.  The result does not depend on the call before it, and is the same from run to run.
+ * workspace: spec_paged_attention_workspace_bytes(args) bytes, 16-byte aligned, its first 256 bytes
+ * zero-filled once before its first use (a call leaves them so); calls that share it must be ordered.
+ * Errors: SPEC_ERR_ARG (NULL pointer, a pool that is not 16-byte aligned, scale not finite),
+ * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of Hkv,
+ * q_row_stride < Hq * D, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
+ * SPEC_ERR_CUDA.  B == 0 launches nothing.
+ */
+typedef struct {
+    int32_t B, kmax;
+    int32_t Hq, Hkv, D;
+    int32_t page_size, num_pages, max_pages;
+    int32_t dtype;
+    int32_t window, sinks;
+    float scale;
+    const int32_t* cu_drafts;    /* [B + 1] or NULL */
+    const int32_t* length;       /* [B] */
+    const int32_t* page_table;   /* [B, max_pages] */
+    const void* q;               /* [rows, Hq, D] */
+    int64_t q_row_stride;        /* elements */
+    const void* k_pages;         /* [num_pages, Hkv, page_size, D] */
+    const void* v_pages;
+    void* out;                   /* [rows, Hq, D] */
+    int32_t* status;             /* [B] */
+    void* workspace;
+    size_t workspace_bytes;
+} spec_attention_args;
+
+int spec_paged_attention(const spec_attention_args* args, void* stream);
+/* Bytes of workspace the call needs (0 for B = 0 and for invalid sizes).  Reads the sizes, the dtype
+ * and the alignment of q; the size also covers every call with smaller B, kmax and max_pages. */
+size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
+
+/*
+ * spec_cache_append - the block's new keys and values into their pages.
+ *   k_pages[page_table[b, p / page_size], h, p % page_size] = k[row, h],   p = length[b] + i
+ * and the same for v.  k, v [rows, Hkv, D] with row strides in elements (slices of a wider
+ * projection); dtype as the pool.  The pages written must belong to the stream alone (ref_count 1,
+ * as spec_cache_resize leaves them).  status [B]: SPEC_ST_OK, BAD_OFFSETS or BAD_LENGTH (nothing
+ * of the stream is written), BAD_PAGE (the rows whose page is not in the pool are not written).
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_DTYPE, SPEC_ERR_SHAPE, SPEC_ERR_CUDA as in spec_paged_attention.
+ */
+typedef struct {
+    int32_t B, kmax;
+    int32_t Hkv, D;
+    int32_t page_size, num_pages, max_pages;
+    int32_t dtype;
+    const int32_t* cu_drafts;    /* [B + 1] or NULL */
+    const int32_t* length;       /* [B] */
+    const int32_t* page_table;   /* [B, max_pages] */
+    const void* k;               /* [rows, Hkv, D] */
+    const void* v;
+    int64_t k_row_stride, v_row_stride;
+    void* k_pages;               /* [num_pages, Hkv, page_size, D] */
+    void* v_pages;
+    int32_t* status;             /* [B] */
+} spec_append_args;
+
+int spec_cache_append(const spec_append_args* args, void* stream);
+
+/*
+ * spec_cache_resize - gives every stream the pages it needs, no more.
+ *   length[b] += advance[b];   held[b] = ceil((length[b] + room[b]) / page_size)
+ * advance [B] (NULL: 0) is the tokens to keep of a block, n_emitted of the verify call (its 0 for a
+ * stream that failed keeps nothing), or negative to roll a stream back; advance = -length with
+ * room 0 releases the stream.  room [B] (NULL: 0) is the tokens that the next append may write.
+ * In this order:
+ *   1. Pages past the new need lose this stream's reference (table entry -1).  So do, from the
+ *      first one on, pages past the kept tokens that another stream holds too.
+ *   2. With room, a page that holds kept tokens and will be written into, and that another stream
+ *      holds too, is replaced by a copy of its own (all layers of K and V); when every holder of
+ *      the page asks for one in this call, the lowest stream keeps the page.
+ *   3. New pages are the lowest pages of the pool that are free after step 1, given out in the
+ *      order of the streams, to each its copy first, then its new positions in order.
+ * status [B]: SPEC_ST_OK; BAD_LENGTH (the stream is left as it was: the new length is negative or
+ * beyond held * page_size, room is negative, length + room is beyond max_pages * page_size, or held
+ * is outside [0, max_pages]); NO_PAGES (streams before it in the batch left too few pages: the new
+ * length and step 1 hold, but the stream got no page and must not be appended to); BAD_PAGE (left as
+ * it was: a page that the call must look at is not in the pool).
+ * k_pool, v_pool: [layers, num_pages, Hkv * page_size * D] in units of page_bytes (a multiple of 16)
+ * per page.  workspace: spec_cache_resize_workspace_bytes(B, num_pages) bytes, 16-byte aligned, any contents.
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_SHAPE (B outside [0, SPEC_MAX_STREAMS], num_pages or max_pages < 1,
+ * layers < 1, page_bytes < 16 or not a multiple of 16), SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA.
+ */
+typedef struct {
+    int32_t B;
+    int32_t page_size, num_pages, max_pages;
+    int32_t layers;
+    int64_t page_bytes;          /* Hkv * page_size * D * sizeof(dtype) */
+    const int32_t* advance;      /* [B] or NULL */
+    const int32_t* room;         /* [B] or NULL */
+    int32_t* page_table;         /* [B, max_pages], updated */
+    int32_t* held;               /* [B], updated */
+    int32_t* length;             /* [B], updated */
+    int32_t* ref_count;          /* [num_pages], updated */
+    void* k_pool;                /* [layers, num_pages, page_bytes] */
+    void* v_pool;
+    int32_t* status;             /* [B] */
+    void* workspace;
+    size_t workspace_bytes;
+} spec_resize_args;
+
+int spec_cache_resize(const spec_resize_args* args, void* stream);
+size_t spec_cache_resize_workspace_bytes(int32_t B, int32_t num_pages);
+
+/*
+ * spec_cache_fork - n times: stream dst[e] becomes a continuation of stream src[e].
+ * dst gives up the pages it held, takes src's length and holds the ceil(length / page_size) pages of
+ * src's tokens with it (one more reference each; room that src has reserved is not shared).  Nothing
+ * is copied: the next spec_cache_resize with room copies a page before it is written into.
+ * src, dst [n] int32.  A stream may be the source of many pairs.  status [n]: SPEC_ST_OK, or (dst
+ * left as it was) BAD_STREAM: src or dst outside [0, B), dst the source of any pair of the call,
+ * or dst also the destination of an earlier pair; BAD_LENGTH: held or length of src or dst is not
+ * within its table row; BAD_PAGE: an entry of src or dst is not a page of the pool.
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_SHAPE (n or B outside [0, SPEC_MAX_STREAMS], sizes < 1), SPEC_ERR_CUDA.
+ * n == 0 launches nothing.
+ */
+int spec_cache_fork(const int32_t* src, const int32_t* dst, int32_t n, int32_t B, int32_t page_size,
+                    int32_t num_pages, int32_t max_pages, int32_t* page_table, int32_t* held,
+                    int32_t* length, int32_t* ref_count, int32_t* status, void* stream);
 
 /*
  * spec_philox_uniforms - the verify calls' uniforms, exposed for checking.

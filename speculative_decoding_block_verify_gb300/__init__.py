@@ -16,6 +16,10 @@ Entry points (same names as the C ABI):
 * ``spec_accept_counters``   - per-position acceptance counts (a_p, tokens per step)
 * ``SpecPipeline``           - pick k -> ragged verify -> counters as one CUDA graph
 * ``CostCurve``              - the online verify-cost table adaptive_pick_k reads
+* ``spec_paged_attention``   - a verify block's attention over a paged key-value cache
+* ``spec_cache_append``      - the block's keys and values into their pages
+* ``spec_cache_resize``      - pages reserved before a block and given back after its verify
+* ``spec_cache_fork``        - a stream's pages shared with other streams
 * ``spec_philox_uniforms``   - the verify calls' uniforms (for checking)
 
 Build the library first: ``python -m speculative_decoding_block_verify_gb300.build`` (or
@@ -24,13 +28,15 @@ Build the library first: ``python -m speculative_decoding_block_verify_gb300.bui
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "dspark_markov_bias", "dspark_markov_walk", "spec_verify_tokenwise", "spec_verify_block",
     "spec_verify_tokenwise_reduced", "spec_verify_block_reduced",
     "adaptive_pick_k", "spec_accept_counters", "acceptance_rates", "SpecPipeline", "CostCurve",
     "spec_philox_uniforms", "spec_verify_launch_info",
-    "spec_verify_workspace_bytes", "spec_verify_block_static", "lib", "lib_path", "SpecError",
+    "spec_verify_workspace_bytes", "spec_verify_block_static",
+    "spec_paged_attention", "spec_cache_append", "spec_cache_resize", "spec_cache_fork", "lib", "lib_path", "SpecError",
     "DTYPE_F32", "DTYPE_BF16", "STATUS_NAMES", "DIAG_COLS",
 ]
 
@@ -38,7 +44,8 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 DIAG_COLS = 8
 STATUS_NAMES = {0: "OK", 1: "BAD_TEMPERATURE", 2: "BAD_TOKEN", 3: "BAD_ROW",
-                4: "ZERO_DRAFT_PROB", 5: "BAD_OFFSETS", 6: "TIMEOUT", 7: "NUMERIC"}
+                4: "ZERO_DRAFT_PROB", 5: "BAD_OFFSETS", 6: "TIMEOUT", 7: "NUMERIC",
+                8: "NO_PAGES", 9: "BAD_LENGTH", 10: "BAD_PAGE", 11: "BAD_STREAM"}
 EXPORTED = ["dspark_markov_bias", "dspark_markov_walk", "dspark_markov_walk_workspace_bytes",
             "spec_verify_tokenwise", "spec_verify_block",
             "spec_verify_tokenwise_reduced", "spec_verify_block_reduced",
@@ -48,6 +55,8 @@ EXPORTED = ["dspark_markov_bias", "dspark_markov_walk", "dspark_markov_walk_work
             "spec_pipeline_destroy", "spec_cost_curve_create", "spec_cost_curve_begin",
             "spec_cost_curve_end", "spec_cost_curve_poll", "spec_cost_curve_observe",
             "spec_cost_curve_table", "spec_cost_curve_upload", "spec_cost_curve_destroy",
+            "spec_paged_attention", "spec_paged_attention_workspace_bytes", "spec_cache_append",
+            "spec_cache_resize", "spec_cache_resize_workspace_bytes", "spec_cache_fork",
             "spec_last_error", "spec_version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -143,6 +152,14 @@ def lib():
     L.spec_cost_curve_destroy.restype = None
     L.spec_verify_workspace_bytes.argtypes = [i32, i32]
     L.spec_verify_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_paged_attention.argtypes = [vp, vp]
+    L.spec_paged_attention_workspace_bytes.argtypes = [vp]
+    L.spec_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_cache_append.argtypes = [vp, vp]
+    L.spec_cache_resize.argtypes = [vp, vp]
+    L.spec_cache_resize_workspace_bytes.argtypes = [i32, i32]
+    L.spec_cache_resize_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_cache_fork.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.spec_last_error.restype = ctypes.c_char_p
     L.spec_version.restype = ctypes.c_int32
     for name in ("dspark_markov_bias", "dspark_markov_walk", "spec_verify_tokenwise", "spec_verify_block", "spec_verify_block_static",
@@ -151,7 +168,8 @@ def lib():
                  "spec_accept_counters", "spec_pipeline_create", "spec_pipeline_launch",
                  "spec_pipeline_destroy", "spec_cost_curve_begin", "spec_cost_curve_end",
                  "spec_cost_curve_poll", "spec_cost_curve_observe", "spec_cost_curve_table",
-                 "spec_cost_curve_upload"):
+                 "spec_cost_curve_upload", "spec_paged_attention", "spec_cache_append", "spec_cache_resize",
+                 "spec_cache_fork"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -573,4 +591,194 @@ def spec_philox_uniforms(seed, step, n_streams, n_slots, device="cuda", stream=N
     out = torch.empty((n_streams, n_slots, 2), dtype=torch.float64, device=device)
     _check(lib().spec_philox_uniforms(int(seed) & 0xFFFFFFFFFFFFFFFF, int(step) & 0xFFFFFFFFFFFFFFFF,
                                       n_streams, n_slots, _ptr(out), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# The paged key-value cache.  These calls sit in a decode loop's every layer, so their argument
+# structs are packed in one go (native alignment, as the C compiler lays them out).
+# ---------------------------------------------------------------------------------------------
+_ATTENTION = struct.Struct("@11i f 4P q 5P N")   # spec_attention_args
+_APPEND = struct.Struct("@8i 5P 2q 3P")          # spec_append_args
+_RESIZE = struct.Struct("@5i q 10P N")           # spec_resize_args
+
+
+def _on(t, name, device, dtype, shape):
+    """``t`` is a dense CUDA tensor of this device, dtype and shape."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    return t.data_ptr()
+
+
+def _rows_of(t, name, device, dtype, heads, D):
+    """(pointer, row stride) of [rows, heads, D] with dense rows (a slice of a wider projection)."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [rows, {heads}, {D}], got {list(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1) or (row < heads * D and t.shape[0] > 1):
+        raise ValueError(f"{name} must have dense rows of heads * D elements")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    return t.data_ptr(), max(row, heads * D)
+
+
+def _layer_of(k_pages, v_pages):
+    """(device, dtype code, num_pages, Hkv, page_size, D) of one layer's pool."""
+    if not (k_pages.is_cuda and v_pages.is_cuda):
+        raise TypeError("k_pages and v_pages must be CUDA tensors")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D] of one dtype")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages and v_pages must be contiguous")
+    device = k_pages.get_device()
+    if v_pages.get_device() != device:
+        raise ValueError("v_pages is on another device")
+    return (device, _dtype_code(k_pages)) + tuple(k_pages.shape)
+
+
+def _blocks_of(device, page_table, length, cu_drafts, rows, kmax):
+    """(B, max_pages, pointers of cu_drafts, length, page_table) of packed blocks."""
+    i32 = _torch().int32
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    if cu_drafts is None:
+        cu = 0
+        if rows != B * (kmax + 1):
+            raise ValueError("without cu_drafts there are B * (kmax + 1) rows")
+    else:
+        cu = _on(cu_drafts, "cu_drafts", device, i32, (B + 1,))
+    return (B, max_pages, cu, _on(length, "length", device, i32, (B,)),
+            _on(page_table, "page_table", device, i32, (B, max_pages)))
+
+
+def _raw_stream(stream, device):
+    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kmax, scale, window=0, sinks=0,
+                         out=None, stream=None):
+    """Attention of every stream's block (its drafts and the token before them) over its pages.
+
+    q [rows, Hq, D] (rows may be slices of a wider projection), k_pages and v_pages [num_pages, Hkv,
+    page_size, D] of q's dtype (float32/bf16), page_table [B, max_pages], length [B] (tokens before the
+    block) and cu_drafts [B + 1] int32 (None: kmax drafts each; kmax = 0 is plain decoding).  window > 0
+    keeps the last ``window`` positions of each row and the first ``sinks`` of its stream.  Returns
+    (and reuses) ``out`` with out [rows, Hq, D], status [B], workspace."""
+    torch = _torch()
+    device, code, num_pages, Hkv, page_size, D = _layer_of(k_pages, v_pages)
+    if q.dim() != 3 or q.shape[1] % Hkv != 0:
+        raise ValueError("q must be [rows, Hq, D] with Hq a multiple of Hkv")
+    rows, Hq, _ = q.shape
+    qp, stride = _rows_of(q, "q", device, k_pages.dtype, Hq, D)
+    B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
+    L = lib()
+    sizes = (B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride,
+             k_pages.data_ptr(), v_pages.data_ptr())
+    if out is None:
+        # the first 256 bytes of the workspace start at zero and every call leaves them so
+        need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(*sizes, 0, 0, 0, 0))
+        out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
+               "status": torch.empty(B, dtype=torch.int32, device=q.device),
+               "workspace": torch.zeros(max(int(need), 256), dtype=torch.uint8, device=q.device)}
+    o, ws = out["out"], out["workspace"]
+    args = _ATTENTION.pack(*sizes, _on(o, "out", device, q.dtype, (rows, Hq, D)),
+                           _on(out["status"], "status", device, torch.int32, (B,)), ws.data_ptr(), ws.numel())
+    rc = L.spec_paged_attention(args, _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kmax, out=None, stream=None):
+    """Writes the block's k and v [rows, Hkv, D] (slices of a wider projection may be passed) to their
+    positions in one layer's pages; the other arguments as in spec_paged_attention.  Returns (and
+    reuses) ``out`` with status [B]."""
+    torch = _torch()
+    device, code, num_pages, Hkv, page_size, D = _layer_of(k_pages, v_pages)
+    kp, ks = _rows_of(k, "k", device, k_pages.dtype, Hkv, D)
+    vp, vs = _rows_of(v, "v", device, k_pages.dtype, Hkv, D)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, k.shape[0], kmax)
+    if out is None:
+        out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
+    args = _APPEND.pack(B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, kp, vp, ks, vs,
+                        k_pages.data_ptr(), v_pages.data_ptr(), _on(out["status"], "status", device, torch.int32, (B,)))
+    rc = lib().spec_cache_append(args, _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+def _book_of(page_table, held, length, ref_count):
+    """(device, B, max_pages, num_pages, pointers) of a cache's bookkeeping."""
+    i32 = _torch().int32
+    if page_table.dim() != 2 or ref_count.dim() != 1:
+        raise ValueError("page_table must be [B, max_pages] and ref_count [num_pages]")
+    device = page_table.get_device()
+    B, max_pages = page_table.shape
+    return (device, B, max_pages, ref_count.shape[0], _on(page_table, "page_table", device, i32, (B, max_pages)),
+            _on(held, "held", device, i32, (B,)), _on(length, "length", device, i32, (B,)),
+            _on(ref_count, "ref_count", device, i32, ref_count.shape))
+
+
+def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advance=None, room=None, out=None,
+                      stream=None):
+    """length += advance (n_emitted of a verify call, or negative to roll back), then every stream
+    holds the pages of length + room tokens.  k_pool and v_pool [layers, num_pages, Hkv, page_size,
+    D]; page_table [B, max_pages], held, length [B] and ref_count [num_pages] int32 are updated in
+    place; advance and room [B] int32 or None.  Returns (and reuses) ``out`` with status [B], workspace."""
+    torch = _torch()
+    device, B, max_pages, num_pages, tp, hp, lp, rp = _book_of(page_table, held, length, ref_count)
+    if k_pool.dim() != 5 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.shape[1] != num_pages:
+        raise ValueError("k_pool and v_pool must be [layers, num_pages, Hkv, page_size, D] of one dtype")
+    _dtype_code(k_pool)
+    layers, _, Hkv, page_size, D = k_pool.shape
+    page_bytes = Hkv * page_size * D * k_pool.element_size()
+    kp = _on(k_pool, "k_pool", device, k_pool.dtype, k_pool.shape)
+    vp = _on(v_pool, "v_pool", device, k_pool.dtype, k_pool.shape)
+    ap = 0 if advance is None else _on(advance, "advance", device, torch.int32, (B,))
+    mp = 0 if room is None else _on(room, "room", device, torch.int32, (B,))
+    L = lib()
+    if out is None:
+        need = max(int(L.spec_cache_resize_workspace_bytes(B, num_pages)), 16)
+        out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
+               "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
+    ws = out["workspace"]
+    args = _RESIZE.pack(B, page_size, num_pages, max_pages, layers, page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
+                        _on(out["status"], "status", device, torch.int32, (B,)), ws.data_ptr(), ws.numel())
+    rc = L.spec_cache_resize(args, _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+def spec_cache_fork(src, dst, page_table, held, length, ref_count, page_size, out=None, stream=None):
+    """Stream dst[e] becomes a continuation of stream src[e] (src, dst [n] int32): it gives up its pages
+    and shares those of src's tokens; spec_cache_resize copies a shared page before it is written
+    into.  Returns (and reuses) ``out`` with status [n]."""
+    torch = _torch()
+    device, B, max_pages, num_pages, tp, hp, lp, rp = _book_of(page_table, held, length, ref_count)
+    n = src.numel()
+    sp = _on(src, "src", device, torch.int32, (n,))
+    dp = _on(dst, "dst", device, torch.int32, (n,))
+    if out is None:
+        out = {"status": torch.empty(n, dtype=torch.int32, device=page_table.device)}
+    rc = lib().spec_cache_fork(sp, dp, n, B, page_size, num_pages, max_pages, tp, hp, lp, rp,
+                               _on(out["status"], "status", device, torch.int32, (n,)), _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
     return out

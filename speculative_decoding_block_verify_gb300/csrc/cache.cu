@@ -1,0 +1,563 @@
+// The paged key-value cache around a verify step: spec_cache_append, spec_cache_resize,
+// spec_cache_fork.
+//
+// The page table, the counts and the lengths live on the device and are only changed there, so a
+// decode loop never waits for the host to learn how many tokens were kept.  All of it is integers
+// whose result does not depend on the order in which threads run: reference counts change by
+// atomic additions, and pages are given out by rank (the lowest free pages, in stream order),
+// found by prefix sums.  A page is free when nobody holds it; there is no list to keep in step.
+
+#include <cooperative_groups.h>
+
+#include "blocks.cuh"
+#include "host_util.h"
+
+namespace sv {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------------------
+// One CTA column per stream: the stream's rows are known from two words of cu_drafts, so no row
+// searches for its stream.  A thread moves 16 bytes of K and of V (or one element of each, where a
+// base or a row stride is not a multiple of 16 bytes).  Bound by latency at decode sizes.
+constexpr int kAppendThreads = 256;
+
+template <typename U>   // the unit moved by a thread: uint4, or one element
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_append_args a, int units_per_head) {
+    __shared__ int s_first;
+    __shared__ int s_page[SPEC_MAX_KMAX + 1];
+    __shared__ int s_bad;
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int len = __ldg(a.length + b);
+    if (tid == 0) s_bad = 0;
+    const bool offsets_ok = valid_prefix(a.cu_drafts, a.B, a.kmax, b + 1, &s_first) > b;
+    int status = SPEC_ST_OK, n = 0;
+    int64_t row0 = 0;
+    if (!offsets_ok) {
+        status = SPEC_ST_BAD_OFFSETS;
+    } else {
+        n = block_rows(a.cu_drafts, b, a.kmax);
+        row0 = first_row(a.cu_drafts, b, a.kmax);
+        if (len < 0 || (int64_t)len + n > (int64_t)a.max_pages * a.page_size) status = SPEC_ST_BAD_LENGTH;
+    }
+    const int shift = __ffs(a.page_size) - 1;
+    __syncthreads();
+    if (status == SPEC_ST_OK) {
+        for (int i = tid; i < n; i += kAppendThreads) {
+            int page = __ldg(a.page_table + (int64_t)b * a.max_pages + ((len + i) >> shift));
+            if ((unsigned)page >= (unsigned)a.num_pages) {
+                page = -1;
+                s_bad = 1;
+            }
+            s_page[i] = page;
+        }
+    }
+    __syncthreads();
+    if (status == SPEC_ST_OK && s_bad) status = SPEC_ST_BAD_PAGE;
+    if (blockIdx.y == 0 && tid == 0) a.status[b] = status;
+    if (status == SPEC_ST_BAD_OFFSETS || status == SPEC_ST_BAD_LENGTH) return;
+    const U* k = reinterpret_cast<const U*>(a.k);
+    const U* v = reinterpret_cast<const U*>(a.v);
+    U* kp = reinterpret_cast<U*>(a.k_pages);
+    U* vp = reinterpret_cast<U*>(a.v_pages);
+    const int64_t per = a.D / units_per_head;   // elements of a unit
+    const int64_t kstride = a.k_row_stride / per, vstride = a.v_row_stride / per;
+    const int per_row = a.Hkv * units_per_head;
+    const int total = n * per_row;
+    for (int u = blockIdx.y * kAppendThreads + tid; u < total; u += gridDim.y * kAppendThreads) {
+        const int i = u / per_row, rest = u - i * per_row;
+        const int h = rest / units_per_head, c = rest - h * units_per_head;
+        const int page = s_page[i];
+        if (page < 0) continue;
+        const U x = __ldg(k + (row0 + i) * kstride + rest);
+        const U y = __ldg(v + (row0 + i) * vstride + rest);
+        const int64_t to = (((int64_t)page * a.Hkv + h) * a.page_size + ((len + i) & (a.page_size - 1))) * units_per_head + c;
+        kp[to] = x;
+        vp[to] = y;
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// resize
+// ---------------------------------------------------------------------------------------
+// Workspace: a header {pairs} and per stream the plan of the call, then the free pages in rank order.
+struct ResizePlan {
+    int32_t* header;   // [0] copies asked for
+    int32_t* keep;     // pages of the stream that stay
+    int32_t* want;     // pages it needs (keep, where the call leaves it alone)
+    int32_t* next;     // its new length
+    int32_t* ask;      // the shared page that it wants a copy of, or -1
+    int32_t* need;     // pages it asks the pool for
+    int32_t* begin;    // rank of the first of them
+    int2* pair;        // copies {from, to}; from = -1: none was made
+    int32_t* nth;      // copies asked for before the stream's
+    int32_t* list;     // [num_pages] the free pages, lowest first
+};
+
+__host__ __device__ inline size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+__host__ __device__ inline ResizePlan resize_plan(void* ws, int B) {
+    char* p = reinterpret_cast<char*>(ws);
+    const size_t per = round16((size_t)B * 4);
+    ResizePlan r;
+    r.header = reinterpret_cast<int32_t*>(p);
+    p += 256;
+    r.pair = reinterpret_cast<int2*>(p);
+    p += 2 * per;
+    int32_t** f[] = {&r.keep, &r.want, &r.next, &r.ask, &r.need, &r.begin, &r.nth};
+    for (int i = 0; i < 7; ++i) {
+        *f[i] = reinterpret_cast<int32_t*>(p);
+        p += per;
+    }
+    r.list = reinterpret_cast<int32_t*>(p);
+    return r;
+}
+
+static size_t resize_workspace(int B, int num_pages) {
+    return 256 + 9 * round16((size_t)B * 4) + round16((size_t)num_pages * 4);
+}
+
+__device__ __forceinline__ bool in_pool(int page, int num_pages) { return (unsigned)page < (unsigned)num_pages; }
+
+// What one stream keeps and needs (step 1's decisions), by one warp; every lane returns the same.
+struct StreamPlan {
+    int status, next, keep, want, held, tail;   // tail: the page that holds kept tokens and room, or -1
+};
+__device__ __forceinline__ StreamPlan plan_stream(const spec_resize_args& a, int b, int lane) {
+    StreamPlan s;
+    const int shift = __ffs(a.page_size) - 1;
+    const int len = __ldcg(a.length + b);
+    s.held = __ldcg(a.held + b);
+    const int adv = a.advance != nullptr ? __ldg(a.advance + b) : 0;
+    const int room = a.room != nullptr ? __ldg(a.room + b) : 0;
+    const int64_t n = (int64_t)len + adv;
+    s.tail = -1;
+    if (len < 0 || n < 0 || room < 0 || s.held < 0 || s.held > a.max_pages || n > (int64_t)s.held << shift ||
+        n + room > (int64_t)a.max_pages << shift) {
+        s.status = SPEC_ST_BAD_LENGTH;
+        s.next = len;
+        s.keep = s.want = s.held;
+        return s;
+    }
+    s.next = (int)n;
+    s.want = (int)((n + room + a.page_size - 1) >> shift);
+    const int full = (int)((n + a.page_size - 1) >> shift);
+    const int lim = min(s.want, s.held);
+    const int32_t* row = a.page_table + (int64_t)b * a.max_pages;
+    int first = lim;
+    bool bad = false;
+    for (int j = full + lane; j < s.held; j += 32) {
+        const int p = __ldcg(row + j);
+        if (!in_pool(p, a.num_pages))
+            bad = true;
+        else if (j < lim && __ldcg(a.ref_count + p) > 1)
+            first = min(first, j);
+    }
+    first = warp_min_i(first);
+    if (room > 0 && (n & (a.page_size - 1)) != 0) {
+        s.tail = __ldcg(row + (n >> shift));
+        bad |= !in_pool(s.tail, a.num_pages);
+    }
+    s.keep = first;
+    s.status = SPEC_ST_OK;
+    if (__any_sync(0xffffffffu, bad)) {
+        s.status = SPEC_ST_BAD_PAGE;
+        s.next = len;
+        s.keep = s.want = s.held;
+        s.tail = -1;
+    }
+    return s;
+}
+
+__device__ __forceinline__ void drop_pages(const spec_resize_args& a, int b, int keep, int held, int lane) {
+    int32_t* row = a.page_table + (int64_t)b * a.max_pages;
+    for (int j = keep + lane; j < held; j += 32) {
+        atomicSub(a.ref_count + __ldcg(row + j), 1);
+        row[j] = -1;
+    }
+}
+
+// Without room no page is asked for, no page is replaced, and no decision reads a count: every
+// stream is independent, one warp each.
+constexpr int kTrimThreads = 128;
+__global__ void __launch_bounds__(kTrimThreads) trim_kernel(const spec_resize_args a) {
+    const int lane = threadIdx.x & 31;
+    const int b = blockIdx.x * (kTrimThreads / 32) + (threadIdx.x >> 5);
+    if (b >= a.B) return;
+    const StreamPlan s = plan_stream(a, b, lane);
+    drop_pages(a, b, s.keep, s.held, lane);
+    if (lane == 0) {
+        a.status[b] = s.status;
+        if (s.status == SPEC_ST_OK) {
+            a.length[b] = s.next;
+            a.held[b] = s.keep;
+        }
+    }
+}
+
+// Exclusive prefix sums over the block of one int per thread (returns the block's total).
+template <int kThreads>
+__device__ __forceinline__ int block_scan(int v, int* before, int* scratch /* [kThreads / 32 + 1] */) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int t = lane < kThreads / 32 ? scratch[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += y;
+        }
+        if (lane < kThreads / 32) scratch[lane] = t;
+    }
+    __syncthreads();
+    *before = x - v + (warp ? scratch[warp - 1] : 0);
+    return scratch[kThreads / 32 - 1];
+}
+
+// With room: one cluster, whose barriers separate the steps (a count is read only when every
+// change of the step before it is done).
+constexpr int kResizeThreads = 512;
+constexpr int kResizeCtas = 8;
+constexpr int kScanPer = 16;   // counts that a thread looks at in one pass over the pool
+
+__global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThreads)
+    resize_kernel(const spec_resize_args a) {
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ int scratch[kResizeThreads / 32 + 1];
+    __shared__ int s_count[2][kResizeCtas];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int rank = (int)cluster.block_rank();
+    const int wid = rank * (kResizeThreads / 32) + (tid >> 5);
+    constexpr int kWarps = kResizeCtas * kResizeThreads / 32;
+    const ResizePlan w = resize_plan(a.workspace, a.B);
+
+    for (int b = wid; b < a.B; b += kWarps) {
+        const StreamPlan s = plan_stream(a, b, lane);
+        if (lane == 0) {
+            a.status[b] = s.status;
+            w.keep[b] = s.keep;
+            w.want[b] = s.want;
+            w.next[b] = s.next;
+            w.ask[b] = s.tail;
+        }
+    }
+    cluster.sync();
+    for (int b = wid; b < a.B; b += kWarps) {
+        drop_pages(a, b, __ldcg(w.keep + b), __ldcg(a.held + b), lane);
+    }
+    cluster.sync();
+    // who holds a shared page that it will write into
+    for (int b = rank * kResizeThreads + tid; b < a.B; b += kResizeCtas * kResizeThreads) {
+        const int p = __ldcg(w.ask + b);
+        if (p >= 0 && __ldcg(a.ref_count + p) <= 1) w.ask[b] = -1;
+    }
+    cluster.sync();
+    for (int b = wid; b < a.B; b += kWarps) {
+        const int p = __ldcg(w.ask + b);
+        int copy = 0;
+        if (p >= 0) {
+            int same = 0, lower = 0;
+            for (int o = lane; o < a.B; o += 32) {
+                const bool eq = __ldcg(w.ask + o) == p;
+                same += eq;
+                lower |= eq && o < b;
+            }
+            same = __reduce_add_sync(0xffffffffu, same);
+            lower = __any_sync(0xffffffffu, lower);
+            copy = !(same == __ldcg(a.ref_count + p) && !lower);
+        }
+        if (lane == 0) {
+            w.need[b] = __ldcg(w.want + b) - __ldcg(w.keep + b) + copy;
+            w.nth[b] = copy;
+        }
+    }
+    cluster.sync();
+    // ranks: every CTA runs the prefix sums, the first one writes them down
+    const int per = (a.B + kResizeThreads - 1) / kResizeThreads;
+    int need = 0, copies = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < a.B) {
+            need += __ldcg(w.need + b);
+            copies += __ldcg(w.nth + b);
+        }
+    }
+    int begin, nth;
+    const int total = block_scan<kResizeThreads>(need, &begin, scratch);
+    const int pairs = block_scan<kResizeThreads>(copies, &nth, scratch);
+    cluster.sync();   // every CTA has read w.nth, which becomes a prefix sum below
+    if (rank == 0) {
+        if (tid == 0) w.header[0] = pairs;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < a.B) {
+                const int c = __ldcg(w.nth + b);
+                w.begin[b] = begin;
+                w.nth[b] = c ? nth : -1;
+                begin += __ldcg(w.need + b);
+                nth += c;
+            }
+        }
+    }
+    // the first `total` free pages, by rank
+    int found = 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.ref_count) & 15) == 0;
+    constexpr int kChunk = kResizeCtas * kResizeThreads * kScanPer;
+    int turn = 0;
+    for (int64_t base = 0; base < a.num_pages && found < total; base += kChunk, turn ^= 1) {
+        const int64_t p0 = base + ((int64_t)rank * kResizeThreads + tid) * kScanPer;
+        unsigned mask = 0;
+        if (vec && p0 + kScanPer <= a.num_pages) {
+            int4 r[kScanPer / 4];
+#pragma unroll
+            for (int i = 0; i < kScanPer / 4; ++i) r[i] = __ldcg(reinterpret_cast<const int4*>(a.ref_count + p0) + i);
+#pragma unroll
+            for (int i = 0; i < kScanPer / 4; ++i)
+                mask |= ((r[i].x == 0) | (r[i].y == 0) << 1 | (r[i].z == 0) << 2 | (r[i].w == 0) << 3) << (4 * i);
+        } else {
+            for (int i = 0; i < kScanPer; ++i)
+                if (p0 + i < a.num_pages && __ldcg(a.ref_count + p0 + i) == 0) mask |= 1u << i;
+        }
+        int before;
+        const int mine = block_scan<kResizeThreads>(__popc(mask), &before, scratch);
+        if (tid < kResizeCtas) *cluster.map_shared_rank(&s_count[turn][rank], tid) = mine;
+        cluster.sync();
+        int at = found + before;
+        for (int c = 0; c < kResizeCtas; ++c) {
+            const int n = s_count[turn][c];
+            if (c < rank) at += n;
+            found += n;
+        }
+        while (mask != 0 && at < total) {
+            const int i = __ffs(mask) - 1;
+            mask &= mask - 1;
+            w.list[at++] = (int)(p0 + i);
+        }
+    }
+    cluster.sync();
+    for (int b = wid; b < a.B; b += kWarps) {
+        const int nb = __ldcg(w.need + b), rank0 = __ldcg(w.begin + b), pr = __ldcg(w.nth + b);
+        const int keep = __ldcg(w.keep + b), want = __ldcg(w.want + b), next = __ldcg(w.next + b);
+        const bool fits = nb == 0 || (int64_t)rank0 + nb <= found;
+        int32_t* row = a.page_table + (int64_t)b * a.max_pages;
+        if (fits) {
+            const int grow0 = rank0 + (pr >= 0);
+            for (int j = keep + lane; j < want; j += 32) {
+                const int p = __ldcg(w.list + grow0 + j - keep);
+                row[j] = p;
+                a.ref_count[p] = 1;
+            }
+        }
+        if (lane == 0) {
+            if (pr >= 0) {
+                int2 move = make_int2(-1, -1);
+                if (fits) {
+                    move = make_int2(__ldcg(w.ask + b), __ldcg(w.list + rank0));
+                    row[next / a.page_size] = move.y;
+                    a.ref_count[move.y] = 1;
+                    atomicSub(a.ref_count + move.x, 1);
+                }
+                w.pair[pr] = move;
+            }
+            if (a.status[b] == SPEC_ST_OK) {
+                a.length[b] = next;
+                a.held[b] = fits ? want : keep;
+                if (!fits) a.status[b] = SPEC_ST_NO_PAGES;
+            }
+        }
+    }
+}
+
+// The copies that resize_kernel asked for: a warp moves up to 4 KB of one page of one layer of K
+// or V, eight 16-byte loads of a lane in flight.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyPart = 4096;
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const spec_resize_args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ResizePlan w = resize_plan(a.workspace, a.B);
+    const int pairs = __ldcg(w.header);
+    if (pairs == 0) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t parts = (a.page_bytes + kCopyPart - 1) / kCopyPart;
+    const int64_t per_pair = parts * a.layers * 2;
+    const int64_t total = per_pair * pairs;
+    for (int64_t u = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < total;
+         u += (int64_t)gridDim.x * (kCopyThreads / 32)) {
+        const int64_t pr = u / per_pair, rest = u - pr * per_pair;
+        const int2 move = __ldcg(w.pair + pr);
+        if (move.x < 0) continue;
+        const int64_t part = rest % parts, lk = rest / parts;
+        char* pool = reinterpret_cast<char*>((lk & 1) ? a.v_pool : a.k_pool) + (lk >> 1) * (int64_t)a.num_pages * a.page_bytes;
+        const int64_t off = part * kCopyPart;
+        const int chunks = (int)((min((int64_t)kCopyPart, a.page_bytes - off)) >> 4);
+        const uint4* from = reinterpret_cast<const uint4*>(pool + move.x * a.page_bytes + off);
+        uint4* to = reinterpret_cast<uint4*>(pool + move.y * a.page_bytes + off);
+        uint4 r[kCopyPart / 512];
+#pragma unroll
+        for (int i = 0; i < kCopyPart / 512; ++i)
+            if (lane + 32 * i < chunks) r[i] = __ldcs(from + lane + 32 * i);
+#pragma unroll
+        for (int i = 0; i < kCopyPart / 512; ++i)
+            if (lane + 32 * i < chunks) to[lane + 32 * i] = r[i];
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------------------
+// One CTA per pair.  A destination is nobody's source, so the rows that are read are not written.
+constexpr int kForkThreads = 256;
+__global__ void __launch_bounds__(kForkThreads)
+    fork_kernel(const int32_t* src, const int32_t* dst, int n, int B, int page_size, int num_pages, int max_pages,
+                int32_t* page_table, int32_t* held, int32_t* length, int32_t* ref_count, int32_t* status) {
+    const int e = blockIdx.x, tid = threadIdx.x;
+    const int s = __ldg(src + e), d = __ldg(dst + e);
+    bool bad = (unsigned)s >= (unsigned)B || (unsigned)d >= (unsigned)B;
+    for (int o = tid; o < n; o += kForkThreads) bad |= __ldg(src + o) == d || (o < e && __ldg(dst + o) == d);
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) status[e] = SPEC_ST_BAD_STREAM;
+        return;
+    }
+    const int shift = __ffs(page_size) - 1;
+    const int len = __ldcg(length + s), hs = __ldcg(held + s), hd = __ldcg(held + d);
+    if (len < 0 || hs < 0 || hs > max_pages || hd < 0 || hd > max_pages || len > (int64_t)hs << shift) {
+        if (tid == 0) status[e] = SPEC_ST_BAD_LENGTH;
+        return;
+    }
+    const int pages = (int)(((int64_t)len + page_size - 1) >> shift);
+    const int32_t* from = page_table + (int64_t)s * max_pages;
+    int32_t* to = page_table + (int64_t)d * max_pages;
+    bad = false;
+    for (int j = tid; j < max(pages, hd); j += kForkThreads) {
+        if (j < pages) bad |= !in_pool(__ldcg(from + j), num_pages);
+        if (j < hd) bad |= !in_pool(__ldcg(to + j), num_pages);
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) status[e] = SPEC_ST_BAD_PAGE;
+        return;
+    }
+    for (int j = tid; j < max(pages, hd); j += kForkThreads) {
+        const int give = j < hd ? __ldcg(to + j) : -1, take = j < pages ? __ldcg(from + j) : -1;
+        if (give == take) continue;
+        if (take >= 0) atomicAdd(ref_count + take, 1);
+        if (give >= 0) atomicSub(ref_count + give, 1);
+        to[j] = take;
+    }
+    if (tid == 0) {
+        length[d] = len;
+        held[d] = pages;
+        status[e] = SPEC_ST_OK;
+    }
+}
+
+static bool page_ok(int page_size) { return page_size >= 8 && page_size <= SPEC_MAX_PAGE && (page_size & (page_size - 1)) == 0; }
+static bool table_ok(int max_pages, int page_size) { return (int64_t)max_pages * page_size <= INT32_MAX; }
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
+    clear_error();
+    if (a == nullptr) return set_error(SPEC_ERR_ARG, "spec_cache_append: args is NULL");
+    if (!valid_dtype(a->dtype)) return set_error(SPEC_ERR_DTYPE, "spec_cache_append: dtype %d", a->dtype);
+    if (a->B < 0 || a->B > SPEC_MAX_STREAMS || a->kmax < 0 || a->kmax > SPEC_MAX_KMAX)
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_append: B = %d, kmax = %d", a->B, a->kmax);
+    if (a->Hkv < 1 || a->Hkv > 1024 || a->D < 8 || a->D > SPEC_MAX_HEAD || a->D % 8 != 0)
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_append: Hkv = %d, D = %d", a->Hkv, a->D);
+    if (!page_ok(a->page_size) || a->num_pages < 1 || a->max_pages < 1 || !table_ok(a->max_pages, a->page_size))
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_append: page_size = %d, num_pages = %d, max_pages = %d", a->page_size,
+                         a->num_pages, a->max_pages);
+    if (a->k_row_stride < (int64_t)a->Hkv * a->D || a->v_row_stride < (int64_t)a->Hkv * a->D)
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_append: a row stride is below Hkv * D");
+    if (a->B == 0) return SPEC_OK;
+    if (a->length == nullptr || a->page_table == nullptr || a->k == nullptr || a->v == nullptr || a->k_pages == nullptr ||
+        a->v_pages == nullptr || a->status == nullptr)
+        return set_error(SPEC_ERR_ARG, "spec_cache_append: a required pointer is NULL");
+    if (((uintptr_t)a->k_pages | (uintptr_t)a->v_pages) & 15)
+        return set_error(SPEC_ERR_ARG, "spec_cache_append: the pool is not 16-byte aligned");
+    const int es = a->dtype == SPEC_DTYPE_F32 ? 4 : 2;
+    const bool vec = (((uintptr_t)a->k | (uintptr_t)a->v | (uintptr_t)(a->k_row_stride * es) | (uintptr_t)(a->v_row_stride * es)) & 15) == 0;
+    const int upb = vec ? a->D * es / 16 : a->D;
+    const int64_t units = (int64_t)(a->kmax + 1) * a->Hkv * upb;
+    const int64_t want = (units + 2 * kAppendThreads - 1) / (2 * kAppendThreads);   // two units a thread
+    const dim3 grid((unsigned)a->B, (unsigned)(want < 1 ? 1 : want > 64 ? 64 : want));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (vec)
+        append_kernel<uint4><<<grid, kAppendThreads, 0, s>>>(*a, upb);
+    else if (es == 2)
+        append_kernel<unsigned short><<<grid, kAppendThreads, 0, s>>>(*a, upb);
+    else
+        append_kernel<float><<<grid, kAppendThreads, 0, s>>>(*a, upb);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_append");
+}
+
+extern "C" size_t spec_cache_resize_workspace_bytes(int32_t B, int32_t num_pages) {
+    if (B <= 0 || B > SPEC_MAX_STREAMS || num_pages < 1) return 0;
+    return resize_workspace(B, num_pages);
+}
+
+extern "C" int spec_cache_resize(const spec_resize_args* a, void* stream) {
+    clear_error();
+    if (a == nullptr) return set_error(SPEC_ERR_ARG, "spec_cache_resize: args is NULL");
+    if (a->B < 0 || a->B > SPEC_MAX_STREAMS) return set_error(SPEC_ERR_SHAPE, "spec_cache_resize: B = %d", a->B);
+    if (!page_ok(a->page_size) || a->num_pages < 1 || a->max_pages < 1 || !table_ok(a->max_pages, a->page_size))
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_resize: page_size = %d, num_pages = %d, max_pages = %d", a->page_size,
+                         a->num_pages, a->max_pages);
+    if (a->layers < 1 || a->page_bytes < 16 || a->page_bytes % 16 != 0)
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_resize: layers = %d, page_bytes = %lld", a->layers, (long long)a->page_bytes);
+    if (a->B == 0) return SPEC_OK;
+    if (a->page_table == nullptr || a->held == nullptr || a->length == nullptr || a->ref_count == nullptr ||
+        a->k_pool == nullptr || a->v_pool == nullptr || a->status == nullptr)
+        return set_error(SPEC_ERR_ARG, "spec_cache_resize: a required pointer is NULL");
+    if (((uintptr_t)a->k_pool | (uintptr_t)a->v_pool) & 15)
+        return set_error(SPEC_ERR_ARG, "spec_cache_resize: the pool is not 16-byte aligned");
+    if (a->workspace == nullptr || ((uintptr_t)a->workspace & 15) || a->workspace_bytes < resize_workspace(a->B, a->num_pages))
+        return set_error(SPEC_ERR_WORKSPACE, "spec_cache_resize: workspace needs %zu bytes, 16-byte aligned",
+                         resize_workspace(a->B, a->num_pages));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->room == nullptr) {
+        trim_kernel<<<(a->B + kTrimThreads / 32 - 1) / (kTrimThreads / 32), kTrimThreads, 0, s>>>(*a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_resize");
+    }
+    resize_kernel<<<kResizeCtas, kResizeThreads, 0, s>>>(*a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
+    // as many CTAs as the largest number of copies (one per stream) can keep busy, two per SM at most
+    const int64_t units = (int64_t)a->B * a->layers * 2 * ((a->page_bytes + kCopyPart - 1) / kCopyPart);
+    const int64_t ctas = (units + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    copy_pages_kernel<<<(unsigned)(ctas < 608 ? ctas : 608), kCopyThreads, 0, s>>>(*a);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_resize");
+}
+
+extern "C" int spec_cache_fork(const int32_t* src, const int32_t* dst, int32_t n, int32_t B, int32_t page_size,
+                               int32_t num_pages, int32_t max_pages, int32_t* page_table, int32_t* held, int32_t* length,
+                               int32_t* ref_count, int32_t* status, void* stream) {
+    clear_error();
+    if (n < 0 || n > SPEC_MAX_STREAMS || B < 0 || B > SPEC_MAX_STREAMS)
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_fork: n = %d, B = %d", n, B);
+    if (!page_ok(page_size) || num_pages < 1 || max_pages < 1 || !table_ok(max_pages, page_size))
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_fork: page_size = %d, num_pages = %d, max_pages = %d", page_size,
+                         num_pages, max_pages);
+    if (n == 0) return SPEC_OK;
+    if (src == nullptr || dst == nullptr || page_table == nullptr || held == nullptr || length == nullptr ||
+        ref_count == nullptr || status == nullptr)
+        return set_error(SPEC_ERR_ARG, "spec_cache_fork: a required pointer is NULL");
+    fork_kernel<<<n, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(src, dst, n, B, page_size, num_pages, max_pages,
+                                                                          page_table, held, length, ref_count, status);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_fork");
+}
