@@ -468,7 +468,7 @@ void spec_cost_curve_destroy(void* curve);
  * positions length[b] .. length[b] + N_b must be in the cache (spec_cache_append).  Pages that hold no
  * visible position are not read, and their table entries may be -1.
  * q [rows, Hq, D] with q_row_stride elements from row to row (a slice of a wider projection),
- * out [rows, Hq, D] dense, both in the cache's dtype.  status [B]: SPEC_ST_OK, BAD_OFFSETS (rows not
+ * out [rows, Hq, D] dense, both in the cache's dtype; q_rows is their number of rows.  status [B]: SPEC_ST_OK, BAD_OFFSETS (rows not
  * written), BAD_LENGTH (length < 0 or the block ends past max_pages * page_size: rows are NaN),
  * BAD_PAGE (entries outside [0, num_pages) at visible positions, whose keys and values read as
  * zeros), TIMEOUT (every stream's rows undefined).
@@ -480,7 +480,7 @@ void spec_cost_curve_destroy(void* curve);
  * zero-filled once before its first use (a call leaves them so); calls that share it must be ordered.
  * Errors: SPEC_ERR_ARG (NULL pointer, a pool that is not 16-byte aligned, scale not finite),
  * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of Hkv,
- * q_row_stride < Hq * D, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
+ * q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
  * SPEC_ERR_CUDA.  B == 0 launches nothing.
  */
 typedef struct {
@@ -495,6 +495,7 @@ typedef struct {
     const int32_t* page_table;   /* [B, max_pages] */
     const void* q;               /* [rows, Hq, D] */
     int64_t q_row_stride;        /* elements */
+    int64_t q_rows;              /* rows of q and out; a block beyond them is BAD_OFFSETS */
     const void* k_pages;         /* [num_pages, Hkv, page_size, D] */
     const void* v_pages;
     void* out;                   /* [rows, Hq, D] */
@@ -504,8 +505,8 @@ typedef struct {
 } spec_attention_args;
 
 int spec_paged_attention(const spec_attention_args* args, void* stream);
-/* Bytes of workspace the call needs (0 for B = 0 and for invalid sizes).  Reads the sizes, the dtype
- * and the alignment of q; the size also covers every call with smaller B, kmax and max_pages. */
+/* Bytes of workspace the call needs (0 for B = 0 and for invalid sizes).  Reads the sizes, the dtype,
+ * the scale, and q's address and stride (rows that are not 16-byte aligned take another kernel). */
 size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
 
 /*
@@ -527,7 +528,8 @@ typedef struct {
     const int32_t* page_table;   /* [B, max_pages] */
     const void* k;               /* [rows, Hkv, D] */
     const void* v;
-    int64_t k_row_stride, v_row_stride;
+    int64_t k_row_stride, v_row_stride;   /* elements */
+    int64_t rows;                /* rows of k and v; a block beyond them is BAD_OFFSETS */
     void* k_pages;               /* [num_pages, Hkv, page_size, D] */
     void* v_pages;
     int32_t* status;             /* [B] */

@@ -598,8 +598,8 @@ def spec_philox_uniforms(seed, step, n_streams, n_slots, device="cuda", stream=N
 # The paged key-value cache.  These calls sit in a decode loop's every layer, so their argument
 # structs are packed in one go (native alignment, as the C compiler lays them out).
 # ---------------------------------------------------------------------------------------------
-_ATTENTION = struct.Struct("@11i f 4P q 5P N")   # spec_attention_args
-_APPEND = struct.Struct("@8i 5P 2q 3P")          # spec_append_args
+_ATTENTION = struct.Struct("@11i f 4P 2q 5P N")  # spec_attention_args
+_APPEND = struct.Struct("@8i 5P 3q 3P")          # spec_append_args
 _RESIZE = struct.Struct("@5i q 10P N")           # spec_resize_args
 
 
@@ -686,7 +686,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     L = lib()
     sizes = (B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride,
-             k_pages.data_ptr(), v_pages.data_ptr())
+             rows, k_pages.data_ptr(), v_pages.data_ptr())
     if out is None:
         # the first 256 bytes of the workspace start at zero and every call leaves them so
         need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(*sizes, 0, 0, 0, 0))
@@ -716,7 +716,7 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
     if out is None:
         out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
     args = _APPEND.pack(B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, kp, vp, ks, vs,
-                        k_pages.data_ptr(), v_pages.data_ptr(), _on(out["status"], "status", device, torch.int32, (B,)))
+                        k.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _on(out["status"], "status", device, torch.int32, (B,)))
     rc = lib().spec_cache_append(args, _raw_stream(stream, device))
     if rc != 0:
         _check(rc)

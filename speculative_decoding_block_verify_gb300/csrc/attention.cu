@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     __shared__ int s_int, s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = p.a.D;
-    const int valid = valid_prefix(p.a.cu_drafts, p.a.B, p.a.kmax, p.a.B, &s_int);
+    const int valid = valid_prefix(p.a.cu_drafts, p.a.B, p.a.kmax, p.a.q_rows, p.a.B, &s_int);
     const int id = blockIdx.y * gridDim.x + blockIdx.x, ids = gridDim.x * gridDim.y;
     int first_status = SPEC_ST_OK;
     for (int b = id; b < p.a.B; b += ids) {
@@ -379,13 +379,12 @@ static int sm_count(int* sms) {
 
 constexpr int kMaxCtas = 512;   // CTAs of the attention grid that the workspace has room for
 
-static bool tensor_path(const spec_attention_args* a) { return false; }
-
 // Rows of a group and CTAs of the grid.
 static void cut(const spec_attention_args* a, int sms, int* rows, int* ctas) {
     const int64_t need = (int64_t)(a->kmax + 1) * (a->Hq / a->Hkv);
-    *rows = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-    int64_t n = 2 * (int64_t)sms;
+    const bool tensor = tensor_path(a);
+    *rows = tensor ? tensor_rows(a) : need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
+    int64_t n = (tensor ? tensor_ctas_per_sm(a) : 2) * (int64_t)sms;
     // no more CTAs than the longest possible contexts have tiles
     const int64_t groups = (need + *rows - 1) / *rows;
     const int64_t tiles = groups * a->B * a->Hkv * (((int64_t)a->max_pages * a->page_size + kTile - 1) / kTile);
@@ -489,6 +488,8 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     if (rc != SPEC_OK) return rc;
     if (a->q_row_stride < (int64_t)a->Hq * a->D)
         return set_error(SPEC_ERR_SHAPE, "spec_paged_attention: q_row_stride is below Hq * D");
+    if (a->q_rows < 0 || (a->cu_drafts == nullptr && a->q_rows < (int64_t)a->B * (a->kmax + 1)))
+        return set_error(SPEC_ERR_SHAPE, "spec_paged_attention: q_rows = %lld", (long long)a->q_rows);
     if (a->B == 0) return SPEC_OK;
     if (a->length == nullptr || a->page_table == nullptr || a->q == nullptr || a->k_pages == nullptr ||
         a->v_pages == nullptr || a->out == nullptr || a->status == nullptr)
@@ -509,10 +510,14 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     p.page_shift = 0;
     while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
     p.scale_log2 = (float)((double)a->scale * kLog2e);
+    const bool tensor = tensor_path(a);
+    if (tensor) p.scale_log2 = std::fabs(p.scale_log2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int es = a->dtype == SPEC_DTYPE_F32 ? 4 : 2;
     const bool q_vec = (((uintptr_t)a->q | (uintptr_t)(a->q_row_stride * es)) & (4 * es - 1)) == 0;
-    cudaError_t e = a->dtype == SPEC_DTYPE_F32 ? launch_float_r<float>(p, s, q_vec) : launch_float_r<unsigned short>(p, s, q_vec);
+    cudaError_t e = tensor                         ? launch_attention_tc(p, s)
+                    : a->dtype == SPEC_DTYPE_F32 ? launch_float_r<float>(p, s, q_vec)
+                                                 : launch_float_r<unsigned short>(p, s, q_vec);
     if (e != cudaSuccess) return set_cuda_error(e, "spec_paged_attention");
     e = a->dtype == SPEC_DTYPE_F32 ? launch_join<float>(p, s) : launch_join<unsigned short>(p, s);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_paged_attention (join)");

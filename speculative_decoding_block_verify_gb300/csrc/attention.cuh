@@ -14,7 +14,6 @@
 namespace sv {
 
 constexpr int kTile = 64;          // positions of a tile
-constexpr int kMaxGroups = 4096;   // row groups of a block (checked on the host)
 
 struct AttnParams {
     spec_attention_args a;
@@ -85,7 +84,7 @@ template <int kThreads>
 __device__ __forceinline__ void find_start(const AttnParams& p, int cta, Start* s /* shared */,
                                            int64_t* scratch /* shared [kThreads / 32] */, int* iscratch /* shared */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int valid = valid_prefix(p.a.cu_drafts, p.a.B, p.a.kmax, p.a.B, iscratch);
+    const int valid = valid_prefix(p.a.cu_drafts, p.a.B, p.a.kmax, p.a.q_rows, p.a.B, iscratch);
     const int per = (valid + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, valid), b1 = min(b0 + per, valid);
     int64_t mine = 0;
@@ -198,6 +197,11 @@ __device__ __forceinline__ bool visible(const AttnParams& p, int at, int j) {
     return j <= at && (p.a.window <= 0 || j > at - p.a.window || j < p.a.sinks);
 }
 
-cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s, bool* unavailable);
+// The tensor-core kernel (attention_tc.cu): whether it takes the call, the rows of its groups, the CTAs of an
+// SM, the launch.
+bool tensor_path(const spec_attention_args* a);
+int tensor_rows(const spec_attention_args* a);
+int tensor_ctas_per_sm(const spec_attention_args* a);
+cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s);
 
 }  // namespace sv

@@ -5,16 +5,16 @@
 
 namespace sv {
 
-// Streams [0, valid_prefix) have defined rows: cu[0] = 0 and every count up to theirs lies in
-// [0, kmax].  Every thread of the block calls this; `scratch` is one shared int.
-__device__ __forceinline__ int valid_prefix(const int32_t* cu, int B, int kmax, int upto, int* scratch) {
+// Streams [0, valid_prefix) have defined rows: cu[0] = 0, every count up to theirs lies in [0,
+// kmax], and their rows are among the `rows` that the caller passed.  Every thread of the block calls this; `scratch` is one shared int.
+__device__ __forceinline__ int valid_prefix(const int32_t* cu, int B, int kmax, int64_t rows, int upto, int* scratch) {
     if (cu == nullptr) return B;
     if (threadIdx.x == 0) *scratch = B;
     __syncthreads();
     int bad = B;
     for (int b = threadIdx.x; b < upto; b += blockDim.x) {
         const int c0 = __ldg(cu + b), n = __ldg(cu + b + 1) - c0;
-        if (n < 0 || n > kmax || (b == 0 && c0 != 0)) {
+        if (n < 0 || n > kmax || (b == 0 && c0 != 0) || (int64_t)c0 + n + b + 1 > rows) {
             bad = b;
             break;
         }

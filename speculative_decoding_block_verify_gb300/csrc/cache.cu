@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
     const int b = blockIdx.x, tid = threadIdx.x;
     const int len = __ldg(a.length + b);
     if (tid == 0) s_bad = 0;
-    const bool offsets_ok = valid_prefix(a.cu_drafts, a.B, a.kmax, b + 1, &s_first) > b;
+    const bool offsets_ok = valid_prefix(a.cu_drafts, a.B, a.kmax, a.rows, b + 1, &s_first) > b;
     int status = SPEC_ST_OK, n = 0;
     int64_t row0 = 0;
     if (!offsets_ok) {
@@ -480,6 +480,8 @@ extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
                          a->num_pages, a->max_pages);
     if (a->k_row_stride < (int64_t)a->Hkv * a->D || a->v_row_stride < (int64_t)a->Hkv * a->D)
         return set_error(SPEC_ERR_SHAPE, "spec_cache_append: a row stride is below Hkv * D");
+    if (a->rows < 0 || (a->cu_drafts == nullptr && a->rows < (int64_t)a->B * (a->kmax + 1)))
+        return set_error(SPEC_ERR_SHAPE, "spec_cache_append: rows = %lld", (long long)a->rows);
     if (a->B == 0) return SPEC_OK;
     if (a->length == nullptr || a->page_table == nullptr || a->k == nullptr || a->v == nullptr || a->k_pages == nullptr ||
         a->v_pages == nullptr || a->status == nullptr)

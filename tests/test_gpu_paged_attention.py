@@ -380,5 +380,5 @@ def test_c_entry_errors():
     L = sv.lib()
     assert L.spec_paged_attention(None, None) == -1 and L.spec_cache_append(None, None) == -1
     assert L.spec_paged_attention_workspace_bytes(None) == 0
-    z = (ctypes.c_char * 136)()
+    z = (ctypes.c_char * 144)()
     assert L.spec_paged_attention(z, None) == -3   # all sizes zero
