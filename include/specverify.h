@@ -94,6 +94,7 @@ extern "C" {
 #define SPEC_MAX_STREAMS 65535    /* streams of a cache call */
 #define SPEC_MAX_HEAD 256         /* elements of an attention head */
 #define SPEC_MAX_PAGE 256         /* tokens of a page */
+#define SPEC_ATTENTION_ZERO_BYTES 16384   /* of spec_paged_attention's workspace */
 
 /* columns of the optional diag output (one row per target row) */
 #define SPEC_DIAG_COLS 8
@@ -476,9 +477,10 @@ void spec_cost_curve_destroy(void* curve);
  * they meet the values, and the same rounded weights are summed.  A value that is not finite at a
  * position that one row of a block sees may reach the block's earlier rows; one that no row sees
  * reaches none.  The result does not depend on the call before it, and is the same from run to run.
- * workspace: spec_paged_attention_workspace_bytes(args) bytes, 16-byte aligned, its first 256 bytes
- * zero-filled once before its first use (a call leaves them so); calls that share it must be ordered.
- * Errors: SPEC_ERR_ARG (NULL pointer, a pool that is not 16-byte aligned, scale not finite),
+ * workspace: spec_paged_attention_workspace_bytes(args) bytes, 16-byte aligned, its first
+ * SPEC_ATTENTION_ZERO_BYTES zero-filled once before its first use (a call leaves them so, except one
+ * that reports TIMEOUT); calls that share it must be ordered.
+ * Errors: SPEC_ERR_ARG (NULL pointer, a pool or out that is not 16-byte aligned, scale not finite),
  * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of Hkv,
  * q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
  * SPEC_ERR_CUDA.  B == 0 launches nothing.

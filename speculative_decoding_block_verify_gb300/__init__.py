@@ -688,11 +688,11 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     sizes = (B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride,
              rows, k_pages.data_ptr(), v_pages.data_ptr())
     if out is None:
-        # the first 256 bytes of the workspace start at zero and every call leaves them so
+        # the workspace starts at zero where the calls count arrivals, and every call leaves it so
         need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(*sizes, 0, 0, 0, 0))
         out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
                "status": torch.empty(B, dtype=torch.int32, device=q.device),
-               "workspace": torch.zeros(max(int(need), 256), dtype=torch.uint8, device=q.device)}
+               "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
     o, ws = out["out"], out["workspace"]
     args = _ATTENTION.pack(*sizes, _on(o, "out", device, q.dtype, (rows, Hq, D)),
                            _on(out["status"], "status", device, torch.int32, (B,)), ws.data_ptr(), ws.numel())

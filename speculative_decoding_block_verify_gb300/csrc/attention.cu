@@ -1,4 +1,4 @@
-// spec_paged_attention: the entry point, the kernel on the float pipes and the join.
+// spec_paged_attention: the entry point, and the kernel on the float pipes.
 //
 //   out[row] = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = scale log2(e) q . k_j,  m = max_j s_j
 //
@@ -29,9 +29,6 @@ template <>
 __device__ __forceinline__ float to_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float to_float<unsigned short>(unsigned short x) { return __uint_as_float((uint32_t)x << 16); }
-
-__device__ __forceinline__ void put(float* o, float x) { *o = x; }
-__device__ __forceinline__ void put(unsigned short* o, float x) { *o = __bfloat16_as_ushort(__float2bfloat16(x)); }
 
 static size_t float_smem(int rows, int D) {
     return sizeof(float) * ((size_t)rows * (D + 4) + 2 * (size_t)kTile * (D + 4) + (size_t)rows * (kTile + 4));
@@ -69,9 +66,9 @@ __global__ void __launch_bounds__(kFloatThreads) attention_float_kernel(const At
     float* ps = vs + kTile * pitch;
     constexpr int ppitch = kTile + 4;
     const int cta = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     find_start<kFloatThreads>(p, cta, &s_start, s_scan, &s_int);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) p.desc[cta] = make_int4(0, 0, 0, 0);
+    if (tid < 32) write_status<T>(p, cta, s_start.valid);
     Walk w;
     if (!w.start(p, s_start)) return;
     const T* q = reinterpret_cast<const T*>(p.a.q);
@@ -200,8 +197,7 @@ __global__ void __launch_bounds__(kFloatThreads) attention_float_kernel(const At
             }
         }
         const bool whole = w.whole();
-        const int slot = w.slot(cta);
-        if (w.begins_part() && tid == 0) p.desc[cta] = make_int4(w.b, w.h, w.g, w.parts(cta, s_start.span));
+        const int64_t slot = w.slot(cta);
 #pragma unroll
         for (int a = 0; a < RM; ++a) {
             const int r = tr + a * TR;
@@ -213,146 +209,19 @@ __global__ void __launch_bounds__(kFloatThreads) attention_float_kernel(const At
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     const int c = (tk + d * TK) * 4;
-                    if (c < D) {
-                        put(to + c, o[a][d].x * inv);
-                        put(to + c + 1, o[a][d].y * inv);
-                        put(to + c + 2, o[a][d].z * inv);
-                        put(to + c + 3, o[a][d].w * inv);
-                    }
+                    if (c < D) put4(to + c, make_float4(o[a][d].x * inv, o[a][d].y * inv, o[a][d].z * inv, o[a][d].w * inv));
                 }
             } else {
-                const int64_t at_row = (int64_t)slot * p.rows + r;
-                if (tk == 0) p.ml[at_row] = make_float2(m[a], l[a]);
+                if (tk == 0) __stcg(p.ml + slot * p.rows + r, make_float2(m[a], l[a]));
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     const int c = (tk + d * TK) * 4;
-                    if (c < D) *reinterpret_cast<float4*>(p.part + at_row * D + c) = o[a][d];
+                    if (c < D) __stcg(p.part + (slot * nd4 + c / 4) * p.rows + r, o[a][d]);
                 }
             }
         }
+        if (!whole) join_parts<T, kFloatThreads, 1>(p, w, cta, s_start.span, tid, &s_int);
     } while (w.next(p));
-}
-
-// ---------------------------------------------------------------------------------------
-// The join: parts of an item that lies across CTAs, and every stream's status.
-// ---------------------------------------------------------------------------------------
-// CTA (c, y) joins every kJoinSplit-th group of eight rows of the item that CTA c of the attention grid began and
-// left to others, a warp per row.  Before that grid is done it looks through the page entries of its share of
-// the streams (they are inputs).
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinSplit = 4;
-
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
-    __shared__ int s_int, s_bad;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int D = p.a.D;
-    const int valid = valid_prefix(p.a.cu_drafts, p.a.B, p.a.kmax, p.a.q_rows, p.a.B, &s_int);
-    const int id = blockIdx.y * gridDim.x + blockIdx.x, ids = gridDim.x * gridDim.y;
-    int first_status = SPEC_ST_OK;
-    for (int b = id; b < p.a.B; b += ids) {
-        int st = SPEC_ST_OK;
-        if (b >= valid) {
-            st = SPEC_ST_BAD_OFFSETS;
-        } else {
-            const int len = __ldg(p.a.length + b), n = block_rows(p.a.cu_drafts, b, p.a.kmax);
-            if (!length_ok(p, len, n)) {
-                st = SPEC_ST_BAD_LENGTH;
-            } else {
-                // visible to any row: [0, sink) and [low, len + n)
-                const int low = p.a.window > 0 ? max(0, len + 1 - p.a.window) : 0;
-                const int sink = min(p.a.sinks, low);
-                const int sp = (sink + p.a.page_size - 1) >> p.page_shift, lp = low >> p.page_shift;
-                const int hp = (len + n + p.a.page_size - 1) >> p.page_shift;
-                bool bad = false;
-                for (int j = tid; j < hp; j += kJoinThreads)
-                    if (j < sp || j >= lp)
-                        bad |= (unsigned)__ldg(p.a.page_table + (int64_t)b * p.a.max_pages + j) >= (unsigned)p.a.num_pages;
-                if (tid == 0) s_bad = 0;
-                __syncthreads();
-                if (bad) s_bad = 1;
-                __syncthreads();
-                if (s_bad) st = SPEC_ST_BAD_PAGE;
-            }
-        }
-        if (b == id) first_status = st;
-        if (b != id && tid == 0) p.a.status[b] = st;   // many streams: a timeout is added below
-        __syncthreads();
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const bool timeout = __ldcg(p.header) != 0;
-    for (int b = id; b < p.a.B; b += ids) {
-        if (tid == 0) {
-            if (b == id) p.a.status[b] = first_status;
-            if (timeout && p.a.status[b] == SPEC_ST_OK) p.a.status[b] = SPEC_ST_TIMEOUT;
-        }
-        if (b < valid) {
-            const int len = __ldg(p.a.length + b), n = block_rows(p.a.cu_drafts, b, p.a.kmax);
-            if (!length_ok(p, len, n)) {
-                T* to = reinterpret_cast<T*>(p.a.out) + first_row(p.a.cu_drafts, b, p.a.kmax) * p.a.Hq * (int64_t)D;
-                for (int64_t i = tid; i < (int64_t)n * p.a.Hq * D; i += kJoinThreads) put(to + i, __int_as_float(0x7fffffff));
-            }
-        }
-    }
-    const int4 it = __ldcg(p.desc + blockIdx.x);
-    if (it.w > 0 && !timeout) {
-        const int len = __ldg(p.a.length + it.x), n = block_rows(p.a.cu_drafts, it.x, p.a.kmax);
-        const Item item = make_item(p, len, n, it.z);
-        const int rows = item.r1 - item.r0;
-        const int64_t row0 = first_row(p.a.cu_drafts, it.x, p.a.kmax);
-        for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += kJoinWarps * gridDim.y) {
-            // part 0 is in the second slot of CTA c, part k in the first of CTA c + k
-            const int64_t slot0 = 2 * (int64_t)blockIdx.x;
-            float big = -kInf;
-            for (int k = lane; k < it.w; k += 32)
-                big = fmaxf(big, __ldcg(p.ml + (slot0 + (k == 0 ? 1 : 2 * k)) * p.rows + r).x);
-            big = warp_max(big);
-            if (big == -kInf) big = 0.f;
-            float sum = 0.f;
-            float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-            for (int k = 0; k < it.w; ++k) {
-                const int64_t at = (slot0 + (k == 0 ? 1 : 2 * k)) * p.rows + r;
-                const float2 ml = __ldcg(p.ml + at);
-                const float f = exp2f(ml.x - big);
-                sum = fmaf(f, ml.y, sum);
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    const int c = (lane + 32 * d) * 4;
-                    if (c < D) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at * D + c));
-                        o[d].x = fmaf(f, y.x, o[d].x);
-                        o[d].y = fmaf(f, y.y, o[d].y);
-                        o[d].z = fmaf(f, y.z, o[d].z);
-                        o[d].w = fmaf(f, y.w, o[d].w);
-                    }
-                }
-            }
-            const int rr = item.r0 + r, i = rr / p.G;
-            T* to = reinterpret_cast<T*>(p.a.out) + ((row0 + i) * p.a.Hq + it.y * p.G + rr - i * p.G) * (int64_t)D;
-            const float inv = 1.f / sum;
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const int c = (lane + 32 * d) * 4;
-                if (c < D) {
-                    put(to + c, o[d].x * inv);
-                    put(to + c + 1, o[d].y * inv);
-                    put(to + c + 2, o[d].z * inv);
-                    put(to + c + 3, o[d].w * inv);
-                }
-            }
-        }
-    }
-    // the last CTA leaves the header as the next call needs it
-    __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        if (atomicAdd(p.header + 1, 1) == ids - 1) {
-            p.header[0] = 0;
-            p.header[1] = 0;
-        }
-    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -376,8 +245,6 @@ static int sm_count(int* sms) {
     *sms = n;
     return SPEC_OK;
 }
-
-constexpr int kMaxCtas = 512;   // CTAs of the attention grid that the workspace has room for
 
 // Rows of a group and CTAs of the grid.
 static void cut(const spec_attention_args* a, int sms, int* rows, int* ctas) {
@@ -412,18 +279,21 @@ static int check(const spec_attention_args* a) {
 
 static size_t layout(const spec_attention_args* a, int rows, int ctas, AttnParams* p) {
     char* base = reinterpret_cast<char*>(a->workspace);
+    auto take = [](size_t* at, size_t bytes) {
+        const size_t from = *at;
+        *at += (bytes + 255) & ~(size_t)255;
+        return from;
+    };
+    // the arrival counts of the largest grid come first, so that every call finds them where it left them
     size_t at = 256;
-    const size_t desc = at;
-    at += ((size_t)ctas * sizeof(int4) + 255) & ~(size_t)255;
-    const size_t ml = at;
-    at += ((size_t)2 * ctas * rows * sizeof(float2) + 255) & ~(size_t)255;
-    const size_t part = at;
-    at += (size_t)2 * ctas * rows * a->D * sizeof(float);
+    const size_t arrived = take(&at, (size_t)kJoinLevels * 2 * kMaxCtas * sizeof(int32_t));
+    const size_t ml = take(&at, (size_t)kJoinLevels * 2 * ctas * rows * sizeof(float2));
+    const size_t part = take(&at, (size_t)2 * ctas * rows * a->D * sizeof(float));
     if (p != nullptr) {
-        p->header = reinterpret_cast<int32_t*>(base);
-        p->desc = reinterpret_cast<int4*>(base + desc);
+        p->timeout = reinterpret_cast<int32_t*>(base);
+        p->arrived = reinterpret_cast<int32_t*>(base + arrived);
         p->ml = reinterpret_cast<float2*>(base + ml);
-        p->part = reinterpret_cast<float*>(base + part);
+        p->part = reinterpret_cast<float4*>(base + part);
     }
     return at;
 }
@@ -434,8 +304,7 @@ static cudaError_t launch_float(const AttnParams& p, cudaStream_t s, bool q_vec)
     const cudaError_t e = cudaFuncSetAttribute(attention_float_kernel<T, R, TK, ND>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attention_float_kernel<T, R, TK, ND><<<p.ctas, kFloatThreads, smem, s>>>(p, q_vec);
-    return cudaGetLastError();
+    return launch_after(attention_float_kernel<T, R, TK, ND>, dim3(p.ctas), dim3(kFloatThreads), smem, s, p, (int)q_vec);
 }
 
 template <typename T, int R, int TK>
@@ -452,20 +321,6 @@ static cudaError_t launch_float_r(const AttnParams& p, cudaStream_t s, bool q_ve
     if (p.rows == 16) return launch_float_d<T, 16, 16>(p, s, q_vec);
     if (p.rows == 32) return launch_float_d<T, 32, 16>(p, s, q_vec);
     return launch_float_d<T, 64, 16>(p, s, q_vec);
-}
-
-template <typename T>
-static cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas, kJoinSplit);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, p);
 }
 
 }  // namespace sv
@@ -496,6 +351,7 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
         return set_error(SPEC_ERR_ARG, "spec_paged_attention: a required pointer is NULL");
     if (((uintptr_t)a->k_pages | (uintptr_t)a->v_pages) & 15)
         return set_error(SPEC_ERR_ARG, "spec_paged_attention: the pool is not 16-byte aligned");
+    if ((uintptr_t)a->out & 15) return set_error(SPEC_ERR_ARG, "spec_paged_attention: out is not 16-byte aligned");
     if (!std::isfinite(a->scale)) return set_error(SPEC_ERR_ARG, "spec_paged_attention: scale is not finite");
     int sms = 0;
     AttnParams p;
@@ -518,7 +374,5 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     cudaError_t e = tensor                         ? launch_attention_tc(p, s)
                     : a->dtype == SPEC_DTYPE_F32 ? launch_float_r<float>(p, s, q_vec)
                                                  : launch_float_r<unsigned short>(p, s, q_vec);
-    if (e != cudaSuccess) return set_cuda_error(e, "spec_paged_attention");
-    e = a->dtype == SPEC_DTYPE_F32 ? launch_join<float>(p, s) : launch_join<unsigned short>(p, s);
-    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_paged_attention (join)");
+    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_paged_attention");
 }

@@ -27,6 +27,7 @@ namespace sv {
 
 constexpr int kTcThreads = 192;
 constexpr int kTcRows = 128;           // M of the products
+constexpr int kQPlace = kTcRows / 2 * 128;   // bytes to Q's second place: up to 64 rows, the next item's rows fit behind
 constexpr int kTcSpinLimit = 1 << 20;  // polls before a wait gives up
 
 // DP: the head padded to 64, 128 or 256 columns (TMA fills the rest with zeros).
@@ -43,7 +44,7 @@ struct TcLayout {
 };
 
 struct TcShared {
-    uint64_t q_full, q_empty, o_done, drain;
+    uint64_t q_full[2], q_empty[2], o_done[2], drain;
     uint64_t full[10], empty[10];
     uint64_t s_full[2], p_full[2];
     Start start;
@@ -53,16 +54,29 @@ struct TcShared {
     int abort;
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], "
+        "%6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One look at the phase, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Waits for the phase; false when the wait (or another one of the CTA) gave up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, int* abort) {
     for (int n = 0; !mbar_try_wait(bar, parity); ++n) {
@@ -128,10 +142,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 #undef SV_R8
 #undef SV_W8
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+// 32 bytes in one store
+__device__ __forceinline__ void store32(void* to, const uint32_t* x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 // ---- warp 4: copies -------------------------------------------------------------------
@@ -149,6 +164,11 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     int slot = 0;
     unsigned phase = 1;                                  // a fresh barrier: the phase before its first is done
     int items = 0;
+    const int q_places = p.rows <= kTcRows / 2 ? 2 : 1;
+    // Keys and values that are read once leave L2 first: otherwise they push out the kernel's own code, the tables
+    // and the parts, and every one of those is then a miss to memory.  A block of several groups reads them again.
+    const uint64_t stay = l2_evict_normal_policy();
+    const uint64_t once = (p.a.kmax + 1) * p.G <= p.rows ? l2_evict_first_policy() : stay;
     bool ok = true;
     do {
         const int32_t* table = p.a.page_table + (int64_t)w.b * p.a.max_pages;
@@ -177,7 +197,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
                 for (int u = lane; u < pages * Lay::kHalves; u += 32) {
                     const int half = u / pages;   // u % pages = lane % pages: 32 is a multiple of pages
                     tma_load_3d(to + half * (kTile * 128) + (lane % pages) * box * 128, kv ? vmap : kmap, half * 64,
-                                pages > 1 ? 0 : y, z, &sh.full[slot]);
+                                pages > 1 ? 0 : y, z, &sh.full[slot], once);
                 }
                 if (++slot == Lay::kSlots) {
                     slot = 0;
@@ -185,14 +205,14 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
                 }
             }
             if (t == w.t0 && ok) {
-                // the item's rows of Q, behind its first keys: they wait for the item before to be through with its own
-                ok = warp_wait_for(&sh.q_empty, (items & 1) ^ 1, &sh.abort);
+                // the item's rows of Q, behind its first keys: they wait for the last user of their place
+                const int at = items % q_places;
+                ok = warp_wait_for(&sh.q_empty[at], ((items / q_places) & 1) ^ 1, &sh.abort);
                 if (ok && lane == 0) {
-                    const int tokens = p.rows / p.G;
-                    mbar_expect_tx(&sh.q_full, Lay::kHalves * tokens * p.G * 128);
+                    mbar_expect_tx(&sh.q_full[at], Lay::kHalves * p.rows * 128);
                     for (int half = 0; half < Lay::kHalves; ++half)
-                        tma_load_3d(q_at + half * (kTcRows * 128), qmap, half * 64, w.h * p.G, (int)row0 + w.it.r0 / p.G,
-                                    &sh.q_full);
+                        tma_load_3d(q_at + half * (kTcRows * 128) + at * kQPlace, qmap, half * 64, w.h * p.G,
+                                    (int)row0 + w.it.r0 / p.G, &sh.q_full[at], stay);
                 }
                 ++items;
             }
@@ -201,26 +221,30 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     if (!ok) {   // gave up: whatever was copied must have arrived before the CTA's memory is given back
         for (int s = 0; s < Lay::kSlots; ++s)
             for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
-        for (int n = 0; n < kTcSpinLimit / 64 && items > 0 && !mbar_try_wait(&sh.q_full, (items - 1) & 1); ++n) {}
+        for (int i = max(0, items - q_places); i < items; ++i)
+            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.q_full[i % q_places], (i / q_places) & 1); ++n) {}
     }
 }
 
 // ---- warp 5, one thread: products ------------------------------------------------------
+// Whichever product has its operands first: S of tile n (its keys, the item's Q, and P of tile n - 2, whose
+// place S takes, used up) or O += P V of tile n (P, and the tile's values).
 template <int DP>
 __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
     const uint32_t q_at = smem_u32(smem), ring = q_at + Lay::kQBytes;
     const uint32_t tmem = sh.tmem;
     const int ksteps = (p.a.D + 15) / 16;
+    const int q_places = p.rows <= kTcRows / 2 ? 2 : 1;
     // a negative scale is a negated Q (bit 13) and its magnitude
     const uint32_t qk = mma_desc(kTile, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t pv = mma_desc(DP, true);
-    Walk w;   // of the tiles whose S product is issued: one tile ahead of the other product
+    Walk w;   // of the S products
     if (!w.start(p, sh.start)) return;
-    int64_t total = min(sh.start.span, sh.start.total - sh.start.tile);
-    int t_qk = w.t0;
-    int items = 0;
-    bool more = true, ok = true;
+    int t = w.t0, items = 0;
+    bool more = true;
+    unsigned n_qk = 0, n_pv = 0;   // products issued
+    unsigned firsts = 0;           // bit (tile & 1): the tile is its item's first
     int kslot = 0, vslot = 1;
     unsigned kphase = 0, vphase = 0;
     auto step = [](int& slot, unsigned& phase) {
@@ -230,60 +254,59 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
             phase ^= 1;
         }
     };
-    unsigned firsts = 0;   // bit (tile & 1): the tile is the first of its item
-    int64_t n_qk = 0;
-    auto issue_qk = [&]() {
-        const int buf = (int)(n_qk & 1);
-        if (t_qk == w.t0) {
-            ok = wait_for(&sh.q_full, items & 1, &sh.abort);
-            firsts |= 1u << buf;
-        } else {
-            firsts &= ~(1u << buf);
-        }
-        ok = ok && wait_for(&sh.full[kslot], kphase, &sh.abort);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t k_at = ring + kslot * Lay::kSlotBytes;
-        for (int k = 0; k < ksteps; ++k) {
-            const int half = k >> 2, in = (k & 3) * 32;
-            mma_ss(tmem + buf * kTile, smem_desc(q_at + half * (kTcRows * 128) + in, 16),
-                   smem_desc(k_at + half * (kTile * 128) + in, 16), qk, k > 0);
-        }
-        mma_commit(&sh.s_full[buf]);
-        mma_commit(&sh.empty[kslot]);
-        step(kslot, kphase);
-        ++n_qk;
-        if (++t_qk == w.t1) {
-            mma_commit(&sh.q_empty);
-            ++items;
-            more = w.next(p);
-            t_qk = w.t0;
-        }
-    };
-    issue_qk();
-    for (int64_t t = 0; t < total && ok; ++t) {
-        if (more) {
-            // S of tile t + 1 goes where P of tile t - 1 was: that product has to be done
-            if (t > 0) ok = wait_for(&sh.o_done, (unsigned)(t - 1) & 1, &sh.abort);
-            if (ok) issue_qk();
-        }
-        const int buf = (int)(t & 1);
-        ok = ok && wait_for(&sh.p_full[buf], (unsigned)(t >> 1) & 1, &sh.abort);
-        ok = ok && wait_for(&sh.full[vslot], vphase, &sh.abort);
-        if (!ok) break;
-        tc_fence_after();
-        const bool first = (firsts >> buf) & 1;
-        const uint32_t v_at = ring + vslot * Lay::kSlotBytes;
+    int spins = 0;
+    while (more || n_pv != n_qk) {
+        bool did = false;
+        if (n_pv != n_qk) {
+            const unsigned buf = n_pv & 1;
+            if (mbar_test(&sh.p_full[buf], (n_pv >> 1) & 1) && mbar_test(&sh.full[vslot], vphase)) {
+                tc_fence_after();
+                const bool first = (firsts >> buf) & 1;
+                const uint32_t v_at = ring + vslot * Lay::kSlotBytes;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, smem_desc(v_at + k * 2048, kTile * 128), pv, !(first && k == 0));
-        mma_commit(&sh.o_done);
-        mma_commit(&sh.empty[vslot]);
-        step(vslot, vphase);
-    }
-    if (!ok) {
-        mma_commit(&sh.drain);
-        for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.drain, 0); ++n) {}
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, smem_desc(v_at + k * 2048, kTile * 128), pv,
+                           !(first && k == 0));
+                mma_commit(&sh.o_done[buf]);
+                mma_commit(&sh.empty[vslot]);
+                step(vslot, vphase);
+                ++n_pv;
+                did = true;
+            }
+        }
+        if (more && n_qk - n_pv < 2) {
+            const unsigned buf = n_qk & 1;
+            const int q = items % q_places;
+            if ((n_qk < 2 || mbar_test(&sh.o_done[buf], ((n_qk >> 1) - 1) & 1)) && mbar_test(&sh.full[kslot], kphase) &&
+                (t != w.t0 || mbar_test(&sh.q_full[q], (items / q_places) & 1))) {
+                tc_fence_after();
+                firsts = (firsts & ~(1u << buf)) | (unsigned)(t == w.t0) << buf;
+                const uint32_t k_at = ring + kslot * Lay::kSlotBytes;
+                for (int k = 0; k < ksteps; ++k) {
+                    const int half = k >> 2, in = (k & 3) * 32;
+                    mma_ss(tmem + buf * kTile, smem_desc(q_at + half * (kTcRows * 128) + q * kQPlace + in, 16),
+                           smem_desc(k_at + half * (kTile * 128) + in, 16), qk, k > 0);
+                }
+                mma_commit(&sh.s_full[buf]);
+                mma_commit(&sh.empty[kslot]);
+                step(kslot, kphase);
+                ++n_qk;
+                if (++t == w.t1) {
+                    mma_commit(&sh.q_empty[q]);
+                    ++items;
+                    more = w.next(p);
+                    t = w.t0;
+                }
+                did = true;
+            }
+        }
+        spins = did ? 0 : spins + 1;
+        if (spins > kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+        if (spins > 0 && *reinterpret_cast<volatile int*>(&sh.abort)) {
+            mma_commit(&sh.drain);
+            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.drain, 0); ++n) {}
+            return;
+        }
     }
 }
 
@@ -296,7 +319,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
     char* ring = smem + Lay::kQBytes;
     Walk w;
     if (!w.start(p, sh.start)) return;
-    int64_t t_all = 0;   // tiles of the CTA so far
+    unsigned t_all = 0;   // tiles of the CTA so far
     int vslot = 1;
     unsigned vphase = 0;
     bool ok = true;
@@ -309,9 +332,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
         const bool work = warp * 32 < rows;                                  // any row in this warp
         float m = -kInf, l = 0.f;
         for (int t = w.t0; t < w.t1; ++t, ++t_all) {
-            const int buf = (int)(t_all & 1);
+            const unsigned buf = t_all & 1;
             const int j0 = tile_start(w.it, t);
-            ok = warp_wait_for(&sh.s_full[buf], (unsigned)(t_all >> 1) & 1, &sh.abort);
+            ok = warp_wait_for(&sh.s_full[buf], (t_all >> 1) & 1, &sh.abort);
             if (!ok) break;
             float scale_o = 1.f;
             if (work) {
@@ -331,7 +354,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 }
                 float x[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-                for (int c = 0; c < kTile; ++c) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
+                for (int c = 0; c < kTile; c += 2)   // three-way maxima
+                    x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
                 const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;   // the scale is positive here
                 if (tid < rows && top > m + 8.f) {   // lanes without a row never ask for the scaling of O
                     scale_o = m == -kInf ? 0.f : ex2(m - top);
@@ -339,17 +363,16 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                     l *= scale_o;
                 }
                 const float base = m == -kInf ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pk[kTile / 2];
 #pragma unroll
                 for (int c = 0; c < kTile; c += 2) {
-                    const float e0 = ex2(fmaf(__uint_as_float(s[c]), p.scale_log2, -base));
-                    const float e1 = ex2(fmaf(__uint_as_float(s[c + 1]), p.scale_log2, -base));
-                    pk[c / 2] = pack_bf16(e0, e1);
-                    sum[c & 2] += bf16_lo(pk[c / 2]);
-                    sum[(c & 2) + 1] += bf16_hi(pk[c / 2]);
+                    const float2 y = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, nb);
+                    pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
+                    sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], make_float2(bf16_lo(pk[c / 2]), bf16_hi(pk[c / 2])));
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 __syncwarp();
                 tmem_st32(lanes + buf * kTile, pk);
             }
@@ -371,13 +394,13 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 vphase ^= 1;
             }
             if (t_all > 0) {   // the product before has to be done before O is scaled, or begun anew
-                ok = warp_wait_for(&sh.o_done, (unsigned)(t_all - 1) & 1, &sh.abort);
+                ok = warp_wait_for(&sh.o_done[buf ^ 1], ((t_all - 1) >> 1) & 1, &sh.abort);
                 if (!ok) break;
             }
             if (work) {
                 if (t > w.t0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(lanes + Lay::kOCol + c, o);
@@ -393,55 +416,55 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[buf]);
         }
-        ok = ok && warp_wait_for(&sh.o_done, (unsigned)(t_all - 1) & 1, &sh.abort);
+        ok = ok && warp_wait_for(&sh.o_done[(t_all - 1) & 1], ((t_all - 1) >> 1) & 1, &sh.abort);
         if (!ok) break;
         const bool whole = w.whole();
-        if (w.begins_part() && tid == 0) p.desc[cta] = make_int4(w.b, w.h, w.g, w.parts(cta, sh.start.span));
         if (work) {
             tc_fence_after();
             const bool mine = tid < rows;
-            const int64_t part_row = (int64_t)w.slot(cta) * p.rows + tid;
             const int rr = w.it.r0 + tid;
             unsigned short* to = reinterpret_cast<unsigned short*>(p.a.out) +
                                  ((first_row(p.a.cu_drafts, w.b, p.a.kmax) + token) * p.a.Hq + w.h * p.G + rr - token * p.G) * (int64_t)p.a.D;
-            const bool vec = (reinterpret_cast<uintptr_t>(p.a.out) & 15) == 0;
+            const bool wide = (((uint32_t)reinterpret_cast<uintptr_t>(p.a.out) | p.a.D * 2) & 31) == 0;
+            const int64_t slot = w.slot(cta);
             const float inv = 1.f / l;
-            if (mine && !whole) p.ml[part_row] = make_float2(m, l);
-#pragma unroll
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-                if (c0 >= p.a.D) break;
+            if (mine && !whole) __stcg(p.ml + slot * p.rows + tid, make_float2(m, l));
+#pragma unroll 1
+            for (int c0 = 0; c0 < p.a.D; c0 += 32) {
                 uint32_t o[32];
                 __syncwarp();
                 tmem_ld32(lanes + Lay::kOCol + c0, o);
                 tc_wait_ld();
                 if (mine && whole) {
+                    uint32_t x[16];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        if (c0 + c >= p.a.D) break;
-                        uint4 x;
-                        x.x = pack_bf16(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
-                        x.y = pack_bf16(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
-                        x.z = pack_bf16(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv);
-                        x.w = pack_bf16(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv);
-                        if (vec) {
-                            *reinterpret_cast<uint4*>(to + c0 + c) = x;
+                    for (int c = 0; c < 32; c += 2)
+                        x[c / 2] = pack_bf16(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 16) {
+                        if (wide && c0 + c < p.a.D) {
+                            store32(to + c0 + c, x + c / 2);
                         } else {
-                            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-                            for (int i = 0; i < 8; ++i) to[c0 + c + i] = (unsigned short)(y[i / 2] >> (16 * (i & 1)));
+                            if (c0 + c < p.a.D)
+                                *reinterpret_cast<uint4*>(to + c0 + c) = make_uint4(x[c / 2], x[c / 2 + 1], x[c / 2 + 2], x[c / 2 + 3]);
+                            if (c0 + c + 8 < p.a.D)
+                                *reinterpret_cast<uint4*>(to + c0 + c + 8) = make_uint4(x[c / 2 + 4], x[c / 2 + 5], x[c / 2 + 6], x[c / 2 + 7]);
                         }
                     }
-                } else if (mine) {
-                    float* q = p.part + part_row * p.a.D + c0;
+                } else if (mine) {   // neighbouring rows are neighbours in memory
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
                         if (c0 + c >= p.a.D) break;
-                        *reinterpret_cast<uint4*>(q + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        __stcg(p.part + (slot * (p.a.D / 4) + (c0 + c) / 4) * p.rows + tid,
+                               make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
+                                           __uint_as_float(o[c + 3])));
                     }
                 }
             }
             __syncwarp();
             tc_fence_before();
         }
+        if (!whole) join_parts<unsigned short, 128, 1>(p, w, cta, sh.start.span, tid, &sh.scratch);
     } while (w.next(p));
 }
 
@@ -454,6 +477,10 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
     TcShared& sh = *reinterpret_cast<TcShared*>(smem + Lay::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5;
     const int cta = blockIdx.x;
+    if (warp == 4 && (tid & 31) < 3) {
+        const CUtensorMap* map = (tid & 31) == 0 ? &kmap : (tid & 31) == 1 ? &vmap : &qmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
     if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"((uint32_t)Lay::kTmemCols)
@@ -461,29 +488,29 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.o_done, 1);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < Lay::kSlots; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.o_done[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 4);
         }
         mbar_init_fence();
         sh.abort = 0;
-        p.desc[cta] = make_int4(0, 0, 0, 0);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     find_start<kTcThreads>(p, cta, &sh.start, sh.scan, &sh.scratch);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 4) {
         copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
+        write_status<unsigned short>(p, cta, sh.start.valid);   // while the last tiles are computed
     } else if (warp == 5) {
         if ((tid & 31) == 0) mma_role<DP>(p, smem, sh);
         __syncwarp();
@@ -496,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"((uint32_t)Lay::kTmemCols));
     }
-    if (tid == 0 && sh.abort) atomicOr(p.header, 1);
+    if (tid == 0 && sh.abort) write_timeout(p);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -547,8 +574,7 @@ static cudaError_t launch_tc(const AttnParams& p, const CUtensorMap (&map)[3], c
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) TcReady<DP>::on[dev].store(1, std::memory_order_release);
     }
-    attention_tc_kernel<DP><<<p.ctas, kTcThreads, bytes, s>>>(p, map[0], map[1], map[2]);
-    return cudaGetLastError();
+    return launch_after(attention_tc_kernel<DP>, dim3(p.ctas), dim3(kTcThreads), bytes, s, p, map[0], map[1], map[2]);
 }
 
 bool tensor_path(const spec_attention_args* a) {
