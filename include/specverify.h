@@ -94,7 +94,7 @@ extern "C" {
 #define SPEC_MAX_STREAMS 65535    /* streams of a cache call */
 #define SPEC_MAX_HEAD 256         /* elements of an attention head */
 #define SPEC_MAX_PAGE 256         /* tokens of a page */
-#define SPEC_ATTENTION_ZERO_BYTES 16384   /* of spec_paged_attention's workspace */
+#define SPEC_ATTENTION_ZERO_BYTES 256   /* of spec_paged_attention's workspace */
 
 /* columns of the optional diag output (one row per target row) */
 #define SPEC_DIAG_COLS 8
@@ -481,8 +481,8 @@ void spec_cost_curve_destroy(void* curve);
  * SPEC_ATTENTION_ZERO_BYTES zero-filled once before its first use (a call leaves them so, except one
  * that reports TIMEOUT); calls that share it must be ordered.
  * Errors: SPEC_ERR_ARG (NULL pointer, a pool or out that is not 16-byte aligned, scale not finite),
- * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of Hkv,
- * q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
+ * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of
+ * Hkv or more than 128 times it, q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
  * SPEC_ERR_CUDA.  B == 0 launches nothing.
  */
 typedef struct {
@@ -508,7 +508,7 @@ typedef struct {
 
 int spec_paged_attention(const spec_attention_args* args, void* stream);
 /* Bytes of workspace the call needs (0 for B = 0 and for invalid sizes).  Reads the sizes, the dtype,
- * the scale, and q's address and stride (rows that are not 16-byte aligned take another kernel). */
+ * the scale, and q's address and stride (bf16 rows that are not 16-byte aligned are packed first). */
 size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
 
 /*

@@ -603,69 +603,88 @@ _APPEND = struct.Struct("@8i 5P 3q 3P")          # spec_append_args
 _RESIZE = struct.Struct("@5i q 10P N")           # spec_resize_args
 
 
-def _on(t, name, device, dtype, shape):
-    """``t`` is a dense CUDA tensor of this device, dtype and shape."""
-    if not t.is_cuda:
+_T = None       # torch, once a cache call has run
+_I32 = None
+_CODES = {}     # dtype -> SPEC_DTYPE_*
+
+
+def _cache_torch():
+    global _T, _I32, _CODES
+    import torch
+    _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    _I32 = torch.int32
+    _T = torch
+    return torch
+
+
+def _wrong(t, name, device, dtype, shape):
+    """Raises what is wrong with a tensor that should be dense, of this device, dtype and shape."""
+    if not isinstance(t, _T.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
+    raise ValueError(f"{name} is on another device")
+
+
+def _on(t, name, device, dtype, shape):
+    """The pointer of a dense tensor of this device, dtype and shape."""
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _wrong(t, name, device, dtype, shape)
     return t.data_ptr()
 
 
 def _rows_of(t, name, device, dtype, heads, D):
     """(pointer, row stride) of [rows, heads, D] with dense rows (a slice of a wider projection)."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} must be [rows, {heads}, {D}], got {list(t.shape)}")
-    row, head, one = t.stride()
-    if one != 1 or (head != D and heads > 1) or (row < heads * D and t.shape[0] > 1):
-        raise ValueError(f"{name} must have dense rows of heads * D elements")
+    shape = t.shape
     if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
-    return t.data_ptr(), max(row, heads * D)
+        raise TypeError(f"{name} must be a CUDA tensor on the cache's device")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} must be [rows, {heads}, {D}], got {list(shape)}")
+    row, head, one = t.stride()
+    dense = heads * D
+    if one != 1 or (head != D and heads > 1) or (row < dense and shape[0] > 1):
+        raise ValueError(f"{name} must have dense rows of heads * D elements")
+    return t.data_ptr(), row if row > dense else dense
 
 
 def _layer_of(k_pages, v_pages):
-    """(device, dtype code, num_pages, Hkv, page_size, D) of one layer's pool."""
-    if not (k_pages.is_cuda and v_pages.is_cuda):
-        raise TypeError("k_pages and v_pages must be CUDA tensors")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    """(device, dtype code, pointers, shape) of one layer's pool."""
+    shape, device, dtype = k_pages.shape, k_pages.get_device(), k_pages.dtype
+    if device < 0 or v_pages.get_device() != device:
+        raise TypeError("k_pages and v_pages must be CUDA tensors on one device")
+    if len(shape) != 4 or shape != v_pages.shape or dtype is not v_pages.dtype:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D] of one dtype")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    device = k_pages.get_device()
-    if v_pages.get_device() != device:
-        raise ValueError("v_pages is on another device")
-    return (device, _dtype_code(k_pages)) + tuple(k_pages.shape)
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return device, code, k_pages.data_ptr(), v_pages.data_ptr(), shape
 
 
 def _blocks_of(device, page_table, length, cu_drafts, rows, kmax):
     """(B, max_pages, pointers of cu_drafts, length, page_table) of packed blocks."""
-    i32 = _torch().int32
-    if page_table.dim() != 2:
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
+    B = shape[0]
     if cu_drafts is None:
         cu = 0
         if rows != B * (kmax + 1):
             raise ValueError("without cu_drafts there are B * (kmax + 1) rows")
     else:
-        cu = _on(cu_drafts, "cu_drafts", device, i32, (B + 1,))
-    return (B, max_pages, cu, _on(length, "length", device, i32, (B,)),
-            _on(page_table, "page_table", device, i32, (B, max_pages)))
+        cu = _on(cu_drafts, "cu_drafts", device, _I32, (B + 1,))
+    return (B, shape[1], cu, _on(length, "length", device, _I32, (B,)), _on(page_table, "page_table", device, _I32, shape))
 
 
 def _raw_stream(stream, device):
-    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _T._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kmax, scale, window=0, sinks=0,
@@ -677,26 +696,28 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     block) and cu_drafts [B + 1] int32 (None: kmax drafts each; kmax = 0 is plain decoding).  window > 0
     keeps the last ``window`` positions of each row and the first ``sinks`` of its stream.  Returns
     (and reuses) ``out`` with out [rows, Hq, D], status [B], workspace."""
-    torch = _torch()
-    device, code, num_pages, Hkv, page_size, D = _layer_of(k_pages, v_pages)
-    if q.dim() != 3 or q.shape[1] % Hkv != 0:
+    torch = _T or _cache_torch()
+    device, code, kp, vp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
+    shape = q.shape
+    if len(shape) != 3 or shape[1] % Hkv != 0:
         raise ValueError("q must be [rows, Hq, D] with Hq a multiple of Hkv")
-    rows, Hq, _ = q.shape
+    rows, Hq, _ = shape
     qp, stride = _rows_of(q, "q", device, k_pages.dtype, Hq, D)
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
-    L = lib()
-    sizes = (B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride,
-             rows, k_pages.data_ptr(), v_pages.data_ptr())
+    L = _lib or lib()
     if out is None:
-        # the workspace starts at zero where the calls count arrivals, and every call leaves it so
-        need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(*sizes, 0, 0, 0, 0))
+        # the first 256 bytes of the workspace start at zero and every call leaves them so
+        need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(
+            B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows,
+            kp, vp, 0, 0, 0, 0))
         out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
                "status": torch.empty(B, dtype=torch.int32, device=q.device),
                "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
-    o, ws = out["out"], out["workspace"]
-    args = _ATTENTION.pack(*sizes, _on(o, "out", device, q.dtype, (rows, Hq, D)),
-                           _on(out["status"], "status", device, torch.int32, (B,)), ws.data_ptr(), ws.numel())
-    rc = L.spec_paged_attention(args, _raw_stream(stream, device))
+    ws = out["workspace"]
+    rc = L.spec_paged_attention(_ATTENTION.pack(
+        B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows, kp, vp,
+        _on(out["out"], "out", device, q.dtype, shape), _on(out["status"], "status", device, _I32, (B,)), ws.data_ptr(),
+        ws.numel()), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out
@@ -706,18 +727,20 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
     """Writes the block's k and v [rows, Hkv, D] (slices of a wider projection may be passed) to their
     positions in one layer's pages; the other arguments as in spec_paged_attention.  Returns (and
     reuses) ``out`` with status [B]."""
-    torch = _torch()
-    device, code, num_pages, Hkv, page_size, D = _layer_of(k_pages, v_pages)
-    kp, ks = _rows_of(k, "k", device, k_pages.dtype, Hkv, D)
-    vp, vs = _rows_of(v, "v", device, k_pages.dtype, Hkv, D)
-    if k.shape[0] != v.shape[0]:
+    torch = _T or _cache_torch()
+    device, code, kp, vp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
+    dtype = k_pages.dtype
+    nk, ks = _rows_of(k, "k", device, dtype, Hkv, D)
+    nv, vs = _rows_of(v, "v", device, dtype, Hkv, D)
+    rows = k.shape[0]
+    if v.shape[0] != rows:
         raise ValueError("k and v must have the same rows")
-    B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, k.shape[0], kmax)
+    B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     if out is None:
         out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
-    args = _APPEND.pack(B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, kp, vp, ks, vs,
-                        k.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _on(out["status"], "status", device, torch.int32, (B,)))
-    rc = lib().spec_cache_append(args, _raw_stream(stream, device))
+    rc = (_lib or lib()).spec_cache_append(_APPEND.pack(
+        B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, nk, nv, ks, vs, rows, kp, vp,
+        _on(out["status"], "status", device, _I32, (B,))), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out
@@ -725,14 +748,15 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
 
 def _book_of(page_table, held, length, ref_count):
     """(device, B, max_pages, num_pages, pointers) of a cache's bookkeeping."""
-    i32 = _torch().int32
-    if page_table.dim() != 2 or ref_count.dim() != 1:
+    shape, pages = page_table.shape, ref_count.shape
+    if len(shape) != 2 or len(pages) != 1:
         raise ValueError("page_table must be [B, max_pages] and ref_count [num_pages]")
-    device = page_table.get_device()
-    B, max_pages = page_table.shape
-    return (device, B, max_pages, ref_count.shape[0], _on(page_table, "page_table", device, i32, (B, max_pages)),
-            _on(held, "held", device, i32, (B,)), _on(length, "length", device, i32, (B,)),
-            _on(ref_count, "ref_count", device, i32, ref_count.shape))
+    device, B = page_table.get_device(), shape[0]
+    if device < 0:
+        raise TypeError("page_table must be a CUDA tensor")
+    return (device, B, shape[1], pages[0], _on(page_table, "page_table", device, _I32, shape),
+            _on(held, "held", device, _I32, (B,)), _on(length, "length", device, _I32, (B,)),
+            _on(ref_count, "ref_count", device, _I32, pages))
 
 
 def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advance=None, room=None, out=None,
@@ -741,26 +765,28 @@ def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advan
     holds the pages of length + room tokens.  k_pool and v_pool [layers, num_pages, Hkv, page_size,
     D]; page_table [B, max_pages], held, length [B] and ref_count [num_pages] int32 are updated in
     place; advance and room [B] int32 or None.  Returns (and reuses) ``out`` with status [B], workspace."""
-    torch = _torch()
+    torch = _T or _cache_torch()
     device, B, max_pages, num_pages, tp, hp, lp, rp = _book_of(page_table, held, length, ref_count)
-    if k_pool.dim() != 5 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.shape[1] != num_pages:
-        raise ValueError("k_pool and v_pool must be [layers, num_pages, Hkv, page_size, D] of one dtype")
-    _dtype_code(k_pool)
-    layers, _, Hkv, page_size, D = k_pool.shape
-    page_bytes = Hkv * page_size * D * k_pool.element_size()
-    kp = _on(k_pool, "k_pool", device, k_pool.dtype, k_pool.shape)
-    vp = _on(v_pool, "v_pool", device, k_pool.dtype, k_pool.shape)
-    ap = 0 if advance is None else _on(advance, "advance", device, torch.int32, (B,))
-    mp = 0 if room is None else _on(room, "room", device, torch.int32, (B,))
-    L = lib()
+    shape, dtype = k_pool.shape, k_pool.dtype
+    if len(shape) != 5 or shape[1] != num_pages:
+        raise ValueError("k_pool and v_pool must be [layers, num_pages, Hkv, page_size, D]")
+    if dtype not in _CODES:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    page_size = shape[3]
+    page_bytes = shape[2] * page_size * shape[4] * (4 if dtype is torch.float32 else 2)
+    kp = _on(k_pool, "k_pool", device, dtype, shape)
+    vp = _on(v_pool, "v_pool", device, dtype, shape)
+    ap = 0 if advance is None else _on(advance, "advance", device, _I32, (B,))
+    mp = 0 if room is None else _on(room, "room", device, _I32, (B,))
+    L = _lib or lib()
     if out is None:
         need = max(int(L.spec_cache_resize_workspace_bytes(B, num_pages)), 16)
         out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
                "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
     ws = out["workspace"]
-    args = _RESIZE.pack(B, page_size, num_pages, max_pages, layers, page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
-                        _on(out["status"], "status", device, torch.int32, (B,)), ws.data_ptr(), ws.numel())
-    rc = L.spec_cache_resize(args, _raw_stream(stream, device))
+    rc = L.spec_cache_resize(_RESIZE.pack(
+        B, page_size, num_pages, max_pages, shape[0], page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
+        _on(out["status"], "status", device, _I32, (B,)), ws.data_ptr(), ws.numel()), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out
@@ -770,15 +796,15 @@ def spec_cache_fork(src, dst, page_table, held, length, ref_count, page_size, ou
     """Stream dst[e] becomes a continuation of stream src[e] (src, dst [n] int32): it gives up its pages
     and shares those of src's tokens; spec_cache_resize copies a shared page before it is written
     into.  Returns (and reuses) ``out`` with status [n]."""
-    torch = _torch()
+    torch = _T or _cache_torch()
     device, B, max_pages, num_pages, tp, hp, lp, rp = _book_of(page_table, held, length, ref_count)
     n = src.numel()
-    sp = _on(src, "src", device, torch.int32, (n,))
-    dp = _on(dst, "dst", device, torch.int32, (n,))
+    sp = _on(src, "src", device, _I32, (n,))
+    dp = _on(dst, "dst", device, _I32, (n,))
     if out is None:
         out = {"status": torch.empty(n, dtype=torch.int32, device=page_table.device)}
-    rc = lib().spec_cache_fork(sp, dp, n, B, page_size, num_pages, max_pages, tp, hp, lp, rp,
-                               _on(out["status"], "status", device, torch.int32, (n,)), _raw_stream(stream, device))
+    rc = (_lib or lib()).spec_cache_fork(sp, dp, n, B, page_size, num_pages, max_pages, tp, hp, lp, rp,
+                                         _on(out["status"], "status", device, _I32, (n,)), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out

@@ -14,10 +14,16 @@
 namespace sv {
 
 constexpr int kTile = 64;          // positions of a tile
-constexpr int kItemCost = 2;       // what beginning and ending an item takes, in tiles
 constexpr int kMaxCtas = 512;      // CTAs of an attention grid
-constexpr int kJoinFan = 8;        // parts joined at a time
-constexpr int kJoinLevels = 3;     // 8^3 = kMaxCtas
+
+// An item that lies across CTAs.  Part 0 is in the second slot of the CTA that begins it (an item is begun in a
+// CTA's second slot and carried on in the first), part k in the first slot of the k-th CTA behind.
+struct __align__(16) Unjoined {
+    int32_t parts, rows;   // 0 rows: none
+    int32_t r0, head;
+    int64_t row0;          // the block's first packed row
+    int64_t pad;
+};
 
 struct AttnParams {
     spec_attention_args a;
@@ -25,11 +31,12 @@ struct AttnParams {
     int rows;         // rows of a full group
     int ctas;         // CTAs of the grid
     int page_shift;
+    int item_cost;    // what beginning and ending an item takes, in tiles
     float scale_log2; // scale * log2(e)
     // workspace
     int32_t* timeout;  // a wait gave up (stays set)
-    int32_t* arrived;  // [kJoinLevels][2 ctas] parts of a group of parts that are there (left at zero)
-    float2* ml;        // [kJoinLevels][2 ctas][rows] maximum (of the scaled scores, base 2) and sum of a part's rows
+    Unjoined* desc;    // [ctas] the item that CTA c begins and leaves to others
+    float2* ml;        // [2 ctas][rows] maximum (of the scaled scores, base 2) and sum of a part's rows
     float4* part;      // [2 ctas][D / 4][rows] their weighted values, not yet divided
 };
 
@@ -69,7 +76,7 @@ __device__ __forceinline__ int64_t head_cost(const AttnParams& p, int len, int n
     if (!length_ok(p, len, n)) return 0;
     int64_t t = 0;
     const int groups = block_groups(p, n);
-    for (int g = 0; g < groups; ++g) t += make_item(p, len, n, g).tiles + kItemCost;
+    for (int g = 0; g < groups; ++g) t += make_item(p, len, n, g).tiles + p.item_cost;
     return t;
 }
 
@@ -103,10 +110,10 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int cta, Start* 
     for (int pass = 0; pass < 2; ++pass) {
         mine = 0;
         for (int b = b0; b < b1 && b < valid; ++b) {
-            const int len = __ldg(p.a.length + b);
+            const int len = *(p.a.length + b);
             int n = p.a.kmax + 1;
             if (cu != nullptr) {
-                const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+                const int c0 = *(cu + b), c1 = *(cu + b + 1);
                 n = c1 - c0 + 1;
                 if (n < 1 || n > p.a.kmax + 1 || (b == 0 && c0 != 0) || (int64_t)c1 + b + 1 > p.a.q_rows) {
                     atomicMin(iscratch, b);
@@ -143,7 +150,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int cta, Start* 
     }
     if (at >= before && at < before + mine) {
         for (int b = b0; b < b1; ++b) {
-            const int64_t t = head_cost(p, __ldg(p.a.length + b), block_rows(cu, b, p.a.kmax)) * p.a.Hkv;
+            const int64_t t = head_cost(p, *(p.a.length + b), block_rows(cu, b, p.a.kmax)) * p.a.Hkv;
             if (at < before + t) {
                 s->stream = b;
                 s->stream0 = before;
@@ -155,8 +162,8 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int cta, Start* 
     __syncthreads();
 }
 
-// The CTA's walk over its tiles, item by item.  Every role of a CTA walks by itself.  An item takes kItemCost +
-// tiles positions of the line: a CTA that ends in the first kItemCost of them leaves the item to the next one.
+// The CTA's walk over its tiles, item by item.  Every role of a CTA walks by itself.  An item takes item_cost +
+// tiles positions of the line: a CTA that ends in the first item_cost of them leaves the item to the next one.
 struct Walk {
     int b, h, g;          // item
     int len, n, groups;   // its stream
@@ -166,7 +173,7 @@ struct Walk {
     int64_t stop;         // where the CTA ends
 
     __device__ __forceinline__ bool load_stream(const AttnParams& p) {
-        len = __ldg(p.a.length + b);
+        len = *(p.a.length + b);
         n = block_rows(p.a.cu_drafts, b, p.a.kmax);
         groups = block_groups(p, n);
         return length_ok(p, len, n);
@@ -187,7 +194,7 @@ struct Walk {
         }
         it = make_item(p, len, n, g);
         t0 = 0;
-        end += it.tiles + kItemCost;
+        end += it.tiles + p.item_cost;
     }
     // false: the CTA has no tiles
     __device__ __forceinline__ bool start(const AttnParams& p, const Start& s) {
@@ -201,11 +208,11 @@ struct Walk {
         off -= h * per_head;
         for (g = 0;; ++g) {
             it = make_item(p, len, n, g);
-            if (off < it.tiles + kItemCost) break;
-            off -= it.tiles + kItemCost;
+            if (off < it.tiles + p.item_cost) break;
+            off -= it.tiles + p.item_cost;
         }
-        end = s.at - off + it.tiles + kItemCost;
-        t0 = max(0, (int)off - kItemCost);
+        end = s.at - off + it.tiles + p.item_cost;
+        t0 = max(0, (int)off - p.item_cost);
         return take();
     }
     // to the CTA's next item; false: the CTA is done
@@ -215,11 +222,11 @@ struct Walk {
         return take();
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == it.tiles; }
-    // slot of this CTA's part (part_slot below)
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0 ? 1 : 0); }
-    // CTA that holds the item's first tile, and how many CTAs hold tiles of it
-    __device__ __forceinline__ int first_cta(int64_t span) const { return (int)quotient(end - it.tiles, span); }
-    __device__ __forceinline__ int parts(int first, int64_t span) const { return (int)quotient(end - 1, span) - first + 1; }
+    __device__ __forceinline__ bool begins_part() const { return t0 == 0 && t1 < it.tiles; }
+    __device__ __forceinline__ Unjoined unjoined(const AttnParams& p, int cta, int64_t span) const {
+        return {(int)quotient(end - 1, span) - cta + 1, it.r1 - it.r0, it.r0, h, first_row(p.a.cu_drafts, b, p.a.kmax), 0};
+    }
 };
 
 // Is position j visible to the row of token i (its own position is len + i)?
@@ -251,7 +258,7 @@ __device__ __forceinline__ void write_status(const AttnParams& p, int cta, int v
     for (int b = cta; b < p.a.B; b += p.ctas) {
         int st = SPEC_ST_BAD_OFFSETS;
         if (b < valid) {
-            const int len = __ldg(p.a.length + b), n = block_rows(p.a.cu_drafts, b, p.a.kmax);
+            const int len = *(p.a.length + b), n = block_rows(p.a.cu_drafts, b, p.a.kmax);
             if (!length_ok(p, len, n)) {
                 st = SPEC_ST_BAD_LENGTH;
                 T* to = reinterpret_cast<T*>(p.a.out) + first_row(p.a.cu_drafts, b, p.a.kmax) * p.a.Hq * (int64_t)p.a.D;
@@ -262,9 +269,9 @@ __device__ __forceinline__ void write_status(const AttnParams& p, int cta, int v
                 const int hp = (len + n + p.a.page_size - 1) >> p.page_shift;
                 const int32_t* table = p.a.page_table + (int64_t)b * p.a.max_pages;
                 bool bad = false;
-                for (int j = lane; j < sp && j < lp; j += 32) bad |= (unsigned)__ldg(table + j) >= (unsigned)p.a.num_pages;
+                for (int j = lane; j < sp && j < lp; j += 32) bad |= (unsigned)*(table + j) >= (unsigned)p.a.num_pages;
 #pragma unroll 8
-                for (int j = lp + lane; j < hp; j += 32) bad |= (unsigned)__ldg(table + j) >= (unsigned)p.a.num_pages;
+                for (int j = lp + lane; j < hp; j += 32) bad |= (unsigned)*(table + j) >= (unsigned)p.a.num_pages;
                 st = __any_sync(0xffffffffu, bad) ? SPEC_ST_BAD_PAGE : SPEC_ST_OK;
             }
         }
@@ -282,99 +289,10 @@ __device__ __forceinline__ void write_timeout(const AttnParams& p) {
     for (int b = 0; b < p.a.B; ++b) p.a.status[b] = SPEC_ST_TIMEOUT;
 }
 
-// Slot of part k of an item whose first tile is CTA `first`'s: an item is begun in a CTA's second slot and
-// carried on in the first one of the CTAs behind.
-__device__ __forceinline__ int part_slot(int first, int k) { return 2 * (first + k) + (k == 0 ? 1 : 0); }
-
-// Joins the parts of an item that lies across CTAs.  Called by `threads` threads of a CTA (`barrier` is theirs)
-// that have written part k.  Parts are joined in groups of kJoinFan by the CTA that comes last to the group,
-// into the group's first slot; with more than kJoinFan groups these are joined in the same way, up to the
-// rows themselves.  Nobody waits, and the tree and the order of its sums do not depend on who comes last.
-//   M = max m_k,  out = sum 2^(m_k - M) o_k / sum 2^(m_k - M) l_k
-template <typename T, int threads, int barrier>
-__device__ __forceinline__ void join_parts(const AttnParams& p, const Walk& w, int cta, int64_t span, int tid, int* scratch /* shared */) {
-    const int first = w.first_cta(span);
-    int nodes = w.parts(first, span), k = cta - first, stride = 1;
-    const int rows = w.it.r1 - w.it.r0;
-    const int64_t slots = 2 * (int64_t)p.ctas;
-    const int nc = p.a.D / 4;
-    for (int level = 0;; ++level) {
-        const int g0 = k / kJoinFan * kJoinFan, n = min(kJoinFan, nodes - g0);
-        const bool last_level = nodes <= kJoinFan;
-        const int to = part_slot(first, g0 * stride);
-        asm volatile("bar.sync %0, %1;" ::"n"(barrier), "n"(threads) : "memory");
-        if (tid == 0) {
-            __threadfence();
-            int32_t* count = p.arrived + level * slots + to;
-            const bool last = atomicAdd(count, 1) == n - 1;
-            if (last) *count = 0;   // for the next call
-            __threadfence();
-            *scratch = last;
-        }
-        asm volatile("bar.sync %0, %1;" ::"n"(barrier), "n"(threads) : "memory");
-        if (!*scratch) return;
-        // a thread keeps to one row, `step` threads share the row's columns; eight columns of two parts are on their
-        // way at a time.  (Loops stay rolled: this code runs once or twice a call, and every line of it is a miss.)
-        int wide = 1;
-        while (wide < rows) wide *= 2;
-        const int r = tid & (wide - 1), step = threads / wide;
-        if (r < rows && (n > 1 || last_level)) {
-            const float2* ml = p.ml + level * slots * p.rows + r;
-            float big = -kInf, sum = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < n; ++i) big = fmaxf(big, __ldcg(ml + (int64_t)part_slot(first, (g0 + i) * stride) * p.rows).x);
-            const float base = big == -kInf ? 0.f : big;
-            const int rr = w.it.r0 + r, token = rr / p.G;
-            T* out = reinterpret_cast<T*>(p.a.out) +
-                     ((first_row(p.a.cu_drafts, w.b, p.a.kmax) + token) * p.a.Hq + w.h * p.G + rr - token * p.G) * (int64_t)p.a.D;
-#pragma unroll 1
-            for (int c0 = tid / wide; c0 < nc; c0 += 8 * step) {
-                float4 y[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                sum = 0.f;
-#pragma unroll 2
-                for (int i = 0; i < n; ++i) {
-                    const int slot = part_slot(first, (g0 + i) * stride);
-                    const float2 x = __ldcg(ml + (int64_t)slot * p.rows);
-                    const float4* from = p.part + ((int64_t)slot * nc + c0) * p.rows + r;
-                    float4 o[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) o[c] = c0 + c * step < nc ? __ldcg(from + c * step * p.rows) : y[c];
-                    const float f = ex2(x.x - base);
-                    sum = fmaf(f, x.y, sum);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        y[c] = make_float4(fmaf(f, o[c].x, y[c].x), fmaf(f, o[c].y, y[c].y), fmaf(f, o[c].z, y[c].z), fmaf(f, o[c].w, y[c].w));
-                }
-                const float inv = last_level ? 1.f / sum : 1.f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if (c0 + c * step >= nc) break;
-                    const float4 x = make_float4(y[c].x * inv, y[c].y * inv, y[c].z * inv, y[c].w * inv);
-                    if (last_level)
-                        put4(out + 4 * (c0 + c * step), x);
-                    else
-                        __stcg(p.part + ((int64_t)to * nc + c0 + c * step) * p.rows + r, x);
-                }
-            }
-            if (!last_level && tid == r) __stcg(p.ml + ((level + 1) * slots + to) * p.rows + r, make_float2(big, sum));
-        } else if (r < rows && tid == r) {   // a group of one: only its row sums move up
-            const int64_t at = (int64_t)to * p.rows + r;
-            __stcg(p.ml + (level + 1) * slots * p.rows + at, __ldcg(p.ml + level * slots * p.rows + at));
-        }
-        if (last_level) return;
-        k /= kJoinFan;
-        nodes = (nodes + kJoinFan - 1) / kJoinFan;
-        stride *= kJoinFan;
-    }
-}
-
-// The tensor-core kernel (attention_tc.cu): whether it takes the call, the rows of its groups, the CTAs of an
-// SM, the launch.
-bool tensor_path(const spec_attention_args* a);
-int tensor_rows(const spec_attention_args* a);
+// The tensor-core kernel (attention_tc.cu): bf16.
+int tensor_rows(const spec_attention_args* a);          // rows of a group
 int tensor_ctas_per_sm(const spec_attention_args* a);
-cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s);
+bool tensor_q(const spec_attention_args* a);            // q's rows can be copied as they lie
+cudaError_t launch_attention_tc(const AttnParams& p, void* q_packed, cudaStream_t s);
 
 }  // namespace sv

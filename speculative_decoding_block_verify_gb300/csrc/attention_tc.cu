@@ -178,7 +178,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
             const int j = tile_start(w.it, t) + (lane % pages) * box;
             const int end = j + box;
             int page = -1;
-            if (j < w.it.high && (end > w.it.low || j < w.it.sink)) page = __ldg(table + (j >> p.page_shift));
+            if (j < w.it.high && (end > w.it.low || j < w.it.sink)) page = *(table + (j >> p.page_shift));
             // past the last page: zeros
             next_z = (unsigned)page < (unsigned)p.a.num_pages ? page * p.a.Hkv + w.h : p.a.num_pages * p.a.Hkv;
         };
@@ -419,6 +419,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
         ok = ok && warp_wait_for(&sh.o_done[(t_all - 1) & 1], ((t_all - 1) >> 1) & 1, &sh.abort);
         if (!ok) break;
         const bool whole = w.whole();
+        if (tid == 0 && w.begins_part()) p.desc[cta] = w.unjoined(p, cta, sh.start.span);
         if (work) {
             tc_fence_after();
             const bool mine = tid < rows;
@@ -464,7 +465,6 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
             __syncwarp();
             tc_fence_before();
         }
-        if (!whole) join_parts<unsigned short, 128, 1>(p, w, cta, sh.start.span, tid, &sh.scratch);
     } while (w.next(p));
 }
 
@@ -504,6 +504,8 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         sh.abort = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join, which waits for the whole grid
+    if (tid == 0) p.desc[cta].rows = 0;
     find_start<kTcThreads>(p, cta, &sh.start, sh.scan, &sh.scratch);
     tc_fence_before();
     __syncthreads();
@@ -577,9 +579,18 @@ static cudaError_t launch_tc(const AttnParams& p, const CUtensorMap (&map)[3], c
     return launch_after(attention_tc_kernel<DP>, dim3(p.ctas), dim3(kTcThreads), bytes, s, p, map[0], map[1], map[2]);
 }
 
-bool tensor_path(const spec_attention_args* a) {
-    return a->dtype == SPEC_DTYPE_BF16 && a->scale != 0.f && a->Hq / a->Hkv <= kTcRows && (int64_t)a->num_pages * a->Hkv < INT32_MAX &&
-           a->q_rows < INT32_MAX && (((uintptr_t)a->q | (uintptr_t)(a->q_row_stride * 2)) & 15) == 0 && encoder() != nullptr;
+bool tensor_q(const spec_attention_args* a) { return (((uintptr_t)a->q | (uintptr_t)(a->q_row_stride * 2)) & 15) == 0; }
+
+// Rows of Q that do not lie on 16-byte boundaries, packed so that they do.
+__global__ void __launch_bounds__(256) pack_rows_kernel(const unsigned short* q, int64_t stride, int width, uint4* to) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const unsigned short* from = q + blockIdx.x * stride;
+    for (int c = threadIdx.x; c < width / 8; c += 256) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = from[8 * c + 2 * i] | (uint32_t)from[8 * c + 2 * i + 1] << 16;
+        to[(int64_t)blockIdx.x * (width / 8) + c] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
 }
 
 int tensor_rows(const spec_attention_args* a) {
@@ -590,12 +601,21 @@ int tensor_rows(const spec_attention_args* a) {
 
 int tensor_ctas_per_sm(const spec_attention_args* a) { return a->D > 128 ? 1 : 2; }
 
-cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_attention_tc(const AttnParams& p, void* q_packed, cudaStream_t s) {
     const spec_attention_args& a = p.a;
+    const void* q = a.q;
+    uint64_t q_stride = (uint64_t)a.q_row_stride * 2;
+    if (q_packed != nullptr && a.q_rows > 0) {
+        const cudaError_t e = launch_after(pack_rows_kernel, dim3((unsigned)a.q_rows), dim3(256), 0, s,
+                                           static_cast<const unsigned short*>(q), a.q_row_stride, a.Hq * a.D, static_cast<uint4*>(q_packed));
+        if (e != cudaSuccess) return e;
+        q = q_packed;
+        q_stride = (uint64_t)a.Hq * a.D * 2;
+    }
     CUtensorMap map[3];
     const uint64_t D = a.D, P = a.page_size;
     const uint32_t box = a.page_size < kTile ? a.page_size : kTile;
-    if (!encode3(&map[0], a.q, D, a.Hq, (uint64_t)a.q_rows, D * 2, (uint64_t)a.q_row_stride * 2, p.G, p.rows / p.G) ||
+    if (!encode3(&map[0], q, D, a.Hq, (uint64_t)(a.q_rows > 0 ? a.q_rows : 1), D * 2, q_stride, p.G, p.rows / p.G) ||
         !encode3(&map[1], a.k_pages, D, P, (uint64_t)a.num_pages * a.Hkv, D * 2, P * D * 2, box, 1) ||
         !encode3(&map[2], a.v_pages, D, P, (uint64_t)a.num_pages * a.Hkv, D * 2, P * D * 2, box, 1))
         return cudaErrorInvalidValue;

@@ -1,4 +1,6 @@
-// The packed blocks of a verify step and their pages, as the cache calls read them.
+// The packed blocks of a verify step and their pages, as the cache calls read them.  (Plain loads throughout: these
+// kernels start while the one before them still writes, and the read-only path is not ordered by
+// griddepcontrol.wait.)
 #pragma once
 
 #include "common.cuh"
@@ -13,7 +15,7 @@ __device__ __forceinline__ int valid_prefix(const int32_t* cu, int B, int kmax, 
     __syncthreads();
     int bad = B;
     for (int b = threadIdx.x; b < upto; b += blockDim.x) {
-        const int c0 = __ldg(cu + b), n = __ldg(cu + b + 1) - c0;
+        const int c0 = *(cu + b), n = *(cu + b + 1) - c0;
         if (n < 0 || n > kmax || (b == 0 && c0 != 0) || (int64_t)c0 + n + b + 1 > rows) {
             bad = b;
             break;
@@ -26,10 +28,10 @@ __device__ __forceinline__ int valid_prefix(const int32_t* cu, int B, int kmax, 
 
 // First packed row of stream b's block, and its number of rows (N_b + 1).
 __device__ __forceinline__ int64_t first_row(const int32_t* cu, int b, int kmax) {
-    return cu == nullptr ? (int64_t)b * (kmax + 1) : (int64_t)__ldg(cu + b) + b;
+    return cu == nullptr ? (int64_t)b * (kmax + 1) : (int64_t)*(cu + b) + b;
 }
 __device__ __forceinline__ int block_rows(const int32_t* cu, int b, int kmax) {
-    return cu == nullptr ? kmax + 1 : __ldg(cu + b + 1) - __ldg(cu + b) + 1;
+    return cu == nullptr ? kmax + 1 : *(cu + b + 1) - *(cu + b) + 1;
 }
 
 }  // namespace sv

@@ -30,7 +30,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
     __shared__ int s_page[SPEC_MAX_KMAX + 1];
     __shared__ int s_bad;
     const int b = blockIdx.x, tid = threadIdx.x;
-    const int len = __ldg(a.length + b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int len = __ldcg(a.length + b);
     if (tid == 0) s_bad = 0;
     const bool offsets_ok = valid_prefix(a.cu_drafts, a.B, a.kmax, a.rows, b + 1, &s_first) > b;
     int status = SPEC_ST_OK, n = 0;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
     __syncthreads();
     if (status == SPEC_ST_OK) {
         for (int i = tid; i < n; i += kAppendThreads) {
-            int page = __ldg(a.page_table + (int64_t)b * a.max_pages + ((len + i) >> shift));
+            int page = *(a.page_table + (int64_t)b * a.max_pages + ((len + i) >> shift));
             if ((unsigned)page >= (unsigned)a.num_pages) {
                 page = -1;
                 s_bad = 1;
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
         const int h = rest / units_per_head, c = rest - h * units_per_head;
         const int page = s_page[i];
         if (page < 0) continue;
-        const U x = __ldg(k + (row0 + i) * kstride + rest);
-        const U y = __ldg(v + (row0 + i) * vstride + rest);
+        const U x = *(k + (row0 + i) * kstride + rest);
+        const U y = *(v + (row0 + i) * vstride + rest);
         const int64_t to = (((int64_t)page * a.Hkv + h) * a.page_size + ((len + i) & (a.page_size - 1))) * units_per_head + c;
         kp[to] = x;
         vp[to] = y;
@@ -82,113 +83,145 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
 // ---------------------------------------------------------------------------------------
 // resize
 // ---------------------------------------------------------------------------------------
-// Workspace: a header {pairs} and per stream the plan of the call, then the free pages in rank order.
-struct ResizePlan {
+// Workspace: a header {pairs}, the copies, the shared pages that streams ask a copy of, and the free pages in rank order.
+struct ResizeSpace {
     int32_t* header;   // [0] copies asked for
-    int32_t* keep;     // pages of the stream that stay
-    int32_t* want;     // pages it needs (keep, where the call leaves it alone)
-    int32_t* next;     // its new length
-    int32_t* ask;      // the shared page that it wants a copy of, or -1
-    int32_t* need;     // pages it asks the pool for
-    int32_t* begin;    // rank of the first of them
     int2* pair;        // copies {from, to}; from = -1: none was made
-    int32_t* nth;      // copies asked for before the stream's
+    int32_t* ask;      // [B] the shared page that stream b wants a copy of, or -1
+    int32_t* copy;     // [B] ... and gets one
     int32_t* list;     // [num_pages] the free pages, lowest first
 };
 
 __host__ __device__ inline size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-__host__ __device__ inline ResizePlan resize_plan(void* ws, int B) {
+__host__ __device__ inline ResizeSpace resize_space(void* ws, int B) {
     char* p = reinterpret_cast<char*>(ws);
     const size_t per = round16((size_t)B * 4);
-    ResizePlan r;
-    r.header = reinterpret_cast<int32_t*>(p);
-    p += 256;
-    r.pair = reinterpret_cast<int2*>(p);
-    p += 2 * per;
-    int32_t** f[] = {&r.keep, &r.want, &r.next, &r.ask, &r.need, &r.begin, &r.nth};
-    for (int i = 0; i < 7; ++i) {
-        *f[i] = reinterpret_cast<int32_t*>(p);
-        p += per;
-    }
-    r.list = reinterpret_cast<int32_t*>(p);
-    return r;
+    return {reinterpret_cast<int32_t*>(p), reinterpret_cast<int2*>(p + 256), reinterpret_cast<int32_t*>(p + 256 + 2 * per),
+            reinterpret_cast<int32_t*>(p + 256 + 3 * per), reinterpret_cast<int32_t*>(p + 256 + 4 * per)};
 }
 
 static size_t resize_workspace(int B, int num_pages) {
-    return 256 + 9 * round16((size_t)B * 4) + round16((size_t)num_pages * 4);
+    return 256 + 4 * round16((size_t)B * 4) + round16((size_t)num_pages * 4);
 }
 
 __device__ __forceinline__ bool in_pool(int page, int num_pages) { return (unsigned)page < (unsigned)num_pages; }
 
-// What one stream keeps and needs (step 1's decisions), by one warp; every lane returns the same.
+// What a stream keeps and needs (step 1's decisions).
 struct StreamPlan {
-    int status, next, keep, want, held, tail;   // tail: the page that holds kept tokens and room, or -1
+    int status, next, keep, want, held;
+    int tail;   // the page that holds kept tokens and will be written into, where it is shared, or -1
 };
-__device__ __forceinline__ StreamPlan plan_stream(const spec_resize_args& a, int b, int lane) {
-    StreamPlan s;
-    const int shift = __ffs(a.page_size) - 1;
-    const int len = __ldcg(a.length + b);
-    s.held = __ldcg(a.held + b);
-    const int adv = a.advance != nullptr ? __ldg(a.advance + b) : 0;
-    const int room = a.room != nullptr ? __ldg(a.room + b) : 0;
-    const int64_t n = (int64_t)len + adv;
-    s.tail = -1;
-    if (len < 0 || n < 0 || room < 0 || s.held < 0 || s.held > a.max_pages || n > (int64_t)s.held << shift ||
-        n + room > (int64_t)a.max_pages << shift) {
-        s.status = SPEC_ST_BAD_LENGTH;
+
+// A thread's stream; stream b may be past the last one (then nothing is planned).  A few pages to look at are the
+// thread's own, many are looked at by the whole warp, one stream after the other.
+constexpr int kOwnPages = 8;
+__device__ __forceinline__ StreamPlan plan_stream(const spec_resize_args& a, int b) {
+    StreamPlan s = {SPEC_ST_OK, 0, 0, 0, 0, -1};
+    const int lane = threadIdx.x & 31, shift = __ffs(a.page_size) - 1;
+    int full = 0, lim = 0;
+    bool bad = false, mixed = false;
+    if (b < a.B) {
+        const int len = __ldcg(a.length + b);
+        s.held = __ldcg(a.held + b);
+        const int adv = a.advance != nullptr ? __ldcg(a.advance + b) : 0;
+        const int room = a.room != nullptr ? __ldcg(a.room + b) : 0;
+        const int64_t n = (int64_t)len + adv;
         s.next = len;
-        s.keep = s.want = s.held;
-        return s;
+        s.keep = s.want = full = lim = s.held;
+        if (len < 0 || n < 0 || room < 0 || s.held < 0 || s.held > a.max_pages || n > (int64_t)s.held << shift ||
+            n + room > (int64_t)a.max_pages << shift) {
+            s.status = SPEC_ST_BAD_LENGTH;
+        } else {
+            s.next = (int)n;
+            s.want = (int)((n + room + a.page_size - 1) >> shift);
+            full = (int)((n + a.page_size - 1) >> shift);
+            s.keep = lim = min(s.want, s.held);
+            mixed = room > 0 && (n & (a.page_size - 1)) != 0;
+        }
     }
-    s.next = (int)n;
-    s.want = (int)((n + room + a.page_size - 1) >> shift);
-    const int full = (int)((n + a.page_size - 1) >> shift);
-    const int lim = min(s.want, s.held);
     const int32_t* row = a.page_table + (int64_t)b * a.max_pages;
-    int first = lim;
-    bool bad = false;
-    for (int j = full + lane; j < s.held; j += 32) {
-        const int p = __ldcg(row + j);
-        if (!in_pool(p, a.num_pages))
+    if (mixed) {
+        s.tail = __ldcg(row + (s.next >> shift));
+        if (!in_pool(s.tail, a.num_pages)) {
             bad = true;
-        else if (j < lim && __ldcg(a.ref_count + p) > 1)
-            first = min(first, j);
+            s.tail = -1;
+        } else if (__ldcg(a.ref_count + s.tail) <= 1) {
+            s.tail = -1;
+        }
     }
-    first = warp_min_i(first);
-    if (room > 0 && (n & (a.page_size - 1)) != 0) {
-        s.tail = __ldcg(row + (n >> shift));
-        bad |= !in_pool(s.tail, a.num_pages);
+    const int look = s.status == SPEC_ST_OK ? s.held - full : 0;
+    if (look <= kOwnPages) {
+        for (int j = full; j < full + look; ++j) {
+            const int p = __ldcg(row + j);
+            if (!in_pool(p, a.num_pages))
+                bad = true;
+            else if (j < lim && __ldcg(a.ref_count + p) > 1)
+                s.keep = min(s.keep, j);
+        }
     }
-    s.keep = first;
-    s.status = SPEC_ST_OK;
-    if (__any_sync(0xffffffffu, bad)) {
+    for (unsigned todo = __ballot_sync(0xffffffffu, look > kOwnPages); todo != 0; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1;
+        const int f = __shfl_sync(0xffffffffu, full, who), h = __shfl_sync(0xffffffffu, s.held, who);
+        const int l = __shfl_sync(0xffffffffu, lim, who), ob = __shfl_sync(0xffffffffu, b, who);
+        const int32_t* other = a.page_table + (int64_t)ob * a.max_pages;
+        int first = l;
+        bool wrong = false;
+#pragma unroll 4
+        for (int j = f + lane; j < h; j += 32) {
+            const int p = __ldcg(other + j);
+            if (!in_pool(p, a.num_pages))
+                wrong = true;
+            else if (j < l && __ldcg(a.ref_count + p) > 1)
+                first = min(first, j);
+        }
+        first = warp_min_i(first);
+        wrong = __any_sync(0xffffffffu, wrong);
+        if (lane == who) {
+            s.keep = first;
+            bad |= wrong;
+        }
+    }
+    if (bad) {
         s.status = SPEC_ST_BAD_PAGE;
-        s.next = len;
+        s.next = __ldcg(a.length + b);
         s.keep = s.want = s.held;
         s.tail = -1;
     }
     return s;
 }
 
-__device__ __forceinline__ void drop_pages(const spec_resize_args& a, int b, int keep, int held, int lane) {
+// Pages [keep, held) of every thread's stream lose a reference.
+__device__ __forceinline__ void drop_pages(const spec_resize_args& a, int b, int keep, int held) {
+    const int lane = threadIdx.x & 31;
     int32_t* row = a.page_table + (int64_t)b * a.max_pages;
-    for (int j = keep + lane; j < held; j += 32) {
-        atomicSub(a.ref_count + __ldcg(row + j), 1);
-        row[j] = -1;
+    if (held - keep <= kOwnPages) {
+        for (int j = keep; j < held; ++j) {
+            atomicSub(a.ref_count + __ldcg(row + j), 1);
+            row[j] = -1;
+        }
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, held - keep > kOwnPages); todo != 0; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1;
+        const int k = __shfl_sync(0xffffffffu, keep, who), h = __shfl_sync(0xffffffffu, held, who);
+        int32_t* other = a.page_table + (int64_t)__shfl_sync(0xffffffffu, b, who) * a.max_pages;
+#pragma unroll 4
+        for (int j = k + lane; j < h; j += 32) {
+            atomicSub(a.ref_count + __ldcg(other + j), 1);
+            other[j] = -1;
+        }
     }
 }
 
 // Without room no page is asked for, no page is replaced, and no decision reads a count: every
-// stream is independent, one warp each.
-constexpr int kTrimThreads = 128;
+// stream is independent, a thread each.
+constexpr int kTrimThreads = 64;
 __global__ void __launch_bounds__(kTrimThreads) trim_kernel(const spec_resize_args a) {
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.x * (kTrimThreads / 32) + (threadIdx.x >> 5);
-    if (b >= a.B) return;
-    const StreamPlan s = plan_stream(a, b, lane);
-    drop_pages(a, b, s.keep, s.held, lane);
-    if (lane == 0) {
+    const int b = blockIdx.x * kTrimThreads + threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const StreamPlan s = plan_stream(a, b);
+    drop_pages(a, b, s.keep, s.held);
+    if (b < a.B) {
         a.status[b] = s.status;
         if (s.status == SPEC_ST_OK) {
             a.length[b] = s.next;
@@ -210,63 +243,78 @@ __device__ __forceinline__ int block_scan(int v, int* before, int* scratch /* [k
     __syncthreads();
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int t = lane < kThreads / 32 ? scratch[lane] : 0;
+    int base = 0, total = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
-        }
-        if (lane < kThreads / 32) scratch[lane] = t;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) base += scratch[w];
+        total += scratch[w];
     }
-    __syncthreads();
-    *before = x - v + (warp ? scratch[warp - 1] : 0);
-    return scratch[kThreads / 32 - 1];
+    *before = base + x - v;
+    return total;
 }
 
 // With room: one cluster, whose barriers separate the steps (a count is read only when every
-// change of the step before it is done).
+// change of the step before it is done).  A thread has neighbouring streams, as many as there are thousands of
+// streams (one up to 4,096), and keeps what it planned in shared memory.
 constexpr int kResizeThreads = 512;
 constexpr int kResizeCtas = 8;
 constexpr int kScanPer = 16;   // counts that a thread looks at in one pass over the pool
 
+struct Planned {
+    int32_t status, next, keep, want, need, copy;
+};
+
 __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThreads)
-    resize_kernel(const spec_resize_args a) {
+    resize_kernel(const spec_resize_args a, int per) {
+    extern __shared__ Planned planned[];   // [per][kResizeThreads]
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ int scratch[kResizeThreads / 32 + 1];
+    __shared__ int scratch[kResizeThreads / 32];
+    __shared__ int s_need[kResizeCtas], s_copies[kResizeCtas], s_asks[kResizeCtas];
     __shared__ int s_count[2][kResizeCtas];
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = (int)cluster.block_rank();
-    const int wid = rank * (kResizeThreads / 32) + (tid >> 5);
-    constexpr int kWarps = kResizeCtas * kResizeThreads / 32;
-    const ResizePlan w = resize_plan(a.workspace, a.B);
+    const int b0 = (rank * kResizeThreads + tid) * per;
+    const ResizeSpace w = resize_space(a.workspace, a.B);
+    auto tell = [&](int* slots, int value) {   // every CTA of the cluster learns this CTA's value
+        if (tid < kResizeCtas) *cluster.map_shared_rank(slots + rank, tid) = value;
+    };
+    cluster.sync();   // every CTA's shared memory is there
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies, which wait for the whole grid
 
-    for (int b = wid; b < a.B; b += kWarps) {
-        const StreamPlan s = plan_stream(a, b, lane);
-        if (lane == 0) {
-            a.status[b] = s.status;
-            w.keep[b] = s.keep;
-            w.want[b] = s.want;
-            w.next[b] = s.next;
-            w.ask[b] = s.tail;
+    bool asks = false;
+    for (int i = 0; i < per; ++i) {
+        const int b = b0 + i;
+        const StreamPlan s = plan_stream(a, b);
+        planned[i * kResizeThreads + tid] = {s.status, s.next, s.keep, s.want, s.want - s.keep, s.held};
+        if (b < a.B) w.ask[b] = s.tail;
+        asks |= s.tail >= 0;
+    }
+    tell(s_asks, __syncthreads_or(asks));
+    cluster.sync();   // every count that a plan looks at has been read
+    bool any_asks = false;
+    for (int c = 0; c < kResizeCtas; ++c) any_asks |= s_asks[c] != 0;
+    for (int i = 0; i < per; ++i) {
+        Planned& q = planned[i * kResizeThreads + tid];
+        drop_pages(a, b0 + i, q.keep, q.copy /* held */);
+        q.copy = 0;
+    }
+    if (any_asks) {
+        cluster.sync();
+        // shared pages that will be written into, now that step 1 is done
+        for (int i = 0; i < per; ++i) {
+            const int p = b0 + i < a.B ? __ldcg(w.ask + b0 + i) : -1;
+            if (p >= 0 && __ldcg(a.ref_count + p) <= 1) w.ask[b0 + i] = -1;
         }
-    }
-    cluster.sync();
-    for (int b = wid; b < a.B; b += kWarps) {
-        drop_pages(a, b, __ldcg(w.keep + b), __ldcg(a.held + b), lane);
-    }
-    cluster.sync();
-    // who holds a shared page that it will write into
-    for (int b = rank * kResizeThreads + tid; b < a.B; b += kResizeCtas * kResizeThreads) {
-        const int p = __ldcg(w.ask + b);
-        if (p >= 0 && __ldcg(a.ref_count + p) <= 1) w.ask[b] = -1;
-    }
-    cluster.sync();
-    for (int b = wid; b < a.B; b += kWarps) {
-        const int p = __ldcg(w.ask + b);
-        int copy = 0;
-        if (p >= 0) {
-            int same = 0, lower = 0;
+        cluster.sync();
+        // A copy for every holder that asks, but the lowest one where all of them ask.  The askers (a fork's
+        // continuations, next to one another) are spread over the cluster's warps.
+        for (int b = rank * (kResizeThreads / 32) + (tid >> 5); b < a.B; b += kResizeCtas * kResizeThreads / 32) {
+            const int p = __ldcg(w.ask + b);
+            if (p < 0) continue;
+            int same = 0;
+            bool lower = false;
+#pragma unroll 4
             for (int o = lane; o < a.B; o += 32) {
                 const bool eq = __ldcg(w.ask + o) == p;
                 same += eq;
@@ -274,41 +322,35 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
             }
             same = __reduce_add_sync(0xffffffffu, same);
             lower = __any_sync(0xffffffffu, lower);
-            copy = !(same == __ldcg(a.ref_count + p) && !lower);
+            if (lane == 0) w.copy[b] = lower || same != __ldcg(a.ref_count + p);
         }
-        if (lane == 0) {
-            w.need[b] = __ldcg(w.want + b) - __ldcg(w.keep + b) + copy;
-            w.nth[b] = copy;
-        }
-    }
-    cluster.sync();
-    // ranks: every CTA runs the prefix sums, the first one writes them down
-    const int per = (a.B + kResizeThreads - 1) / kResizeThreads;
-    int need = 0, copies = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < a.B) {
-            need += __ldcg(w.need + b);
-            copies += __ldcg(w.nth + b);
-        }
-    }
-    int begin, nth;
-    const int total = block_scan<kResizeThreads>(need, &begin, scratch);
-    const int pairs = block_scan<kResizeThreads>(copies, &nth, scratch);
-    cluster.sync();   // every CTA has read w.nth, which becomes a prefix sum below
-    if (rank == 0) {
-        if (tid == 0) w.header[0] = pairs;
+        cluster.sync();
         for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < a.B) {
-                const int c = __ldcg(w.nth + b);
-                w.begin[b] = begin;
-                w.nth[b] = c ? nth : -1;
-                begin += __ldcg(w.need + b);
-                nth += c;
+            if (b0 + i < a.B && __ldcg(w.ask + b0 + i) >= 0 && __ldcg(w.copy + b0 + i) != 0) {
+                planned[i * kResizeThreads + tid].copy = 1;
+                ++planned[i * kResizeThreads + tid].need;
             }
         }
     }
+    // ranks of the streams' new pages and copies, in stream order
+    int need = 0, copies = 0, begin, nth;
+    for (int i = 0; i < per; ++i) {
+        need += planned[i * kResizeThreads + tid].need;
+        copies += planned[i * kResizeThreads + tid].copy;
+    }
+    tell(s_need, block_scan<kResizeThreads>(need, &begin, scratch));
+    tell(s_copies, any_asks ? block_scan<kResizeThreads>(copies, &nth, scratch) : (nth = 0));
+    cluster.sync();   // (and every reference given up is given up)
+    int total = 0, pairs = 0;
+    for (int c = 0; c < kResizeCtas; ++c) {
+        if (c < rank) {
+            begin += s_need[c];
+            nth += s_copies[c];
+        }
+        total += s_need[c];
+        pairs += s_copies[c];
+    }
+    if (rank == 0 && tid == 0) w.header[0] = pairs;
     // the first `total` free pages, by rank
     int found = 0;
     const bool vec = (reinterpret_cast<uintptr_t>(a.ref_count) & 15) == 0;
@@ -325,12 +367,12 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
             for (int i = 0; i < kScanPer / 4; ++i)
                 mask |= ((r[i].x == 0) | (r[i].y == 0) << 1 | (r[i].z == 0) << 2 | (r[i].w == 0) << 3) << (4 * i);
         } else {
+#pragma unroll 4
             for (int i = 0; i < kScanPer; ++i)
                 if (p0 + i < a.num_pages && __ldcg(a.ref_count + p0 + i) == 0) mask |= 1u << i;
         }
         int before;
-        const int mine = block_scan<kResizeThreads>(__popc(mask), &before, scratch);
-        if (tid < kResizeCtas) *cluster.map_shared_rank(&s_count[turn][rank], tid) = mine;
+        tell(s_count[turn], block_scan<kResizeThreads>(__popc(mask), &before, scratch));
         cluster.sync();
         int at = found + before;
         for (int c = 0; c < kResizeCtas; ++c) {
@@ -344,37 +386,50 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
             w.list[at++] = (int)(p0 + i);
         }
     }
-    cluster.sync();
-    for (int b = wid; b < a.B; b += kWarps) {
-        const int nb = __ldcg(w.need + b), rank0 = __ldcg(w.begin + b), pr = __ldcg(w.nth + b);
-        const int keep = __ldcg(w.keep + b), want = __ldcg(w.want + b), next = __ldcg(w.next + b);
-        const bool fits = nb == 0 || (int64_t)rank0 + nb <= found;
+    cluster.sync();   // the list is written, and nobody's shared memory is written any more
+    for (int i = 0; i < per; ++i) {
+        const int b = b0 + i;
+        const Planned q = planned[i * kResizeThreads + tid];
+        const bool fits = q.need == 0 || (int64_t)begin + q.need <= found;
         int32_t* row = a.page_table + (int64_t)b * a.max_pages;
-        if (fits) {
-            const int grow0 = rank0 + (pr >= 0);
-            for (int j = keep + lane; j < want; j += 32) {
-                const int p = __ldcg(w.list + grow0 + j - keep);
-                row[j] = p;
+        const int grow = fits ? q.want - q.keep : 0, from = begin + q.copy;
+        if (grow <= kOwnPages) {
+            for (int j = 0; j < grow; ++j) {
+                const int p = __ldcg(w.list + from + j);
+                row[q.keep + j] = p;
                 a.ref_count[p] = 1;
             }
         }
-        if (lane == 0) {
-            if (pr >= 0) {
+        for (unsigned todo = __ballot_sync(0xffffffffu, grow > kOwnPages); todo != 0; todo &= todo - 1) {
+            const int who = __ffs(todo) - 1;
+            const int g = __shfl_sync(0xffffffffu, grow, who), f = __shfl_sync(0xffffffffu, from, who);
+            int32_t* other = a.page_table + (int64_t)__shfl_sync(0xffffffffu, b, who) * a.max_pages + __shfl_sync(0xffffffffu, q.keep, who);
+#pragma unroll 4
+            for (int j = lane; j < g; j += 32) {
+                const int p = __ldcg(w.list + f + j);
+                other[j] = p;
+                a.ref_count[p] = 1;
+            }
+        }
+        if (b < a.B) {
+            if (q.copy) {
                 int2 move = make_int2(-1, -1);
                 if (fits) {
-                    move = make_int2(__ldcg(w.ask + b), __ldcg(w.list + rank0));
-                    row[next / a.page_size] = move.y;
+                    move = make_int2(__ldcg(w.ask + b), __ldcg(w.list + begin));
+                    row[q.next / a.page_size] = move.y;
                     a.ref_count[move.y] = 1;
                     atomicSub(a.ref_count + move.x, 1);
                 }
-                w.pair[pr] = move;
+                w.pair[nth] = move;
             }
-            if (a.status[b] == SPEC_ST_OK) {
-                a.length[b] = next;
-                a.held[b] = fits ? want : keep;
-                if (!fits) a.status[b] = SPEC_ST_NO_PAGES;
+            a.status[b] = q.status == SPEC_ST_OK && !fits ? SPEC_ST_NO_PAGES : q.status;
+            if (q.status == SPEC_ST_OK) {
+                a.length[b] = q.next;
+                a.held[b] = q.keep + grow;
             }
         }
+        begin += q.need;
+        nth += q.copy;
     }
 }
 
@@ -384,7 +439,7 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyPart = 4096;
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const spec_resize_args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const ResizePlan w = resize_plan(a.workspace, a.B);
+    const ResizeSpace w = resize_space(a.workspace, a.B);
     const int pairs = __ldcg(w.header);
     if (pairs == 0) return;
     const int lane = threadIdx.x & 31;
@@ -421,9 +476,10 @@ __global__ void __launch_bounds__(kForkThreads)
     fork_kernel(const int32_t* src, const int32_t* dst, int n, int B, int page_size, int num_pages, int max_pages,
                 int32_t* page_table, int32_t* held, int32_t* length, int32_t* ref_count, int32_t* status) {
     const int e = blockIdx.x, tid = threadIdx.x;
-    const int s = __ldg(src + e), d = __ldg(dst + e);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = *(src + e), d = *(dst + e);
     bool bad = (unsigned)s >= (unsigned)B || (unsigned)d >= (unsigned)B;
-    for (int o = tid; o < n; o += kForkThreads) bad |= __ldg(src + o) == d || (o < e && __ldg(dst + o) == d);
+    for (int o = tid; o < n; o += kForkThreads) bad |= *(src + o) == d || (o < e && *(dst + o) == d);
     if (__syncthreads_or(bad)) {
         if (tid == 0) status[e] = SPEC_ST_BAD_STREAM;
         return;
@@ -495,13 +551,9 @@ extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
     const int64_t want = (units + 2 * kAppendThreads - 1) / (2 * kAppendThreads);   // two units a thread
     const dim3 grid((unsigned)a->B, (unsigned)(want < 1 ? 1 : want > 64 ? 64 : want));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (vec)
-        append_kernel<uint4><<<grid, kAppendThreads, 0, s>>>(*a, upb);
-    else if (es == 2)
-        append_kernel<unsigned short><<<grid, kAppendThreads, 0, s>>>(*a, upb);
-    else
-        append_kernel<float><<<grid, kAppendThreads, 0, s>>>(*a, upb);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = vec       ? launch_after(append_kernel<uint4>, grid, dim3(kAppendThreads), 0, s, *a, upb)
+                          : es == 2 ? launch_after(append_kernel<unsigned short>, grid, dim3(kAppendThreads), 0, s, *a, upb)
+                                    : launch_after(append_kernel<float>, grid, dim3(kAppendThreads), 0, s, *a, upb);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_append");
 }
 
@@ -530,18 +582,22 @@ extern "C" int spec_cache_resize(const spec_resize_args* a, void* stream) {
                          resize_workspace(a->B, a->num_pages));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a->room == nullptr) {
-        trim_kernel<<<(a->B + kTrimThreads / 32 - 1) / (kTrimThreads / 32), kTrimThreads, 0, s>>>(*a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_after(trim_kernel, dim3((unsigned)((a->B + kTrimThreads - 1) / kTrimThreads)), dim3(kTrimThreads), 0, s, *a);
         return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_resize");
     }
-    resize_kernel<<<kResizeCtas, kResizeThreads, 0, s>>>(*a);
-    cudaError_t e = cudaGetLastError();
+    const int per = (a->B + kResizeCtas * kResizeThreads - 1) / (kResizeCtas * kResizeThreads);
+    const size_t smem = (size_t)per * kResizeThreads * sizeof(Planned);   // up to 192 KB
+    cudaError_t e = cudaSuccess;
+    if (smem > 40000) {
+        e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
+    }
+    e = launch_after(resize_kernel, dim3(kResizeCtas), dim3(kResizeThreads), smem, s, *a, per);
     if (e != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
     // as many CTAs as the largest number of copies (one per stream) can keep busy, two per SM at most
     const int64_t units = (int64_t)a->B * a->layers * 2 * ((a->page_bytes + kCopyPart - 1) / kCopyPart);
     const int64_t ctas = (units + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    copy_pages_kernel<<<(unsigned)(ctas < 608 ? ctas : 608), kCopyThreads, 0, s>>>(*a);
-    e = cudaGetLastError();
+    e = launch_after(copy_pages_kernel, dim3((unsigned)(ctas < 608 ? ctas : 608)), dim3(kCopyThreads), 0, s, *a);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_resize");
 }
 
@@ -558,8 +614,7 @@ extern "C" int spec_cache_fork(const int32_t* src, const int32_t* dst, int32_t n
     if (src == nullptr || dst == nullptr || page_table == nullptr || held == nullptr || length == nullptr ||
         ref_count == nullptr || status == nullptr)
         return set_error(SPEC_ERR_ARG, "spec_cache_fork: a required pointer is NULL");
-    fork_kernel<<<n, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(src, dst, n, B, page_size, num_pages, max_pages,
-                                                                          page_table, held, length, ref_count, status);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(fork_kernel, dim3((unsigned)n), dim3(kForkThreads), 0, static_cast<cudaStream_t>(stream), src, dst, n, B,
+                                       page_size, num_pages, max_pages, page_table, held, length, ref_count, status);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_fork");
 }

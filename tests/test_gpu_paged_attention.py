@@ -213,7 +213,7 @@ def test_runs_are_equal_and_workspaces_can_be_shared():
                  "workspace": first["workspace"]}
         assert torch.equal(call(b, out=other)["out"], alone)
         first["out"].zero_()
-        first["workspace"][16384:].fill_(255)
+        first["workspace"][256:].fill_(255)
         assert torch.equal(call(a, out=first)["out"], want)
 
 
