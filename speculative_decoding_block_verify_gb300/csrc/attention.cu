@@ -281,6 +281,7 @@ struct JoinSum {
 // Many items, so few parts each: CTA (c, y) takes columns of the item that CTA c began.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Unjoined d = p.desc[blockIdx.x];
     const int u = blockIdx.y * kJoinThreads + threadIdx.x;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_spread_kernel(con
     __shared__ float2 s_ml[kJoinThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nc = p.a.D / 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int total = 0;
     {   // prefix sums over the items: two neighbouring ones per thread

@@ -43,10 +43,23 @@ struct TcLayout {
     static constexpr int kBytes = kQBytes + kSlots * kSlotBytes;
 };
 
+// One item's share of a CTA, as the copying warp tells it to the other roles.
+struct Segment {
+    int32_t t0, t1;            // tiles [t0, t1); none: the CTA is done
+    int32_t sink_tiles, first_tile, low, high, sink;   // as in Item
+    int32_t len, r0, rows, head;
+    int32_t whole, slot;       // the whole item, or the slot of its part
+    int64_t row0;              // the block's first packed row
+    __device__ __forceinline__ int start(int t) const { return (t < sink_tiles ? t : first_tile + t - sink_tiles) * kTile; }
+};
+constexpr int kSegments = 4;   // told ahead
+
 struct TcShared {
     uint64_t q_full[2], q_empty[2], o_done[2], drain;
     uint64_t full[10], empty[10];
     uint64_t s_full[2], p_full[2];
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
+    Segment seg[kSegments];
     Start start;
     int64_t scan[kTcThreads / 32];
     int scratch;
@@ -59,6 +72,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], "
         "%6;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int rg, int z, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %2, %2, %3, %4}], "
+        "[%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(rg), "r"(z), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -89,12 +109,16 @@ __device__ __forceinline__ bool warp_wait_for(uint64_t* bar, unsigned parity, in
     return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
 }
 
-// Shared-memory matrix descriptors, 128-byte swizzle: start and strides in units of 16 bytes.
-// K-major (Q, K): 8 rows of 128 bytes are 1,024 bytes, rows 8 further on begin there.  MN-major (V, whose
-// rows are the product's K): `lead` bytes from one 64-column panel to the next.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
+// Shared-memory matrix descriptors, 128-byte swizzle, strides in units of 16 bytes.  K-major (Q, K): 8 rows of 128
+// bytes are an atom of 1,024 bytes, the next 8 rows begin `group` further on.  MN-major (V, whose rows are the
+// product's K): the same atoms, and `panel` from one 64-column panel to the next.  The low word holds the
+// address, so that stepping through an operand is one 32-bit addition.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t panel) { return (addr & 0x3ffff) >> 4 | panel << 16; }
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t group) {
+    const uint32_t hi = group | 1u << 14 | 2u << 29;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
 }
 // kind::f16: float32 accumulator, bf16 operands, M = 128; `mn` = the B operand is MN-major
 constexpr uint32_t mma_desc(int n, bool mn) {
@@ -149,75 +173,108 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* x) {
                  : "memory");
 }
 
-// ---- warp 4: copies -------------------------------------------------------------------
+// How a slot of the ring is laid out: 8-row groups and 64-column panels, in bytes.  A head of whole panels comes with
+// one copy per page, [group][panel][8 rows][128 bytes]; any other width panel by panel (columns past the
+// head read as zeros), [panel][64 rows][128 bytes].
+template <int DP>
+struct SlotLayout {
+    uint32_t group, panel;
+    __device__ __forceinline__ explicit SlotLayout(const AttnParams& p) {
+        const bool pages = p.a.D == DP;
+        group = pages ? DP / 64 * 1024 : 1024;
+        panel = pages ? 1024 : kTile * 128;
+    }
+};
+
+// ---- warp 4: the walk over the CTA's items, and the copies --------------------------------
 template <int DP>
 __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
     const int lane = threadIdx.x & 31;
     const uint32_t q_at = smem_u32(smem), ring = q_at + Lay::kQBytes;
-    Walk w;
-    if (!w.start(p, sh.start)) return;
-    // a lane's share of a tile: one page (or the tile's part of it) and one 64-column panel at a time
-    const int box = min(p.a.page_size, kTile);          // positions of a copy
-    const int pages = kTile / box;                       // copies of a panel
-    int slot = 0;
-    unsigned phase = 1;                                  // a fresh barrier: the phase before its first is done
-    int items = 0;
+    const int box = min(p.a.page_size, kTile);   // positions of a page's copy
+    const int pages = kTile / box;
     const int q_places = p.rows <= kTcRows / 2 ? 2 : 1;
+    const bool by_page = p.a.D == DP;
     // Keys and values that are read once leave L2 first: otherwise they push out the kernel's own code, the tables
-    // and the parts, and every one of those is then a miss to memory.  A block of several groups reads them again.
+    // and the parts, and every one of those is then a miss to memory (the 64-stream verify step: 124 us instead of
+    // 98).  A block of several groups reads them again.
     const uint64_t stay = l2_evict_normal_policy();
     const uint64_t once = (p.a.kmax + 1) * p.G <= p.rows ? l2_evict_first_policy() : stay;
+    Walk w = {};
+    int told = 0, items = 0, slot = 0;
+    unsigned phase = 1;   // a fresh barrier: the phase before its first is done
     bool ok = true;
-    do {
-        const int32_t* table = p.a.page_table + (int64_t)w.b * p.a.max_pages;
-        const int64_t row0 = first_row(p.a.cu_drafts, w.b, p.a.kmax);
-        int next_z = 0;
-        auto look_up = [&](int t) {   // the lane's page of tile t, as the map's third coordinate
-            const int j = tile_start(w.it, t) + (lane % pages) * box;
-            const int end = j + box;
-            int page = -1;
-            if (j < w.it.high && (end > w.it.low || j < w.it.sink)) page = *(table + (j >> p.page_shift));
-            // past the last page: zeros
-            next_z = (unsigned)page < (unsigned)p.a.num_pages ? page * p.a.Hkv + w.h : p.a.num_pages * p.a.Hkv;
-        };
-        look_up(w.t0);
-        for (int t = w.t0; t < w.t1 && ok; ++t) {
-            const int z = next_z;
-            const int y = tile_start(w.it, t) & (p.a.page_size - 1) & ~(box - 1);
-            if (t + 1 < w.t1) look_up(t + 1);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                ok = warp_wait_for(&sh.empty[slot], phase, &sh.abort);
-                if (!ok) break;
-                if (lane == 0) mbar_expect_tx(&sh.full[slot], Lay::kSlotBytes);
-                __syncwarp();
-                const uint32_t to = ring + slot * Lay::kSlotBytes;
-                for (int u = lane; u < pages * Lay::kHalves; u += 32) {
-                    const int half = u / pages;   // u % pages = lane % pages: 32 is a multiple of pages
-                    tma_load_3d(to + half * (kTile * 128) + (lane % pages) * box * 128, kv ? vmap : kmap, half * 64,
-                                pages > 1 ? 0 : y, z, &sh.full[slot], once);
-                }
-                if (++slot == Lay::kSlots) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+    auto tell = [&](bool any) {   // the next segment, or that there is none
+        Segment& seg = sh.seg[told % kSegments];
+        ok = ok && warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort);
+        if (ok && lane == 0) {
+            if (any) {
+                const int64_t row0 = first_row(p.a.cu_drafts, w.b, p.a.kmax);
+                seg = {w.t0, w.t1, w.it.sink_tiles, w.it.first_tile, w.it.low, w.it.high, w.it.sink, w.len, w.it.r0, w.it.r1 - w.it.r0, w.h,
+                       w.whole(), w.slot(blockIdx.x), row0};
+                if (w.begins_part()) p.desc[blockIdx.x] = w.unjoined(p, blockIdx.x, sh.start.span);
+            } else {
+                seg.t0 = seg.t1 = 0;
             }
-            if (t == w.t0 && ok) {
-                // the item's rows of Q, behind its first keys: they wait for the last user of their place
-                const int at = items % q_places;
-                ok = warp_wait_for(&sh.q_empty[at], ((items / q_places) & 1) ^ 1, &sh.abort);
-                if (ok && lane == 0) {
-                    mbar_expect_tx(&sh.q_full[at], Lay::kHalves * p.rows * 128);
-                    for (int half = 0; half < Lay::kHalves; ++half)
-                        tma_load_3d(q_at + half * (kTcRows * 128) + at * kQPlace, qmap, half * 64, w.h * p.G,
-                                    (int)row0 + w.it.r0 / p.G, &sh.q_full[at], stay);
-                }
-                ++items;
-            }
+            mbar_arrive(&sh.seg_full[told % kSegments]);
         }
-    } while (ok && w.next(p));
+        ++told;
+    };
+    auto look_up = [&](int t) {   // lane i: page i of tile t, as the map's last coordinate (past the last page: zeros)
+        const int j = tile_start(w.it, t) + (lane % pages) * box;
+        int page = -1;
+        if (j < w.it.high && (j + box > w.it.low || j < w.it.sink))
+            page = p.a.page_table[(int64_t)w.b * p.a.max_pages + (j >> p.page_shift)];
+        return (unsigned)page < (unsigned)p.a.num_pages ? page * p.a.Hkv + w.h : p.a.num_pages * p.a.Hkv;
+    };
+    auto copy = [&](const CUtensorMap* map, int z, int y) {   // one tile of K or V into the next slot
+        ok = ok && warp_wait_for(&sh.empty[slot], phase, &sh.abort);
+        if (!ok) return;
+        const uint32_t to = ring + slot * Lay::kSlotBytes;
+        if (lane == 0) mbar_expect_tx(&sh.full[slot], Lay::kSlotBytes);
+        __syncwarp();
+        if (by_page) {   // a lane per page
+            if (lane < pages) tma_load_5d(to + lane * box * Lay::kHalves * 128, map, y >> 3, z, &sh.full[slot], once);
+        } else if (lane < pages) {
+            for (int half = 0; half < Lay::kHalves; ++half)
+                tma_load_3d(to + half * (kTile * 128) + lane * box * 128, map, half * 64, y, z, &sh.full[slot], once);
+        }
+        if (++slot == Lay::kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    bool more = w.start(p, sh.start);
+    tell(more);
+    int t = more ? w.t0 : 0;
+    int z = more ? look_up(t) : 0;
+    while (more && ok) {
+        const int y = pages > 1 ? 0 : tile_start(w.it, t) & (p.a.page_size - 1);
+        copy(kmap, z, y);
+        if (t == w.t0 && ok) {
+            // the item's rows of Q, behind its first keys: they wait for the last user of their place
+            const int at = items % q_places;
+            ok = warp_wait_for(&sh.q_empty[at], ((items / q_places) & 1) ^ 1, &sh.abort);
+            if (ok && lane == 0) {
+                const int row = (int)first_row(p.a.cu_drafts, w.b, p.a.kmax) + w.it.r0 / p.G;
+                mbar_expect_tx(&sh.q_full[at], Lay::kHalves * p.rows * 128);
+                for (int half = 0; half < Lay::kHalves; ++half)
+                    tma_load_3d(q_at + half * (kTcRows * 128) + at * kQPlace, qmap, half * 64, w.h * p.G, row, &sh.q_full[at], stay);
+            }
+            ++items;
+        }
+        // the tile after this one, and its pages, before its slot is waited for
+        const int z_now = z;
+        if (++t == w.t1) {
+            more = w.next(p);
+            tell(more);
+            t = w.t0;
+        }
+        if (more) z = look_up(t);
+        copy(vmap, z_now, y);
+    }
     if (!ok) {   // gave up: whatever was copied must have arrived before the CTA's memory is given back
         for (int s = 0; s < Lay::kSlots; ++s)
             for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
@@ -226,85 +283,112 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     }
 }
 
-// ---- warp 5, one thread: products ------------------------------------------------------
+// ---- warp 5: products ------------------------------------------------------------------
 // Whichever product has its operands first: S of tile n (its keys, the item's Q, and P of tile n - 2, whose
-// place S takes, used up) or O += P V of tile n (P, and the tile's values).
+// place S takes, used up) or O += P V of tile n (P, and the tile's values).  The whole warp runs the loop, on votes, so
+// that descriptors and addresses are uniform; one lane issues.
+__device__ __forceinline__ bool all_test(uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); }
+__device__ __forceinline__ bool elected() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
 template <int DP>
 __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
+    const SlotLayout<DP> lay(p);
+    const uint32_t group = lay.group >> 4, panel = lay.panel >> 4;
     const uint32_t q_at = smem_u32(smem), ring = q_at + Lay::kQBytes;
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = __reduce_or_sync(0xffffffffu, sh.tmem);
     const int ksteps = (p.a.D + 15) / 16;
     const int q_places = p.rows <= kTcRows / 2 ? 2 : 1;
     // a negative scale is a negated Q (bit 13) and its magnitude
     const uint32_t qk = mma_desc(kTile, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t pv = mma_desc(DP, true);
-    Walk w;   // of the S products
-    if (!w.start(p, sh.start)) return;
-    int t = w.t0, items = 0;
-    bool more = true;
+    int items = 0, left = 0;       // of the S products: items begun, tiles of the present one not yet issued
+    int q = 0;                     // the present item's place of Q
+    unsigned q_phase = 0;
+    bool first = false, done = false;
     unsigned n_qk = 0, n_pv = 0;   // products issued
     unsigned firsts = 0;           // bit (tile & 1): the tile is its item's first
     int kslot = 0, vslot = 1;
     unsigned kphase = 0, vphase = 0;
-    auto step = [](int& slot, unsigned& phase) {
-        slot += 2;
-        if (slot >= Lay::kSlots) {
-            slot -= Lay::kSlots;
-            phase ^= 1;
-        }
-    };
     int spins = 0;
-    while (more || n_pv != n_qk) {
+    while (!done || n_pv != n_qk) {
         bool did = false;
         if (n_pv != n_qk) {
             const unsigned buf = n_pv & 1;
-            if (mbar_test(&sh.p_full[buf], (n_pv >> 1) & 1) && mbar_test(&sh.full[vslot], vphase)) {
+            if (all_test(&sh.p_full[buf], (n_pv >> 1) & 1) && all_test(&sh.full[vslot], vphase)) {
                 tc_fence_after();
-                const bool first = (firsts >> buf) & 1;
-                const uint32_t v_at = ring + vslot * Lay::kSlotBytes;
+                const bool begin = (firsts >> buf) & 1;
+                const uint32_t v = desc_lo(ring + vslot * Lay::kSlotBytes, panel);
+                if (elected()) {
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, smem_desc(v_at + k * 2048, kTile * 128), pv,
-                           !(first && k == 0));
-                mma_commit(&sh.o_done[buf]);
-                mma_commit(&sh.empty[vslot]);
-                step(vslot, vphase);
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, desc(v + 2 * k * group, group), pv, !(begin && k == 0));
+                    mma_commit(&sh.o_done[buf]);
+                    mma_commit(&sh.empty[vslot]);
+                }
+                __syncwarp();
+                vslot += 2;
+                if (vslot >= Lay::kSlots) {
+                    vslot -= Lay::kSlots;
+                    vphase ^= 1;
+                }
                 ++n_pv;
                 did = true;
             }
         }
-        if (more && n_qk - n_pv < 2) {
+        if (left == 0 && !done) {   // the next item
+            const int at = items % kSegments;
+            if (all_test(&sh.seg_full[at], (items / kSegments) & 1)) {
+                left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+                if (elected()) mbar_arrive(&sh.seg_empty[at]);
+                __syncwarp();
+                done = left == 0;
+                first = true;
+                q = items % q_places;
+                q_phase = (items / q_places) & 1;
+                ++items;
+                did = true;
+            }
+        }
+        if (left > 0 && n_qk - n_pv < 2) {
             const unsigned buf = n_qk & 1;
-            const int q = items % q_places;
-            if ((n_qk < 2 || mbar_test(&sh.o_done[buf], ((n_qk >> 1) - 1) & 1)) && mbar_test(&sh.full[kslot], kphase) &&
-                (t != w.t0 || mbar_test(&sh.q_full[q], (items / q_places) & 1))) {
+            if ((n_qk < 2 || all_test(&sh.o_done[buf], ((n_qk >> 1) - 1) & 1)) && all_test(&sh.full[kslot], kphase) &&
+                (!first || all_test(&sh.q_full[q], q_phase))) {
                 tc_fence_after();
-                firsts = (firsts & ~(1u << buf)) | (unsigned)(t == w.t0) << buf;
-                const uint32_t k_at = ring + kslot * Lay::kSlotBytes;
-                for (int k = 0; k < ksteps; ++k) {
-                    const int half = k >> 2, in = (k & 3) * 32;
-                    mma_ss(tmem + buf * kTile, smem_desc(q_at + half * (kTcRows * 128) + q * kQPlace + in, 16),
-                           smem_desc(k_at + half * (kTile * 128) + in, 16), qk, k > 0);
+                firsts = (firsts & ~(1u << buf)) | (unsigned)first << buf;
+                first = false;
+                --left;
+                const uint32_t a = desc_lo(q_at + q * kQPlace, 1), b = desc_lo(ring + kslot * Lay::kSlotBytes, 1);
+                if (elected()) {
+#pragma unroll
+                    for (int k = 0; k < Lay::kHalves * 4; ++k)
+                        if (k < ksteps)
+                            mma_ss(tmem + buf * kTile, desc(a + (k >> 2) * (kTcRows * 128 >> 4) + (k & 3) * 2, 1024 >> 4),
+                                   desc(b + (k >> 2) * panel + (k & 3) * 2, group), qk, k > 0);
+                    mma_commit(&sh.s_full[buf]);
+                    mma_commit(&sh.empty[kslot]);
+                    if (left == 0) mma_commit(&sh.q_empty[q]);
                 }
-                mma_commit(&sh.s_full[buf]);
-                mma_commit(&sh.empty[kslot]);
-                step(kslot, kphase);
+                __syncwarp();
+                kslot += 2;
+                if (kslot >= Lay::kSlots) {
+                    kslot -= Lay::kSlots;
+                    kphase ^= 1;
+                }
                 ++n_qk;
-                if (++t == w.t1) {
-                    mma_commit(&sh.q_empty[q]);
-                    ++items;
-                    more = w.next(p);
-                    t = w.t0;
-                }
                 did = true;
             }
         }
         spins = did ? 0 : spins + 1;
         if (spins > kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        if (spins > 0 && *reinterpret_cast<volatile int*>(&sh.abort)) {
-            mma_commit(&sh.drain);
-            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.drain, 0); ++n) {}
+        if (spins > 0 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
+            if (elected()) mma_commit(&sh.drain);
+            __syncwarp();
+            for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}
             return;
         }
     }
@@ -312,28 +396,39 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
 
 // ---- warps 0 to 3: softmax, scaling, output ---------------------------------------------
 template <int DP>
-__device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, TcShared& sh, int cta) {
+__device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
+    const SlotLayout<DP> lay(p);
     char* ring = smem + Lay::kQBytes;
-    Walk w;
-    if (!w.start(p, sh.start)) return;
+    const bool wide = (((uint32_t)reinterpret_cast<uintptr_t>(p.a.out) | p.a.D * 2) & 31) == 0;   // 32-byte stores
     unsigned t_all = 0;   // tiles of the CTA so far
     int vslot = 1;
     unsigned vphase = 0;
     bool ok = true;
-    do {
-        const int rows = w.it.r1 - w.it.r0;
-        const int token = (w.it.r0 + min(tid, rows - 1)) / p.G;
+    for (int n_seg = 0;; ++n_seg) {
+        const int seg_at = n_seg % kSegments;
+        ok = warp_wait_for(&sh.seg_full[seg_at], (n_seg / kSegments) & 1, &sh.abort);
+        if (!ok) break;
+        const Segment w = sh.seg[seg_at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[seg_at]);
+        if (w.t0 == w.t1) break;
+        const int rows = w.rows;
+        const int rr = w.r0 + min(tid, rows - 1), token = rr / p.G;
         const int at = w.len + token;                                        // the row's position
         const int low = p.a.window > 0 ? at + 1 - p.a.window : 0;            // ... sees [low, at] and [0, sinks)
-        const int at_first = w.len + w.it.r0 / p.G;
+        const int at_first = w.len + w.r0 / p.G, at_last = w.len + (w.r0 + rows - 1) / p.G;
         const bool work = warp * 32 < rows;                                  // any row in this warp
+        const bool mine = tid < rows;
+        unsigned short* const to = reinterpret_cast<unsigned short*>(p.a.out) +
+                                   ((w.row0 + token) * p.a.Hq + w.head * p.G + rr - token * p.G) * (int64_t)p.a.D;
+        float4* const part = p.part + (int64_t)w.slot * (p.a.D / 4) * p.rows + tid;
         float m = -kInf, l = 0.f;
         for (int t = w.t0; t < w.t1; ++t, ++t_all) {
             const unsigned buf = t_all & 1;
-            const int j0 = tile_start(w.it, t);
+            const int j0 = w.start(t);
             ok = warp_wait_for(&sh.s_full[buf], (t_all >> 1) & 1, &sh.abort);
             if (!ok) break;
             float scale_o = 1.f;
@@ -345,7 +440,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 tc_wait_ld();
                 // a tile that every row sees whole needs no mask
                 const bool clean = j0 + kTile - 1 <= at_first &&
-                                   (p.a.window <= 0 || j0 >= w.len + (w.it.r1 - 1) / p.G + 1 - p.a.window || j0 + kTile <= p.a.sinks);
+                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
                 if (!clean) {
                     const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll
@@ -357,7 +452,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 for (int c = 0; c < kTile; c += 2)   // three-way maxima
                     x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
                 const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;   // the scale is positive here
-                if (tid < rows && top > m + 8.f) {   // lanes without a row never ask for the scaling of O
+                if (mine && top > m + 8.f) {   // lanes without a row never ask for the scaling of O
                     scale_o = m == -kInf ? 0.f : ex2(m - top);
                     m = top;
                     l *= scale_o;
@@ -377,14 +472,15 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 tmem_st32(lanes + buf * kTile, pk);
             }
             // V of positions that no row of the item sees: zeros, whatever the cache holds there
-            if (j0 + kTile > w.it.high || (j0 < w.it.low && j0 + kTile > w.it.sink)) {
+            if (j0 + kTile > w.high || (j0 < w.low && j0 + kTile > w.sink)) {
                 ok = warp_wait_for(&sh.full[vslot], vphase, &sh.abort);
                 if (!ok) break;
                 char* v = ring + vslot * Lay::kSlotBytes;
                 for (int u = tid; u < Lay::kHalves * kTile * 8; u += 128) {
-                    const int j = j0 + ((u >> 3) & (kTile - 1));
-                    if (j >= w.it.high || (j < w.it.low && j >= w.it.sink))
-                        *reinterpret_cast<uint4*>(v + u * 16) = make_uint4(0, 0, 0, 0);
+                    const int row = (u >> 3) & (kTile - 1), j = j0 + row;
+                    if (j >= w.high || (j < w.low && j >= w.sink))
+                        *reinterpret_cast<uint4*>(v + (row >> 3) * lay.group + (u / (kTile * 8)) * lay.panel + (row & 7) * 128 + (u & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
@@ -393,12 +489,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 vslot -= Lay::kSlots;
                 vphase ^= 1;
             }
-            if (t_all > 0) {   // the product before has to be done before O is scaled, or begun anew
-                ok = warp_wait_for(&sh.o_done[buf ^ 1], ((t_all - 1) >> 1) & 1, &sh.abort);
-                if (!ok) break;
-            }
             if (work) {
                 if (t > w.t0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
+                    // the product before has to be done before O is scaled.  (Looked for only here and at the item's end: S of
+                    // this tile was issued behind the product two tiles back, so the barrier is at most one phase ahead.)
+                    ok = warp_wait_for(&sh.o_done[buf ^ 1], ((t_all - 1) >> 1) & 1, &sh.abort);
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
@@ -418,25 +514,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
         }
         ok = ok && warp_wait_for(&sh.o_done[(t_all - 1) & 1], ((t_all - 1) >> 1) & 1, &sh.abort);
         if (!ok) break;
-        const bool whole = w.whole();
-        if (tid == 0 && w.begins_part()) p.desc[cta] = w.unjoined(p, cta, sh.start.span);
         if (work) {
             tc_fence_after();
-            const bool mine = tid < rows;
-            const int rr = w.it.r0 + tid;
-            unsigned short* to = reinterpret_cast<unsigned short*>(p.a.out) +
-                                 ((first_row(p.a.cu_drafts, w.b, p.a.kmax) + token) * p.a.Hq + w.h * p.G + rr - token * p.G) * (int64_t)p.a.D;
-            const bool wide = (((uint32_t)reinterpret_cast<uintptr_t>(p.a.out) | p.a.D * 2) & 31) == 0;
-            const int64_t slot = w.slot(cta);
             const float inv = 1.f / l;
-            if (mine && !whole) __stcg(p.ml + slot * p.rows + tid, make_float2(m, l));
+            if (mine && !w.whole) __stcg(p.ml + (int64_t)w.slot * p.rows + tid, make_float2(m, l));
 #pragma unroll 1
             for (int c0 = 0; c0 < p.a.D; c0 += 32) {
                 uint32_t o[32];
                 __syncwarp();
                 tmem_ld32(lanes + Lay::kOCol + c0, o);
                 tc_wait_ld();
-                if (mine && whole) {
+                if (mine && w.whole) {
                     uint32_t x[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2)
@@ -456,7 +544,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
                         if (c0 + c >= p.a.D) break;
-                        __stcg(p.part + (slot * (p.a.D / 4) + (c0 + c) / 4) * p.rows + tid,
+                        __stcg(part + (c0 + c) / 4 * p.rows,
                                make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
                                            __uint_as_float(o[c + 3])));
                     }
@@ -465,7 +553,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
             __syncwarp();
             tc_fence_before();
         }
-    } while (w.next(p));
+    }
 }
 
 template <int DP>
@@ -500,6 +588,10 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 4);
         }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_empty[i], 5);   // the products' thread and four warps
+        }
         mbar_init_fence();
         sh.abort = 0;
     }
@@ -514,10 +606,9 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
         write_status<unsigned short>(p, cta, sh.start.valid);   // while the last tiles are computed
     } else if (warp == 5) {
-        if ((tid & 31) == 0) mma_role<DP>(p, smem, sh);
-        __syncwarp();
+        mma_role<DP>(p, smem, sh);
     } else {
-        softmax_role<DP>(p, smem, sh, cta);
+        softmax_role<DP>(p, smem, sh);
     }
     tc_fence_before();
     __syncthreads();
@@ -544,16 +635,35 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// [outer][middle][inner] of bf16 as boxes of 64 inner elements, 128-byte swizzled
-static bool encode3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer, uint64_t middle_stride,
-                    uint64_t outer_stride, uint32_t box_middle, uint32_t box_outer) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {inner, middle, outer}, strides[2] = {middle_stride, outer_stride};
-    const cuuint32_t box[3] = {64, box_middle, box_outer}, elem[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+static bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 f = encoder();
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    return f != nullptr && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, elem,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of Q: [rows][Hq][D] as boxes of 64 columns, a key head's query heads, a group's tokens.
+static bool encode_q(CUtensorMap* map, const void* base, const AttnParams& p, uint64_t stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.a.D, (cuuint64_t)p.a.Hq, (cuuint64_t)(p.a.q_rows > 0 ? p.a.q_rows : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.a.D * 2, stride};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(p.rows / p.G)};
+    return encode(map, base, 3, dims, strides, box);
+}
+
+// A layer's pages: [page and head][position][D].  A head of whole 64-column panels as [page and head][position / 8][panel]
+// [position % 8][64], a page (or 64 positions of one) a box; any other width in boxes of 64 columns.
+static bool encode_pages(CUtensorMap* map, const void* base, const AttnParams& p) {
+    const cuuint64_t D = p.a.D, P = p.a.page_size, heads = (cuuint64_t)p.a.num_pages * p.a.Hkv;
+    const cuuint32_t positions = p.a.page_size < kTile ? p.a.page_size : kTile;
+    if (D % 64 == 0 && D != 192) {
+        const cuuint64_t dims[5] = {64, 8, D / 64, P / 8, heads}, strides[4] = {D * 2, 128, 8 * D * 2, P * D * 2};
+        const cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64), positions / 8, 1};
+        return encode(map, base, 5, dims, strides, box);
+    }
+    const cuuint64_t dims[3] = {D, P, heads}, strides[2] = {D * 2, P * D * 2};
+    const cuuint32_t box[3] = {64, positions, 1};
+    return encode(map, base, 3, dims, strides, box);
 }
 
 template <int DP>
@@ -584,6 +694,7 @@ bool tensor_q(const spec_attention_args* a) { return (((uintptr_t)a->q | (uintpt
 // Rows of Q that do not lie on 16-byte boundaries, packed so that they do.
 __global__ void __launch_bounds__(256) pack_rows_kernel(const unsigned short* q, int64_t stride, int width, uint4* to) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const unsigned short* from = q + blockIdx.x * stride;
     for (int c = threadIdx.x; c < width / 8; c += 256) {
         uint32_t x[4];
@@ -613,11 +724,7 @@ cudaError_t launch_attention_tc(const AttnParams& p, void* q_packed, cudaStream_
         q_stride = (uint64_t)a.Hq * a.D * 2;
     }
     CUtensorMap map[3];
-    const uint64_t D = a.D, P = a.page_size;
-    const uint32_t box = a.page_size < kTile ? a.page_size : kTile;
-    if (!encode3(&map[0], q, D, a.Hq, (uint64_t)(a.q_rows > 0 ? a.q_rows : 1), D * 2, q_stride, p.G, p.rows / p.G) ||
-        !encode3(&map[1], a.k_pages, D, P, (uint64_t)a.num_pages * a.Hkv, D * 2, P * D * 2, box, 1) ||
-        !encode3(&map[2], a.v_pages, D, P, (uint64_t)a.num_pages * a.Hkv, D * 2, P * D * 2, box, 1))
+    if (!encode_q(&map[0], q, p, q_stride) || !encode_pages(&map[1], a.k_pages, p) || !encode_pages(&map[2], a.v_pages, p))
         return cudaErrorInvalidValue;
     if (a.D <= 64) return launch_tc<64>(p, map, s);
     if (a.D <= 128) return launch_tc<128>(p, map, s);

@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
     __shared__ int s_page[SPEC_MAX_KMAX + 1];
     __shared__ int s_bad;
     const int b = blockIdx.x, tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = __ldcg(a.length + b);
     if (tid == 0) s_bad = 0;
@@ -218,6 +219,7 @@ __device__ __forceinline__ void drop_pages(const spec_resize_args& a, int b, int
 constexpr int kTrimThreads = 64;
 __global__ void __launch_bounds__(kTrimThreads) trim_kernel(const spec_resize_args a) {
     const int b = blockIdx.x * kTrimThreads + threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const StreamPlan s = plan_stream(a, b);
     drop_pages(a, b, s.keep, s.held);
@@ -438,6 +440,7 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPart = 4096;
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const spec_resize_args a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ResizeSpace w = resize_space(a.workspace, a.B);
     const int pairs = __ldcg(w.header);
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(kForkThreads)
     fork_kernel(const int32_t* src, const int32_t* dst, int n, int B, int page_size, int num_pages, int max_pages,
                 int32_t* page_table, int32_t* held, int32_t* length, int32_t* ref_count, int32_t* status) {
     const int e = blockIdx.x, tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int s = *(src + e), d = *(dst + e);
     bool bad = (unsigned)s >= (unsigned)B || (unsigned)d >= (unsigned)B;
