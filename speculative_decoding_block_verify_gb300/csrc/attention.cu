@@ -15,7 +15,7 @@
 namespace sv {
 
 // ---------------------------------------------------------------------------------------
-// The kernel on the float pipes: float32 caches.
+// The kernel on the float pipes: float32 heads of more than 128.
 // ---------------------------------------------------------------------------------------
 // 256 threads: TK along the keys (then along the columns of the values), 256 / TK along the rows;
 // a thread owns RM rows and 64 / TK keys of a tile.  Q, K, V tiles and the weights are in shared memory, rows padded by
@@ -390,12 +390,14 @@ static int sm_count(int* sms) {
     return SPEC_OK;
 }
 
+constexpr int kTensorF32 = 128;   // float32 heads up to here go to the tensor cores
+
 // Rows of a group and CTAs of the grid.
 static void cut(const spec_attention_args* a, int sms, int* rows, int* ctas) {
     const int64_t need = (int64_t)(a->kmax + 1) * (a->Hq / a->Hkv);
-    const bool tensor = a->dtype == SPEC_DTYPE_BF16;
+    const bool bf16 = a->dtype == SPEC_DTYPE_BF16, tensor = bf16 || a->D <= kTensorF32;
     *rows = tensor ? tensor_rows(a) : need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-    int64_t n = (tensor ? tensor_ctas_per_sm(a) : *rows < 64 ? 2 : 1) * (int64_t)sms;   // as many as are resident
+    int64_t n = (bf16 ? tensor_ctas_per_sm(a) : !tensor && *rows < 64 ? 2 : 1) * (int64_t)sms;   // as many as are resident
     // no more CTAs than the longest possible contexts have tiles
     const int64_t groups = (need + *rows - 1) / *rows;
     const int64_t tiles = groups * a->B * a->Hkv * (((int64_t)a->max_pages * a->page_size + kTile - 1) / kTile);
@@ -462,19 +464,11 @@ static cudaError_t launch_float(const AttnParams& p, cudaStream_t s, bool q_vec)
     return launch_after(attention_float_kernel<R, TK, ND>, dim3(p.ctas), dim3(kFloatThreads), smem, s, p, (int)q_vec);
 }
 
-template <int R, int TK>
-static cudaError_t launch_float_d(const AttnParams& p, cudaStream_t s, bool q_vec) {
-    const int nd = (p.a.D / 4 + TK - 1) / TK;
-    if (nd == 1) return launch_float<R, TK, 1>(p, s, q_vec);
-    if (nd == 2) return launch_float<R, TK, 2>(p, s, q_vec);
-    return launch_float<R, TK, 64 / TK>(p, s, q_vec);
-}
-
 static cudaError_t launch_float_r(const AttnParams& p, cudaStream_t s, bool q_vec) {
-    if (p.rows == 8) return launch_float_d<8, 32>(p, s, q_vec);
-    if (p.rows == 16) return launch_float_d<16, 16>(p, s, q_vec);
-    if (p.rows == 32) return launch_float_d<32, 16>(p, s, q_vec);
-    return launch_float_d<64, 16>(p, s, q_vec);
+    if (p.rows == 8) return launch_float<8, 32, 2>(p, s, q_vec);
+    if (p.rows == 16) return launch_float<16, 16, 4>(p, s, q_vec);
+    if (p.rows == 32) return launch_float<32, 16, 4>(p, s, q_vec);
+    return launch_float<64, 16, 4>(p, s, q_vec);
 }
 
 template <typename T>
@@ -538,17 +532,17 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     p.page_shift = 0;
     while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
     p.scale_log2 = (float)((double)a->scale * kLog2e);
+    // the tensor-core kernels negate Q for a negative scale, and multiply masked scores of -inf by it
+    if (a->dtype == SPEC_DTYPE_BF16 || a->D <= kTensorF32) p.scale_log2 = a->scale == 0.f ? 1e-30f : std::fabs(p.scale_log2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (a->dtype == SPEC_DTYPE_BF16) {
-        // the tensor-core kernel negates Q for a negative scale, and multiplies masked scores of -inf by it
-        p.scale_log2 = a->scale == 0.f ? 1e-30f : std::fabs(p.scale_log2);
         p.item_cost = 2;
         e = launch_attention_tc(p, q_packed, s);
         if (e == cudaSuccess) e = launch_join<unsigned short>(p, sms, s);
     } else {
         p.item_cost = 1;
-        e = launch_float_r(p, s, (((uintptr_t)a->q | (uintptr_t)(a->q_row_stride * 4)) & 15) == 0);
+        e = a->D <= kTensorF32 ? launch_attention_f32(p, s) : launch_float_r(p, s, (((uintptr_t)a->q | (uintptr_t)(a->q_row_stride * 4)) & 15) == 0);
         if (e == cudaSuccess) e = launch_join<float>(p, sms, s);
     }
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_paged_attention");

@@ -294,5 +294,7 @@ int tensor_rows(const spec_attention_args* a);          // rows of a group
 int tensor_ctas_per_sm(const spec_attention_args* a);
 bool tensor_q(const spec_attention_args* a);            // q's rows can be copied as they lie
 cudaError_t launch_attention_tc(const AttnParams& p, void* q_packed, cudaStream_t s);
+// ... for float32 heads up to 128 (attention_f32.cu); same groups, one CTA an SM.
+cudaError_t launch_attention_f32(const AttnParams& p, cudaStream_t s);
 
 }  // namespace sv
