@@ -115,12 +115,30 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
         }
         ++told;
     };
-    auto look_up = [&](int t) {   // lane i: page i of tile t, as the map's last coordinate (past the last page: zeros)
-        const int j = tile_start(w.it, t) + (lane % pages) * box;
+    // One load of the warp looks up the pages of several tiles: lane i has page i % pages of tile t + i / pages, as the map's last
+    // coordinate (past the last page: zeros).  The next tiles' load is on its way while these are copied.
+    const int per = 32 / pages;
+    int z_now = 0, z_next = 0, z_base = 0;
+    auto look_up = [&](int t) {
+        const int tile = t + lane / pages;
+        const int j = tile_start(w.it, tile) + (lane % pages) * box;
         int page = -1;
-        if (j < w.it.high && (j + box > w.it.low || j < w.it.sink))
+        if (tile < w.t1 && j < w.it.high && (j + box > w.it.low || j < w.it.sink))
             page = p.a.page_table[(int64_t)w.b * p.a.max_pages + (j >> p.page_shift)];
         return (unsigned)page < (unsigned)p.a.num_pages ? page * p.a.Hkv + w.h : p.a.num_pages * p.a.Hkv;
+    };
+    auto begin_look_up = [&](int t) {
+        z_base = t;
+        z_now = look_up(t);
+        z_next = t + per < w.t1 ? look_up(t + per) : 0;
+    };
+    auto pages_of = [&](int t) {
+        if (t - z_base == per) {
+            z_base = t;
+            z_now = z_next;
+            if (t + per < w.t1) z_next = look_up(t + per);
+        }
+        return __shfl_sync(0xffffffffu, z_now, (t - z_base) * pages + lane % pages);
     };
     auto copy = [&](const CUtensorMap* map, int z, int y) {   // one tile of K or V into the next slot
         ok = ok && warp_wait_for(&sh.empty[slot], phase, &sh.abort);
@@ -142,8 +160,9 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     bool more = w.start(p, sh.start);
     tell(more);
     int t = more ? w.t0 : 0;
-    int z = more ? look_up(t) : 0;
+    if (more) begin_look_up(t);
     while (more && ok) {
+        const int z = pages_of(t);
         const int y = pages > 1 ? 0 : tile_start(w.it, t) & (p.a.page_size - 1);
         copy(kmap, z, y);
         if (t == w.t0 && ok) {
@@ -158,15 +177,14 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
             }
             ++items;
         }
-        // the tile after this one, and its pages, before its slot is waited for
-        const int z_now = z;
+        // the next item and its first pages, before the last values' slot is waited for
         if (++t == w.t1) {
             more = w.next(p);
             tell(more);
             t = w.t0;
+            if (more) begin_look_up(t);
         }
-        if (more) z = look_up(t);
-        copy(vmap, z_now, y);
+        copy(vmap, z, y);
     }
     if (!ok) {   // gave up: whatever was copied must have arrived before the CTA's memory is given back
         for (int s = 0; s < Lay::kSlots; ++s)
