@@ -6,10 +6,12 @@
 // product.  At M = 128 a tile of 64 positions costs 6 x 512 = 3,072 tensor cycles against about 2,800 that its
 // 64 KB take from memory; on the float pipes 32 rows alone take 8,192.
 //
-// One CTA per SM, ten warps: copies (warp 8) bring pages as they lie, 256 bytes to the page row, into a ring; four
-// warps (4 to 7) split keys and values into swizzled bf16 planes (zeros where no row of the item sees a position,
-// whatever the cache holds there) and the item's rows of Q into tensor memory; warp 9 issues the products; warps 0 to
-// 3 hold a row per thread: softmax, P split into three planes in tensor memory, scaling of O, output.
+// One CTA per SM, fourteen warps: copies (warp 12) bring pages as they lie into a ring; warps 4 to 7 split the keys and
+// warps 8 to 11 the values into swizzled bf16 planes (zeros where no row of the item sees a position, whatever the
+// cache holds there), the latter also the item's rows of Q into tensor memory; warp 13 issues the products; warps 0
+// to 3 hold a row per thread: softmax, P split into three planes in tensor memory, scaling of O, output.  There is
+// one set of planes each for keys and values: a tile's keys are split during the product of the values before,
+// and its values during its keys' product, so the tensor cores do not wait for either.
 // An infinite key or value counts as NaN here (the difference to its rounding is).
 
 #include <atomic>
@@ -19,7 +21,7 @@
 
 namespace sv {
 
-constexpr int kF32Threads = 320;
+constexpr int kF32Threads = 448;
 constexpr int kPlanes = 3;
 constexpr int kTerms = 6;   // (plane of A, plane of B), the largest last
 __host__ __device__ constexpr int term_a(int i) { return i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0; }
@@ -61,7 +63,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[kPlanes]) 
     w[2] = pack_bf16(x, y);
 }
 
-// ---- warp 8: the walk over the CTA's items, and the copies --------------------------------
+// ---- warp 12: the walk over the CTA's items, and the copies --------------------------------
 template <int DP>
 __device__ __forceinline__ void f32_copy_role(const AttnParams& p, char* raw, F32Shared& sh) {
     using Lay = F32Layout<DP>;
@@ -130,17 +132,20 @@ __device__ __forceinline__ void f32_copy_role(const AttnParams& p, char* raw, F3
             for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.raw_full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
 }
 
-// ---- warps 4 to 7: float32 into planes -----------------------------------------------------
-template <int DP>
+// ---- warps 4 to 7 (keys) and 8 to 11 (values, and Q): float32 into planes ------------------
+template <int DP, int KV>
 __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes, char* raw, F32Shared& sh) {
     using Lay = F32Layout<DP>;
-    const int tid = threadIdx.x - 128, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
     constexpr int kChunks = DP / 8;   // of a row, eight columns each
     const int chunk = tid % kChunks, row0 = tid / kChunks;
     const int box_shift = min(p.page_shift, 6);
     const bool q_vec = ((reinterpret_cast<uintptr_t>(p.a.q) | (uintptr_t)(p.a.q_row_stride * 4)) & 15) == 0;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
-    int slot = 0;
+    uint64_t* const full = KV ? &sh.v_full : &sh.k_full;
+    uint64_t* const empty = KV ? &sh.v_empty : &sh.k_empty;
+    char* const to = planes + KV * kPlanes * Lay::kPlane + (chunk >> 3) * (kTile * 128);
+    int slot = KV;   // keys and values alternate in the ring
     unsigned phase = 0, n_tile = 0;
     for (int n_seg = 0;; ++n_seg) {
         const int seg_at = n_seg % kSegments;
@@ -149,10 +154,10 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[seg_at]);
         if (w.t0 == w.t1) return;
-        // the item's rows of Q: a thread its row, once the item before is through with its own
-        if (!warp_wait_for(&sh.q_empty, (n_seg & 1) ^ 1, &sh.abort)) return;
-        tc_fence_after();
-        {
+        if (KV == 1) {
+            // the item's rows of Q: a thread its row, once the item before is through with its own
+            if (!warp_wait_for(&sh.q_empty, (n_seg & 1) ^ 1, &sh.abort)) return;
+            tc_fence_after();
             const int rr = w.r0 + min(tid, w.rows - 1), token = rr / p.G;
             const float* q = reinterpret_cast<const float*>(p.a.q) + (w.row0 + token) * p.a.q_row_stride +
                              (int64_t)(w.head * p.G + rr - token * p.G) * p.a.D;
@@ -186,55 +191,50 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
         }
         for (int t = w.t0; t < w.t1; ++t, ++n_tile) {
             const int j0 = w.start(t);
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                if (!warp_wait_for(&sh.raw_full[slot], phase, &sh.abort)) return;
-                const int there = sh.there[slot];
-                if (!warp_wait_for(kv ? &sh.v_empty : &sh.k_empty, (n_tile & 1) ^ 1, &sh.abort)) return;
-                const char* from = raw + slot * Lay::kRaw;
-                char* to = planes + kv * kPlanes * Lay::kPlane + (chunk >> 3) * (kTile * 128);
-#pragma unroll 2
-                for (int r = row0; r < kTile; r += 128 / kChunks) {
-                    const int j = j0 + r;
-                    uint32_t x[kPlanes][4];
-                    if (chunk * 8 < p.a.D && j < w.high && (j >= w.low || j < w.sink) && (there >> (r >> box_shift)) & 1) {
-                        const float4* y = reinterpret_cast<const float4*>(from + (r * p.a.D + chunk * 8) * 4);
-                        const float4 a = y[0], b = y[1];
-                        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t u[kPlanes];
-                            split(f[2 * c], f[2 * c + 1], u);
-#pragma unroll
-                            for (int i = 0; i < kPlanes; ++i) x[i][c] = u[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kPlanes; ++i)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) x[i][c] = 0;
-                    }
-                    char* at = to + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);   // the 128-byte swizzle
-#pragma unroll
-                    for (int i = 0; i < kPlanes; ++i)
-                        *reinterpret_cast<uint4*>(at + i * Lay::kPlane) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            if (!warp_wait_for(&sh.raw_full[slot], phase, &sh.abort)) return;
+            const int there = sh.there[slot];
+            if (!warp_wait_for(empty, (n_tile & 1) ^ 1, &sh.abort)) return;
+            const char* from = raw + slot * Lay::kRaw;
+#pragma unroll 4
+            for (int r = row0; r < kTile; r += 128 / kChunks) {
+                const int j = j0 + r;
+                uint32_t x[kPlanes][4];
+                const bool seen = chunk * 8 < p.a.D && j < w.high && (j >= w.low || j < w.sink) && (there >> (r >> box_shift)) & 1;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                if (seen) {
+                    const float4* y = reinterpret_cast<const float4*>(from + (r * p.a.D + chunk * 8) * 4);
+                    a = y[0];
+                    b = y[1];
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(kv ? &sh.v_full : &sh.k_full);
-                    mbar_arrive(&sh.raw_empty[slot]);
+                const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t u[kPlanes];
+                    split(f[2 * c], f[2 * c + 1], u);
+#pragma unroll
+                    for (int i = 0; i < kPlanes; ++i) x[i][c] = u[i];
                 }
-                if (++slot == Lay::kRaws) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                char* at = to + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);   // the 128-byte swizzle
+#pragma unroll
+                for (int i = 0; i < kPlanes; ++i)
+                    *reinterpret_cast<uint4*>(at + i * Lay::kPlane) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full);
+                mbar_arrive(&sh.raw_empty[slot]);
+            }
+            slot += 2;
+            if (slot >= Lay::kRaws) {
+                slot -= Lay::kRaws;
+                phase ^= 1;
             }
         }
     }
 }
 
-// ---- warp 9: products ------------------------------------------------------------------
+// ---- warp 13: products ------------------------------------------------------------------
 template <int DP>
 __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, F32Shared& sh) {
     using Lay = F32Layout<DP>;
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     char* const raw = smem + 2 * kPlanes * Lay::kPlane;
     F32Shared& sh = *reinterpret_cast<F32Shared*>(smem + Lay::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
-    if (warp == 9) {
+    if (warp == 13) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"((uint32_t)Lay::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
         for (int i = 0; i < 6; ++i) mbar_init(one[i], 1);
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 9);
+            mbar_init(&sh.seg_empty[i], 13);   // twelve warps and the products'
         }
         mbar_init_fence();
         sh.abort = 0;
@@ -479,19 +479,21 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) {
+    if (warp == 12) {
         f32_copy_role<DP>(p, raw, sh);
         write_status<float>(p, cta, sh.start.valid);
-    } else if (warp == 9) {
+    } else if (warp == 13) {
         f32_mma_role<DP>(p, planes, sh);
+    } else if (warp >= 8) {
+        f32_split_role<DP, 1>(p, planes, raw, sh);
     } else if (warp >= 4) {
-        f32_split_role<DP>(p, planes, raw, sh);
+        f32_split_role<DP, 0>(p, planes, raw, sh);
     } else {
         f32_softmax_role<DP>(p, sh);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"((uint32_t)Lay::kCols));
     }
