@@ -43,6 +43,7 @@ __all__ = [
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
 DIAG_COLS = 8
+MAX_DRAFTS = 32
 STATUS_NAMES = {0: "OK", 1: "BAD_TEMPERATURE", 2: "BAD_TOKEN", 3: "BAD_ROW",
                 4: "ZERO_DRAFT_PROB", 5: "BAD_OFFSETS", 6: "TIMEOUT", 7: "NUMERIC",
                 8: "NO_PAGES", 9: "BAD_LENGTH", 10: "BAD_PAGE", 11: "BAD_STREAM"}
