@@ -12,6 +12,9 @@
 // to 3 hold a row per thread: softmax, P split into three planes in tensor memory, scaling of O, output.  There is
 // one set of planes each for keys and values: a tile's keys are split during the product of the values before,
 // and its values during its keys' product, so the tensor cores do not wait for either.
+// The tensor cores cut their running sums off instead of rounding them: over 5,000 positions in one accumulator the output
+// came out 1.7e-5 too small.  So every tile's P V is a product of its own, and the sums over tiles are rounded float32
+// additions in shared memory: 6e-7 off there, a third of what a float32 matrix product is, at the same speed.
 // An infinite key or value counts as NaN here (the difference to its rounding is).
 
 #include <atomic>
@@ -32,8 +35,9 @@ template <int DP>
 struct F32Layout {
     static constexpr int kPlane = DP / 64 * kTile * 128;          // one plane of 64 positions, [panel][64 rows][128 bytes]
     static constexpr int kRaw = kTile * DP * 4;                    // a tile as it lies
-    static constexpr int kRaws = DP == 128 ? 4 : 8;
-    static constexpr int kBytes = 2 * kPlanes * kPlane + kRaws * kRaw;
+    static constexpr int kRaws = DP == 128 ? 2 : 8;
+    static constexpr int kSums = kTcRows * DP * 4;                 // O of the tiles so far, [D / 4][row]
+    static constexpr int kBytes = 2 * kPlanes * kPlane + kRaws * kRaw + kSums;
     // columns of tensor memory
     static constexpr int kQ = 0, kS = 192, kP = 256, kO = 384, kCols = 512;
 };
@@ -245,7 +249,7 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
     constexpr uint32_t pv = mma_desc(DP, true);
     int items = 0, left = 0;
     bool first = false, done = false;
-    unsigned n_qk = 0, n_pv = 0, firsts = 0;
+    unsigned n_qk = 0, n_pv = 0;
     int spins = 0;
     while (!done || n_pv != n_qk) {
         bool did = false;
@@ -265,7 +269,6 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
         if (left > 0 && n_qk - n_pv < 2 && all_test(&sh.k_full, n_qk & 1) && (n_qk == 0 || all_test(&sh.s_empty, (n_qk - 1) & 1)) &&
             (!first || all_test(&sh.q_full, (items - 1) & 1))) {
             tc_fence_after();
-            firsts = (firsts & ~(1u << (n_qk & 1))) | (unsigned)first << (n_qk & 1);
             first = false;
             --left;
             if (elected()) {
@@ -288,14 +291,13 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
         }
         if (n_pv != n_qk && all_test(&sh.p_full, n_pv & 1) && all_test(&sh.v_full, n_pv & 1)) {
             tc_fence_after();
-            const bool begin = (firsts >> (n_pv & 1)) & 1;
             if (elected()) {
 #pragma unroll
                 for (int term = 0; term < kTerms; ++term) {
                     const uint32_t a = tmem + Lay::kP + term_a(term) * 32, b = v_at + term_b(term) * (Lay::kPlane >> 4);
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, !begin || term > 0 || k > 0);
+                        mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, term > 0 || k > 0);
                 }
                 mma_commit(&sh.o_done);
                 mma_commit(&sh.v_empty);
@@ -317,7 +319,7 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
 
 // ---- warps 0 to 3: softmax, scaling, output ---------------------------------------------
 template <int DP>
-__device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared& sh) {
+__device__ __forceinline__ void f32_softmax_role(const AttnParams& p, float4* sums, F32Shared& sh) {
     using Lay = F32Layout<DP>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
@@ -336,6 +338,7 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
         const int at_first = w.len + w.r0 / p.G, at_last = w.len + (w.r0 + rows - 1) / p.G;
         const bool work = warp * 32 < rows, mine = tid < rows;
         float m = -kInf, l = 0.f;
+        float before = 1.f;   // scale of the sums so far, from the tile before to this one
         for (int t = w.t0; t < w.t1; ++t, ++n) {
             const int j0 = w.start(t);
             if (!warp_wait_for(&sh.s_full, n & 1, &sh.abort)) return;
@@ -395,17 +398,26 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
 #pragma unroll
                     for (int i = 0; i < kPlanes; ++i) tmem_st16(lanes + Lay::kP + i * 32 + c0 / 2, pk[i]);
                 }
-                if (t > w.t0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
+                if (t > w.t0) {   // O of the tile before joins the sums (scaled to its maximum), or begins them
+                    const bool more = t - w.t0 > 1;
 #pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(lanes + Lay::kO + c, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale_o);
-                        tmem_st32(lanes + Lay::kO + c, o);
+                        for (int i = 0; i < 32; i += 4) {
+                            float4* at = sums + (c + i) / 4 * kTcRows + tid;
+                            float4 x = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                            if (more) {
+                                const float4 y = *at;
+                                x = make_float4(fmaf(y.x, before, x.x), fmaf(y.y, before, x.y), fmaf(y.z, before, x.z), fmaf(y.w, before, x.w));
+                            }
+                            *at = x;
+                        }
                     }
                 }
+                before = scale_o;
                 tc_wait_st();
                 tc_fence_before();
             }
@@ -419,6 +431,7 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
             float4* const part = p.part + (int64_t)w.slot * (p.a.D / 4) * p.rows + tid;
             const float inv = 1.f / l;
             if (mine && !w.whole) __stcg(p.ml + (int64_t)w.slot * p.rows + tid, make_float2(m, l));
+            const bool summed = w.t1 - w.t0 > 1;
 #pragma unroll 1
             for (int c0 = 0; c0 < p.a.D; c0 += 32) {
                 uint32_t o[32];
@@ -430,6 +443,10 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
                     for (int c = 0; c < 32; c += 4) {
                         if (c0 + c >= p.a.D) break;
                         float4 x = make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]), __uint_as_float(o[c + 3]));
+                        if (summed) {
+                            const float4 y = sums[(c0 + c) / 4 * kTcRows + tid];
+                            x = make_float4(fmaf(y.x, before, x.x), fmaf(y.y, before, x.y), fmaf(y.z, before, x.z), fmaf(y.w, before, x.w));
+                        }
                         if (w.whole)
                             put4(to + c0 + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
                         else
@@ -449,6 +466,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     extern __shared__ __align__(1024) char smem[];
     char* const planes = smem;
     char* const raw = smem + 2 * kPlanes * Lay::kPlane;
+    float4* const sums = reinterpret_cast<float4*>(raw + Lay::kRaws * Lay::kRaw);
     F32Shared& sh = *reinterpret_cast<F32Shared*>(smem + Lay::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
     if (warp == 13) {
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     } else if (warp >= 4) {
         f32_split_role<DP, 0>(p, planes, raw, sh);
     } else {
-        f32_softmax_role<DP>(p, sh);
+        f32_softmax_role<DP>(p, sums, sh);
     }
     tc_fence_before();
     __syncthreads();
