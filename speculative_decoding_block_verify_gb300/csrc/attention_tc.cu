@@ -216,6 +216,8 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
     bool first = false, done = false;
     unsigned n_qk = 0, n_pv = 0;   // products issued
     unsigned firsts = 0;           // bit (tile & 1): the tile is its item's first
+    int seen_tile = 0, seen_high = 0, seen_low = 0, seen_sink = 0, seen_sinks = 0, seen_first = 0;   // the item of the S products
+    int hide_from[2] = {kTile, kTile}, hide_low[2] = {0, 0}, hide_sink[2] = {0, 0};   // of tile n: rows from hide_from on, and [hide_sink, hide_low)
     int kslot = 0, vslot = 1;
     unsigned kphase = 0, vphase = 0;
     int spins = 0;
@@ -226,6 +228,20 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
             if (all_test(&sh.p_full[buf], (n_pv >> 1) & 1) && all_test(&sh.full[vslot], vphase)) {
                 tc_fence_after();
                 const bool begin = (firsts >> buf) & 1;
+                const int from = buf ? hide_from[1] : hide_from[0], low = buf ? hide_low[1] : hide_low[0], sink = buf ? hide_sink[1] : hide_sink[0];
+                if (from < kTile || sink < low) {
+                    // values of positions that no row of the item sees: zeros, whatever the cache holds there
+                    char* const at = smem + Lay::kQBytes + vslot * Lay::kSlotBytes;
+                    constexpr int kChunks = Lay::kHalves * 8;   // 16 bytes each, of a row
+                    for (int u = threadIdx.x & 31; u < kTile * kChunks; u += 32) {
+                        const int row = u / kChunks, c = u % kChunks;
+                        if (row >= from || (row >= sink && row < low))
+                            *reinterpret_cast<uint4*>(at + (row >> 3) * lay.group + (c >> 3) * lay.panel + (row & 7) * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
                 const uint32_t v = desc_lo(ring + vslot * Lay::kSlotBytes, panel);
                 if (elected()) {
 #pragma unroll
@@ -247,7 +263,15 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
         if (left == 0 && !done) {   // the next item
             const int at = items % kSegments;
             if (all_test(&sh.seg_full[at], (items / kSegments) & 1)) {
-                left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+                const Segment& seg = sh.seg[at];
+                left = __reduce_max_sync(0xffffffffu, seg.t1 - seg.t0);
+                seen_tile = seg.t0;
+                seen_high = seg.high;
+                seen_low = seg.low;
+                seen_sink = seg.sink;
+                seen_sinks = seg.sink_tiles;
+                seen_first = seg.first_tile;
+                __syncwarp();
                 if (elected()) mbar_arrive(&sh.seg_empty[at]);
                 __syncwarp();
                 done = left == 0;
@@ -266,6 +290,18 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
                 firsts = (firsts & ~(1u << buf)) | (unsigned)first << buf;
                 first = false;
                 --left;
+                const int j0 = (seen_tile < seen_sinks ? seen_tile : seen_first + seen_tile - seen_sinks) * kTile;
+                ++seen_tile;
+                const int from = min(kTile, seen_high - j0), low = min(kTile, max(0, seen_low - j0)), sink = max(0, seen_sink - j0);
+                if (buf) {
+                    hide_from[1] = from;
+                    hide_low[1] = low;
+                    hide_sink[1] = sink;
+                } else {
+                    hide_from[0] = from;
+                    hide_low[0] = low;
+                    hide_sink[0] = sink;
+                }
                 const uint32_t a = desc_lo(q_at + q * kQPlace, 1), b = desc_lo(ring + kslot * Lay::kSlotBytes, 1);
                 if (elected()) {
 #pragma unroll
@@ -300,16 +336,12 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
 
 // ---- warps 0 to 3: softmax, scaling, output ---------------------------------------------
 template <int DP>
-__device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, TcShared& sh) {
+__device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) {
     using Lay = TcLayout<DP>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
-    const SlotLayout<DP> lay(p);
-    char* ring = smem + Lay::kQBytes;
     const bool wide = (((uint32_t)reinterpret_cast<uintptr_t>(p.a.out) | p.a.D * 2) & 31) == 0;   // 32-byte stores
     unsigned t_all = 0;   // tiles of the CTA so far
-    int vslot = 1;
-    unsigned vphase = 0;
     bool ok = true;
     for (int n_seg = 0;; ++n_seg) {
         const int seg_at = n_seg % kSegments;
@@ -374,24 +406,6 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, char* smem, Tc
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 __syncwarp();
                 tmem_st32(lanes + buf * kTile, pk);
-            }
-            // V of positions that no row of the item sees: zeros, whatever the cache holds there
-            if (j0 + kTile > w.high || (j0 < w.low && j0 + kTile > w.sink)) {
-                ok = warp_wait_for(&sh.full[vslot], vphase, &sh.abort);
-                if (!ok) break;
-                char* v = ring + vslot * Lay::kSlotBytes;
-                for (int u = tid; u < Lay::kHalves * kTile * 8; u += 128) {
-                    const int row = (u >> 3) & (kTile - 1), j = j0 + row;
-                    if (j >= w.high || (j < w.low && j >= w.sink))
-                        *reinterpret_cast<uint4*>(v + (row >> 3) * lay.group + (u / (kTile * 8)) * lay.panel + (row & 7) * 128 + (u & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-            }
-            vslot += 2;
-            if (vslot >= Lay::kSlots) {
-                vslot -= Lay::kSlots;
-                vphase ^= 1;
             }
             if (work) {
                 if (t > w.t0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
     } else if (warp == 5) {
         mma_role<DP>(p, smem, sh);
     } else {
-        softmax_role<DP>(p, smem, sh);
+        softmax_role<DP>(p, sh);
     }
     tc_fence_before();
     __syncthreads();
