@@ -441,7 +441,7 @@ void spec_cost_curve_destroy(void* curve);
 
 /*
  * The paged key-value cache.  A verify step scores N_b + 1 slots per stream in one pass of the
- * target ([P1] §3 "One pass, N slots"): the block of stream b is the last emitted token and its
+ * target ([P1] "One pass, N slots"): the block of stream b is the last emitted token and its
  * N_b drafts, at positions length[b] .. length[b] + N_b.  The pass writes the block's keys and
  * values behind the stream's cached ones (spec_cache_append) and attends over all of them
  * (spec_paged_attention), layer by layer; the verify call then keeps the first n_emitted[b] of

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
             const int r = u / nd4, c = (u - r * nd4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
-                const int rr = w.it.r0 + r, i = rr / p.G;
+                const int rr = w.it.r0 + r, i = p.by_G.of(rr);
                 const float* from = q + (row0 + i) * p.a.q_row_stride + (int64_t)(w.h * p.G + rr - i * p.G) * D + c;
                 x = q_vec ? *reinterpret_cast<const float4*>(from)
                           : make_float4(*(from), *(from + 1), *(from + 2), *(from + 3));
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
         for (int a = 0; a < RM; ++a) {
             m[a] = -kInf;
             l[a] = 0.f;
-            at[a] = w.len + (w.it.r0 + min(tr + a * TR, rows - 1)) / p.G;
+            at[a] = w.len + p.by_G.of(w.it.r0 + min(tr + a * TR, rows - 1));
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[a][d] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
             const int r = tr + a * TR;
             if (r >= rows) continue;
             if (whole) {
-                const int rr = w.it.r0 + r, i = rr / p.G;
+                const int rr = w.it.r0 + r, i = p.by_G.of(rr);
                 float* to = reinterpret_cast<float*>(p.a.out) + ((row0 + i) * p.a.Hq + w.h * p.G + rr - i * p.G) * (int64_t)D;
                 const float inv = 1.f / l[a];
 #pragma unroll
@@ -271,7 +271,7 @@ struct JoinSum {
     }
     template <typename T>
     __device__ __forceinline__ void write(const AttnParams& p, const Unjoined& d, int r, int col) const {
-        const int rr = d.r0 + r, token = rr / p.G;
+        const int rr = d.r0 + r, token = p.by_G.of(rr);
         T* out = reinterpret_cast<T*>(p.a.out) + ((d.row0 + token) * p.a.Hq + d.head * p.G + rr - token * p.G) * (int64_t)p.a.D + 4 * col;
         const float inv = 1.f / sum;
         put4(out, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -529,6 +529,8 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     layout(a, p.rows, p.ctas, &p, &q_packed);
     p.a = *a;
     p.G = a->Hq / a->Hkv;
+    p.by_G = divisor(p.G);
+    p.by_rows = divisor(p.rows);
     p.page_shift = 0;
     while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
     p.scale_log2 = (float)((double)a->scale * kLog2e);

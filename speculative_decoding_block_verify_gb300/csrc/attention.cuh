@@ -25,12 +25,21 @@ struct __align__(16) Unjoined {
     int64_t pad;
 };
 
+// Division by a number fixed for the call: the quotient is the high word of a product with 2^32 / d, rounded up (exact while
+// n * d < 2^32; a runtime division is about 150 cycles of dependent instructions).
+struct Divisor {
+    uint32_t d, magic;   // magic 0: d is 1
+    __device__ __forceinline__ int of(int n) const { return magic ? (int)__umulhi((uint32_t)n, magic) : n; }
+};
+inline Divisor divisor(int d) { return {(uint32_t)d, d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u}; }
+
 struct AttnParams {
     spec_attention_args a;
     int G;            // query heads per key head
     int rows;         // rows of a full group
     int ctas;         // CTAs of the grid
     int page_shift;
+    Divisor by_G, by_rows;
     int item_cost;    // what beginning and ending an item takes, in tiles
     float scale_log2; // scale * log2(e)
     // workspace
@@ -51,7 +60,7 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int len, int bloc
     Item it;
     it.r0 = group * p.rows;
     it.r1 = min(it.r0 + p.rows, block_rows * p.G);
-    const int i0 = it.r0 / p.G, i1 = (it.r1 - 1) / p.G;
+    const int i0 = p.by_G.of(it.r0), i1 = p.by_G.of(it.r1 - 1);
     it.high = len + i1 + 1;
     it.low = p.a.window > 0 ? max(0, len + i0 + 1 - p.a.window) : 0;
     it.sink = min(p.a.sinks, it.low);
@@ -69,7 +78,7 @@ __device__ __forceinline__ bool length_ok(const AttnParams& p, int len, int n) {
     return len >= 0 && (int64_t)len + n <= (int64_t)p.a.max_pages << p.page_shift;
 }
 
-__device__ __forceinline__ int block_groups(const AttnParams& p, int n) { return (n * p.G + p.rows - 1) / p.rows; }
+__device__ __forceinline__ int block_groups(const AttnParams& p, int n) { return p.by_rows.of(n * p.G + p.rows - 1); }
 
 // Length on the line of one key head of a stream (0 where its length is not in its table row).
 __device__ __forceinline__ int64_t head_cost(const AttnParams& p, int len, int n) {

@@ -162,7 +162,7 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
             // the item's rows of Q: a thread its row, once the item before is through with its own
             if (!warp_wait_for(&sh.q_empty, (n_seg & 1) ^ 1, &sh.abort)) return;
             tc_fence_after();
-            const int rr = w.r0 + min(tid, w.rows - 1), token = rr / p.G;
+            const int rr = w.r0 + min(tid, w.rows - 1), token = p.by_G.of(rr);
             const float* q = reinterpret_cast<const float*>(p.a.q) + (w.row0 + token) * p.a.q_row_stride +
                              (int64_t)(w.head * p.G + rr - token * p.G) * p.a.D;
 #pragma unroll 1
@@ -332,10 +332,10 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, float4* su
         if (lane == 0) mbar_arrive(&sh.seg_empty[seg_at]);
         if (w.t0 == w.t1) return;
         const int rows = w.rows;
-        const int rr = w.r0 + min(tid, rows - 1), token = rr / p.G;
+        const int rr = w.r0 + min(tid, rows - 1), token = p.by_G.of(rr);
         const int at = w.len + token;
         const int low = p.a.window > 0 ? at + 1 - p.a.window : 0;
-        const int at_first = w.len + w.r0 / p.G, at_last = w.len + (w.r0 + rows - 1) / p.G;
+        const int at_first = w.len + p.by_G.of(w.r0), at_last = w.len + p.by_G.of(w.r0 + rows - 1);
         const bool work = warp * 32 < rows, mine = tid < rows;
         float m = -kInf, l = 0.f;
         float before = 1.f;   // scale of the sums so far, from the tile before to this one

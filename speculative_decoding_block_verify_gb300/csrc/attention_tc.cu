@@ -170,7 +170,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
             const int at = items % q_places;
             ok = warp_wait_for(&sh.q_empty[at], ((items / q_places) & 1) ^ 1, &sh.abort);
             if (ok && lane == 0) {
-                const int row = (int)first_row(p.a.cu_drafts, w.b, p.a.kmax) + w.it.r0 / p.G;
+                const int row = (int)first_row(p.a.cu_drafts, w.b, p.a.kmax) + p.by_G.of(w.it.r0);
                 mbar_expect_tx(&sh.q_full[at], Lay::kHalves * p.rows * 128);
                 for (int half = 0; half < Lay::kHalves; ++half)
                     tma_load_3d(q_at + half * (kTcRows * 128) + at * kQPlace, qmap, half * 64, w.h * p.G, row, &sh.q_full[at], stay);
@@ -352,10 +352,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) 
         if (lane == 0) mbar_arrive(&sh.seg_empty[seg_at]);
         if (w.t0 == w.t1) break;
         const int rows = w.rows;
-        const int rr = w.r0 + min(tid, rows - 1), token = rr / p.G;
+        const int rr = w.r0 + min(tid, rows - 1), token = p.by_G.of(rr);
         const int at = w.len + token;                                        // the row's position
         const int low = p.a.window > 0 ? at + 1 - p.a.window : 0;            // ... sees [low, at] and [0, sinks)
-        const int at_first = w.len + w.r0 / p.G, at_last = w.len + (w.r0 + rows - 1) / p.G;
+        const int at_first = w.len + p.by_G.of(w.r0), at_last = w.len + p.by_G.of(w.r0 + rows - 1);
         const bool work = warp * 32 < rows;                                  // any row in this warp
         const bool mine = tid < rows;
         unsigned short* const to = reinterpret_cast<unsigned short*>(p.a.out) +
@@ -437,18 +437,19 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) 
             const float inv = 1.f / l;
             if (mine && !w.whole) __stcg(p.ml + (int64_t)w.slot * p.rows + tid, make_float2(m, l));
 #pragma unroll 1
-            for (int c0 = 0; c0 < p.a.D; c0 += 32) {
-                uint32_t o[32];
+            for (int c0 = 0; c0 < p.a.D; c0 += 64) {
+                uint32_t o[64];
                 __syncwarp();
                 tmem_ld32(lanes + Lay::kOCol + c0, o);
+                tmem_ld32(lanes + Lay::kOCol + c0 + 32, o + 32);
                 tc_wait_ld();
                 if (mine && w.whole) {
-                    uint32_t x[16];
+                    uint32_t x[32];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2)
+                    for (int c = 0; c < 64; c += 2)
                         x[c / 2] = pack_bf16(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 16) {
+                    for (int c = 0; c < 64; c += 16) {
                         if (wide && c0 + c < p.a.D) {
                             store32(to + c0 + c, x + c / 2);
                         } else {
@@ -460,7 +461,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) 
                     }
                 } else if (mine) {   // neighbouring rows are neighbours in memory
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
+                    for (int c = 0; c < 64; c += 4) {
                         if (c0 + c >= p.a.D) break;
                         __stcg(part + (c0 + c) / 4 * p.rows,
                                make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
