@@ -307,8 +307,8 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
             did = true;
         }
         spins = did ? 0 : spins + 1;
-        if (spins > kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        if (spins > 0 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
+        if (spins == kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+        if ((spins & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
             if (elected()) mma_commit(&sh.drain);
             __syncwarp();
             for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}

@@ -324,8 +324,8 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
             }
         }
         spins = did ? 0 : spins + 1;
-        if (spins > kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        if (spins > 0 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
+        if (spins == kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+        if ((spins & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
             if (elected()) mma_commit(&sh.drain);
             __syncwarp();
             for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}
