@@ -3,18 +3,27 @@
 // A float32 is the sum of three bf16: x = x0 + x1 + x2 + O(2^-27 |x|), each the rounding of what the ones before
 // leave.  A product of two such sums needs the six terms x0 y0, x0 y1, x1 y0, x1 y1, x0 y2, x2 y0 (the other three are
 // below 2^-24 of x0 y0), each exact in float32, so six bf16 products with a float32 accumulator stand for a float32
-// product.  At M = 128 a tile of 64 positions costs 6 x 512 = 3,072 tensor cycles against about 2,800 that its
-// 64 KB take from memory; on the float pipes 32 rows alone take 8,192.
+// product.  At M = 128 a tile of 64 positions costs 48 of 32 cycles and 24 of 64, 3,072 tensor cycles, against about 2,800
+// that its 64 KB take from memory; on the float pipes 32 rows alone take 8,192.
 //
-// One CTA per SM, fourteen warps: copies (warp 12) bring pages as they lie into a ring; warps 4 to 7 split the keys and
-// warps 8 to 11 the values into swizzled bf16 planes (zeros where no row of the item sees a position, whatever the
-// cache holds there), the latter also the item's rows of Q into tensor memory; warp 13 issues the products; warps 0
-// to 3 hold a row per thread: softmax, P split into three planes in tensor memory, scaling of O, output.  There is
-// one set of planes each for keys and values: a tile's keys are split during the product of the values before,
+// One CTA per SM, sixteen warps: copies (warp 12) bring pages as they lie into a ring; warps 4 to 11 split the item's rows of
+// Q into tensor memory and keys and values into swizzled bf16 planes (zeros where no row of the item sees a position,
+// whatever the cache holds there); warp 13 issues the products; warps 0 to 3 hold a row per thread: softmax, and P split
+// into three planes in tensor memory.
+// There is one set of planes each for keys and values: a tile's keys are split during the product of the values before,
 // and its values during its keys' product, so the tensor cores do not wait for either.
 // The tensor cores cut their running sums off instead of rounding them: over 5,000 positions in one accumulator the output
 // came out 1.7e-5 too small.  So every tile's P V is a product of its own, and the sums over tiles are rounded float32
-// additions in shared memory: 6e-7 off there, a third of what a float32 matrix product is, at the same speed.
+// additions: 6e-7 off there, a third of what a float32 matrix product is.  Warps 4 to 11 hold them, half of a row per
+// thread in DP / 2 registers, and the softmax hands them its scales through tensor memory.  (Sums in shared memory,
+// added by the softmax's warps, took a third of a tile's time.)
+//
+// What bounds it: a tile takes about 4,700 cycles.  No pipe is full (issue slots a third, tensor cores two thirds); what it
+// waits for is instructions.  Four different pieces of code run on each quarter of an SM, together more than is kept where
+// instructions are fetched from, and every line of it that is not there costs a trip.  What made the code shorter made it
+// faster: one piece of code for keys and values (122 -> 109 us for 16 streams of 2,100 and 5 tokens of 4 rows a key head), a
+// subtraction of bf16 from float32 in one instruction (107 -> 103), waits that look for a given-up one every 16th time
+// (103 -> 101), and products partly unrolled.  The same kernel with keys and values in warps of their own took 123 us.
 // An infinite key or value counts as NaN here (the difference to its rounding is).
 
 #include <atomic>
@@ -24,7 +33,10 @@
 
 namespace sv {
 
-constexpr int kF32Threads = 448;
+constexpr int kF32Threads = 512;
+// registers of a thread: softmax, splitting and sums (two warpgroups), copies and products
+constexpr int kRegsSoftmax = 136, kRegsSplit = 152, kRegsRest = 72, kRegsLaunch = 128;
+static_assert(kRegsSoftmax + 2 * kRegsSplit + kRegsRest <= 4 * kRegsLaunch, "setmaxnreg would wait for ever");
 constexpr int kPlanes = 3;
 constexpr int kTerms = 6;   // (plane of A, plane of B), the largest last
 __host__ __device__ constexpr int term_a(int i) { return i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0; }
@@ -35,17 +47,16 @@ template <int DP>
 struct F32Layout {
     static constexpr int kPlane = DP / 64 * kTile * 128;          // one plane of 64 positions, [panel][64 rows][128 bytes]
     static constexpr int kRaw = kTile * DP * 4;                    // a tile as it lies
-    static constexpr int kRaws = DP == 128 ? 2 : 8;
-    static constexpr int kSums = kTcRows * DP * 4;                 // O of the tiles so far, [D / 4][row]
-    static constexpr int kBytes = 2 * kPlanes * kPlane + kRaws * kRaw + kSums;
-    // columns of tensor memory
-    static constexpr int kQ = 0, kS = 192, kP = 256, kO = 384, kCols = 512;
+    static constexpr int kRaws = DP == 128 ? 4 : 8;
+    static constexpr int kBytes = 2 * kPlanes * kPlane + kRaws * kRaw;
+    // columns of tensor memory; kScale: two tiles' scale, maximum and sum of a row
+    static constexpr int kQ = 0, kS = 192, kP = 256, kScale = 352, kO = 384, kCols = 512;
 };
 
 struct F32Shared {
     uint64_t raw_full[8], raw_empty[8];
-    uint64_t k_full, k_empty, v_full, v_empty;   // the planes
-    uint64_t q_full, q_empty, s_full, s_empty, p_full, o_done, drain;
+    uint64_t k_full, k_empty, v_full;   // the planes; those of V are used up when O is there
+    uint64_t q_full, q_empty, s_full, s_empty, p_full[2], o_done, drain;
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     Segment seg[kSegments];
     int there[8];   // bit i: page i of the slot's tile is in the pool
@@ -56,15 +67,22 @@ struct F32Shared {
     int abort;
 };
 
+// x less the bf16 pair w, exact for the roundings below
+__device__ __forceinline__ float2 less(float2 x, uint32_t w) {
+    float2 y;
+    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b16 m, 0xBF80;\n\tmov.b32 {l, h}, %2;\n\t"   // m: -1
+        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, h, m, %4;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "r"(w), "f"(x.x), "f"(x.y));
+    return y;
+}
 // Two floats as three bf16 pairs.
-__device__ __forceinline__ void split(float x, float y, uint32_t (&w)[kPlanes]) {
-    w[0] = pack_bf16(x, y);
-    x -= bf16_lo(w[0]);
-    y -= bf16_hi(w[0]);
-    w[1] = pack_bf16(x, y);
-    x -= bf16_lo(w[1]);
-    y -= bf16_hi(w[1]);
-    w[2] = pack_bf16(x, y);
+__device__ __forceinline__ void split(float2 x, uint32_t (&w)[kPlanes]) {
+    w[0] = pack_bf16(x.x, x.y);
+    x = less(x, w[0]);
+    w[1] = pack_bf16(x.x, x.y);
+    x = less(x, w[1]);
+    w[2] = pack_bf16(x.x, x.y);
 }
 
 // ---- warp 12: the walk over the CTA's items, and the copies --------------------------------
@@ -136,105 +154,193 @@ __device__ __forceinline__ void f32_copy_role(const AttnParams& p, char* raw, F3
             for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.raw_full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
 }
 
-// ---- warps 4 to 7 (keys) and 8 to 11 (values, and Q): float32 into planes ------------------
-template <int DP, int KV>
+// ---- warps 4 to 11: Q, keys and values into planes, the sums over tiles, output -----------------
+// Each half of them takes half of a tile's positions, of Q's columns and of O's.  Keys go two tiles ahead of values: a tile's
+// planes are free once the product before has used them, and then the other kind's product runs.  When a tile's O is there its
+// planes of V are used up too; what an item's last tile has completed is written while the next item is computed.
+// Keys and values share one piece of code: unrolled twice over it no longer fits where instructions are fetched from.
+template <int DP>
 __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes, char* raw, F32Shared& sh) {
     using Lay = F32Layout<DP>;
-    const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
-    constexpr int kChunks = DP / 8;   // of a row, eight columns each
-    const int chunk = tid % kChunks, row0 = tid / kChunks;
-    const int box_shift = min(p.page_shift, 6);
-    const bool q_vec = ((reinterpret_cast<uintptr_t>(p.a.q) | (uintptr_t)(p.a.q_row_stride * 4)) & 15) == 0;
+    constexpr int kHalf = DP / 2, kChunks = DP / 8;
+    const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5, half = (threadIdx.x >> 7) - 1;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
-    uint64_t* const full = KV ? &sh.v_full : &sh.k_full;
-    uint64_t* const empty = KV ? &sh.v_empty : &sh.k_empty;
-    char* const to = planes + KV * kPlanes * Lay::kPlane + (chunk >> 3) * (kTile * 128);
-    int slot = KV;   // keys and values alternate in the ring
-    unsigned phase = 0, n_tile = 0;
-    for (int n_seg = 0;; ++n_seg) {
-        const int seg_at = n_seg % kSegments;
-        if (!warp_wait_for(&sh.seg_full[seg_at], (n_seg / kSegments) & 1, &sh.abort)) return;
-        const Segment w = sh.seg[seg_at];
+    const int part = tid % kChunks, box_shift = min(p.page_shift, 6);
+    const bool q_vec = ((reinterpret_cast<uintptr_t>(p.a.q) | (uintptr_t)(p.a.q_row_stride * 4)) & 15) == 0;
+    Segment wk = {}, wv = {}, was = {};   // the items of the next key and value tiles, and the one that the last value tile ended
+    int tk = 0, tv = 0, segs_k = 0, segs_v = 0;
+    unsigned nk = 0, nv = 0;              // tiles of the CTA so far
+    bool k_end = false;
+    float2 sum[kHalf / 2];
+#pragma unroll
+    for (int c = 0; c < kHalf / 2; ++c) sum[c] = make_float2(0.f, 0.f);
+    auto next = [&](Segment& w, int& t, int& segs) {
+        const int at = segs % kSegments;
+        if (!warp_wait_for(&sh.seg_full[at], (segs / kSegments) & 1, &sh.abort)) return false;
+        w = sh.seg[at];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.seg_empty[seg_at]);
-        if (w.t0 == w.t1) return;
-        if (KV == 1) {
-            // the item's rows of Q: a thread its row, once the item before is through with its own
-            if (!warp_wait_for(&sh.q_empty, (n_seg & 1) ^ 1, &sh.abort)) return;
-            tc_fence_after();
-            const int rr = w.r0 + min(tid, w.rows - 1), token = p.by_G.of(rr);
-            const float* q = reinterpret_cast<const float*>(p.a.q) + (w.row0 + token) * p.a.q_row_stride +
-                             (int64_t)(w.head * p.G + rr - token * p.G) * p.a.D;
+        if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
+        ++segs;
+        t = w.t0;
+        return true;
+    };
+    for (int kv = 0;; kv ^= 1) {
+        bool write = false, end = false;
+        float m = 0.f, l = 1.f;
+        int j0, high, low, sink;   // of the tile to split
+        unsigned in;
+        if (kv == 0) {
+            if (k_end) continue;
+            if (tk == wk.t1) {
+                if (!next(wk, tk, segs_k)) return;
+                k_end = wk.t0 == wk.t1;
+                if (k_end) continue;
+                // the item's rows of Q: a thread its row, the first columns on their way while the item before still uses its own
+                const int rr = wk.r0 + min(tid, wk.rows - 1), token = p.by_G.of(rr);
+                const float* q = reinterpret_cast<const float*>(p.a.q) + (wk.row0 + token) * p.a.q_row_stride +
+                                 (int64_t)(wk.head * p.G + rr - token * p.G) * p.a.D;
 #pragma unroll 1
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-                uint32_t x[kPlanes][16];
+                for (int c0 = half * kHalf; c0 < (half + 1) * kHalf; c0 += 32) {
+                    float4 y[8];
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c0 + c < p.a.D) {
-                        const float* from = q + c0 + c;
-                        y = q_vec ? *reinterpret_cast<const float4*>(from) : make_float4(from[0], from[1], from[2], from[3]);
+                    for (int c = 0; c < 8; ++c) {
+                        y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (c0 + 4 * c < p.a.D) {
+                            const float* from = q + c0 + 4 * c;
+                            y[c] = q_vec ? *reinterpret_cast<const float4*>(from) : make_float4(from[0], from[1], from[2], from[3]);
+                        }
                     }
-                    uint32_t u[kPlanes], v[kPlanes];
-                    split(y.x, y.y, u);
-                    split(y.z, y.w, v);
+                    if (c0 == half * kHalf) {
+                        if (!warp_wait_for(&sh.q_empty, segs_k & 1, &sh.abort)) return;
+                        tc_fence_after();
+                    }
 #pragma unroll
-                    for (int i = 0; i < kPlanes; ++i) {
-                        x[i][c / 2] = u[i];
-                        x[i][c / 2 + 1] = v[i];
+                    for (int side = 0; side < 2; ++side) {
+                        uint32_t x[kPlanes][8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 f = y[side * 4 + c];
+                            uint32_t u[kPlanes], v[kPlanes];
+                            split(make_float2(f.x, f.y), u);
+                            split(make_float2(f.z, f.w), v);
+#pragma unroll
+                            for (int i = 0; i < kPlanes; ++i) {
+                                x[i][2 * c] = u[i];
+                                x[i][2 * c + 1] = v[i];
+                            }
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < kPlanes; ++i) tmem_st8(lanes + Lay::kQ + i * (DP / 2) + c0 / 2 + side * 8, x[i]);
                     }
                 }
+                tc_wait_st();
+                tc_fence_before();
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kPlanes; ++i) tmem_st16(lanes + Lay::kQ + i * (DP / 2) + c0 / 2, x[i]);
+                if (lane == 0) mbar_arrive(&sh.q_full);
             }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full);
+            j0 = wk.start(tk++);
+            high = wk.high;
+            low = wk.low;
+            sink = wk.sink;
+            in = 2 * nk;   // keys and values alternate in the ring
+        } else {
+            if (nk < 2 && !k_end) continue;
+            const bool first = tv == wv.t1;
+            if (first) {
+                was = wv;
+                if (!next(wv, tv, segs_v)) return;
+            }
+            end = wv.t0 == wv.t1;
+            if (nv > 0) {
+                const unsigned before = nv - 1;
+                if (!warp_wait_for(&sh.p_full[before & 1], (before >> 1) & 1, &sh.abort)) return;   // the row's scale
+                if (!warp_wait_for(&sh.o_done, before & 1, &sh.abort)) return;
+                write = first;
+                if (warp * 32 < (first ? was.rows : wv.rows)) {
+                    tc_fence_after();
+                    uint32_t r[4];
+                    tmem_ld4(lanes + Lay::kScale + (before & 1) * 4, r);
+#pragma unroll
+                    for (int c0 = 0; c0 < kHalf; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + Lay::kO + half * kHalf + c0, o);
+                        tc_wait_ld();
+                        const float2 scale = make_float2(__uint_as_float(r[0]), __uint_as_float(r[0]));
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2)
+                            sum[(c0 + c) / 2] = ffma2(sum[(c0 + c) / 2], scale, make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])));
+                    }
+                    m = __uint_as_float(r[1]);
+                    l = __uint_as_float(r[2]);
+                    tc_fence_before();
+                }
+            }
+            j0 = wv.start(tv++);
+            high = wv.high;
+            low = wv.low;
+            sink = wv.sink;
+            in = 2 * nv++ + 1;
         }
-        for (int t = w.t0; t < w.t1; ++t, ++n_tile) {
-            const int j0 = w.start(t);
-            if (!warp_wait_for(&sh.raw_full[slot], phase, &sh.abort)) return;
+        if (!end) {
+            const unsigned slot = in % Lay::kRaws;
+            if (!warp_wait_for(&sh.raw_full[slot], (in / Lay::kRaws) & 1, &sh.abort)) return;
+            if (kv == 0 && !warp_wait_for(&sh.k_empty, (nk++ & 1) ^ 1, &sh.abort)) return;
             const int there = sh.there[slot];
-            if (!warp_wait_for(empty, (n_tile & 1) ^ 1, &sh.abort)) return;
-            const char* from = raw + slot * Lay::kRaw;
-#pragma unroll 4
-            for (int r = row0; r < kTile; r += 128 / kChunks) {
-                const int j = j0 + r;
-                uint32_t x[kPlanes][4];
-                const bool seen = chunk * 8 < p.a.D && j < w.high && (j >= w.low || j < w.sink) && (there >> (r >> box_shift)) & 1;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                if (seen) {
-                    const float4* y = reinterpret_cast<const float4*>(from + (r * p.a.D + chunk * 8) * 4);
-                    a = y[0];
-                    b = y[1];
+            const char* const from = raw + slot * Lay::kRaw;
+            char* const to = planes + kv * kPlanes * Lay::kPlane + (part & 1) * 8;
+            // a thread takes columns 4 part and DP / 2 + 4 part on of every kStep-th position of its half: neighbours read neighbours
+            constexpr int kStep = 128 / kChunks;
+#pragma unroll
+            for (int i = 0; i < kTile / 2 / kStep; ++i) {
+                const int r = half * (kTile / 2) + i * kStep + tid / kChunks, j = j0 + r;
+                const bool seen = j < high && (j >= low || j < sink) && (there >> (r >> box_shift)) & 1;
+                const float* const row = reinterpret_cast<const float*>(from) + r * p.a.D + 4 * part;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (seen && side * kHalf + 4 * part < p.a.D) f = *reinterpret_cast<const float4*>(row + side * kHalf);
+                    uint32_t u[kPlanes], v[kPlanes];
+                    split(make_float2(f.x, f.y), u);
+                    split(make_float2(f.z, f.w), v);
+                    // panels of 64 columns, 128 bytes a row, their 16-byte pieces swizzled
+                    const int piece = side * kHalf / 8 + part / 2;
+                    char* const at = to + (piece >> 3) * (kTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+#pragma unroll
+                    for (int k = 0; k < kPlanes; ++k) *reinterpret_cast<uint2*>(at + k * Lay::kPlane) = make_uint2(u[k], v[k]);
                 }
-                const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t u[kPlanes];
-                    split(f[2 * c], f[2 * c + 1], u);
-#pragma unroll
-                    for (int i = 0; i < kPlanes; ++i) x[i][c] = u[i];
-                }
-                char* at = to + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);   // the 128-byte swizzle
-#pragma unroll
-                for (int i = 0; i < kPlanes; ++i)
-                    *reinterpret_cast<uint4*>(at + i * Lay::kPlane) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(full);
+                mbar_arrive(kv ? &sh.v_full : &sh.k_full);   // v_full: and O of the tile before is read
                 mbar_arrive(&sh.raw_empty[slot]);
             }
-            slot += 2;
-            if (slot >= Lay::kRaws) {
-                slot -= Lay::kRaws;
-                phase ^= 1;
-            }
         }
+        if (write) {
+            if (tid < was.rows) {
+                const int rr = was.r0 + tid, token = p.by_G.of(rr);
+                float* const to = reinterpret_cast<float*>(p.a.out) +
+                                  ((was.row0 + token) * p.a.Hq + was.head * p.G + rr - token * p.G) * (int64_t)p.a.D;
+                float4* const unjoined = p.part + (int64_t)was.slot * (p.a.D / 4) * p.rows + tid;
+                const float inv = 1.f / l;
+                if (half == 0 && !was.whole) __stcg(p.ml + (int64_t)was.slot * p.rows + tid, make_float2(m, l));
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 4) {
+                    const int col = half * kHalf + c;
+                    if (col >= p.a.D) break;
+                    const float2 x = sum[c / 2], y = sum[c / 2 + 1];
+                    if (was.whole)
+                        put4(to + col, make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv));
+                    else
+                        __stcg(unjoined + col / 4 * p.rows, make_float4(x.x, x.y, y.x, y.y));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kHalf / 2; ++c) sum[c] = make_float2(0.f, 0.f);
+            __syncwarp();
+        }
+        if (end) return;   // values, and with them the keys, are through
     }
 }
 
@@ -247,68 +353,69 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
     const int ksteps = (p.a.D + 15) / 16;
     const uint32_t qk = mma_desc(kTile, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t pv = mma_desc(DP, true);
+    constexpr int kTermsUnrolled = DP == 64 ? kTerms : 2;   // measured: 1 / 2 / 3 / 6 terms unrolled 101 / 99 / 101 / 106 us, at DP = 64 82 / - / 69 / 69
     int items = 0, left = 0;
-    bool first = false, done = false;
+    bool done = false;
     unsigned n_qk = 0, n_pv = 0;
-    int spins = 0;
-    while (!done || n_pv != n_qk) {
-        bool did = false;
-        if (left == 0 && !done) {
+    // S of a tile, then P V of the tile before: the order in which their operands come
+    auto keys = [&]() {
+        bool first = false;
+        if (left == 0) {
             const int at = items % kSegments;
-            if (all_test(&sh.seg_full[at], (items / kSegments) & 1)) {
-                left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
-                if (elected()) mbar_arrive(&sh.seg_empty[at]);
-                __syncwarp();
-                done = left == 0;
-                first = true;
-                ++items;
-                did = true;
-            }
+            if (!warp_wait_for(&sh.seg_full[at], (items / kSegments) & 1, &sh.abort)) return false;
+            left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+            if (elected()) mbar_arrive(&sh.seg_empty[at]);
+            __syncwarp();
+            done = left == 0;
+            if (done) return true;
+            first = true;
+            ++items;
         }
         // S of tile n goes where S of tile n - 1 was, once that has been read
-        if (left > 0 && n_qk - n_pv < 2 && all_test(&sh.k_full, n_qk & 1) && (n_qk == 0 || all_test(&sh.s_empty, (n_qk - 1) & 1)) &&
-            (!first || all_test(&sh.q_full, (items - 1) & 1))) {
-            tc_fence_after();
-            first = false;
-            --left;
-            if (elected()) {
+        if (n_qk > 0 && !warp_wait_for(&sh.s_empty, (n_qk - 1) & 1, &sh.abort)) return false;
+        if (first && !warp_wait_for(&sh.q_full, (items - 1) & 1, &sh.abort)) return false;
+        if (!warp_wait_for(&sh.k_full, n_qk & 1, &sh.abort)) return false;
+        tc_fence_after();
+        --left;
+        if (elected()) {
+#pragma unroll(kTermsUnrolled)
+            for (int term = 0; term < kTerms; ++term) {
+                const uint32_t a = tmem + Lay::kQ + term_a(term) * (DP / 2), b = k_at + term_b(term) * (Lay::kPlane >> 4);
 #pragma unroll
-                for (int term = 0; term < kTerms; ++term) {
-                    const uint32_t a = tmem + Lay::kQ + term_a(term) * (DP / 2), b = k_at + term_b(term) * (Lay::kPlane >> 4);
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        if (k < ksteps)
-                            mma_ts(tmem + Lay::kS, a + k * 8, desc(b + (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2, 1024 >> 4), qk,
-                                   term > 0 || k > 0);
-                }
-                mma_commit(&sh.s_full);
-                mma_commit(&sh.k_empty);
-                if (left == 0) mma_commit(&sh.q_empty);
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < ksteps)
+                        mma_ts(tmem + Lay::kS, a + k * 8, desc(b + (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2, 1024 >> 4), qk,
+                               term > 0 || k > 0);
             }
-            __syncwarp();
-            ++n_qk;
-            did = true;
+            mma_commit(&sh.s_full);
+            mma_commit(&sh.k_empty);
+            if (left == 0) mma_commit(&sh.q_empty);
         }
-        if (n_pv != n_qk && all_test(&sh.p_full, n_pv & 1) && all_test(&sh.v_full, n_pv & 1)) {
-            tc_fence_after();
-            if (elected()) {
+        __syncwarp();
+        ++n_qk;
+        return true;
+    };
+    auto values = [&]() {
+        if (!warp_wait_for(&sh.v_full, n_pv & 1, &sh.abort) || !warp_wait_for(&sh.p_full[n_pv & 1], (n_pv >> 1) & 1, &sh.abort)) return false;
+        tc_fence_after();
+        if (elected()) {
+#pragma unroll(kTermsUnrolled)
+            for (int term = 0; term < kTerms; ++term) {
+                const uint32_t a = tmem + Lay::kP + term_a(term) * 32, b = v_at + term_b(term) * (Lay::kPlane >> 4);
 #pragma unroll
-                for (int term = 0; term < kTerms; ++term) {
-                    const uint32_t a = tmem + Lay::kP + term_a(term) * 32, b = v_at + term_b(term) * (Lay::kPlane >> 4);
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, term > 0 || k > 0);
-                }
-                mma_commit(&sh.o_done);
-                mma_commit(&sh.v_empty);
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, term > 0 || k > 0);
             }
-            __syncwarp();
-            ++n_pv;
-            did = true;
+            mma_commit(&sh.o_done);
         }
-        spins = did ? 0 : spins + 1;
-        if (spins == kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        if ((spins & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
+        __syncwarp();
+        ++n_pv;
+        return true;
+    };
+    while (!done || n_pv != n_qk) {
+        bool ok = done || keys();
+        if (ok && (done ? n_pv != n_qk : n_qk - n_pv == 2)) ok = values();
+        if (!ok) {   // gave up: what was issued has to end before the CTA's memory is given back
             if (elected()) mma_commit(&sh.drain);
             __syncwarp();
             for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}
@@ -317,9 +424,9 @@ __device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, 
     }
 }
 
-// ---- warps 0 to 3: softmax, scaling, output ---------------------------------------------
+// ---- warps 0 to 3: softmax, P ------------------------------------------------------------
 template <int DP>
-__device__ __forceinline__ void f32_softmax_role(const AttnParams& p, float4* sums, F32Shared& sh) {
+__device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared& sh) {
     using Lay = F32Layout<DP>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
@@ -338,22 +445,22 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, float4* su
         const int at_first = w.len + p.by_G.of(w.r0), at_last = w.len + p.by_G.of(w.r0 + rows - 1);
         const bool work = warp * 32 < rows, mine = tid < rows;
         float m = -kInf, l = 0.f;
-        float before = 1.f;   // scale of the sums so far, from the tile before to this one
         for (int t = w.t0; t < w.t1; ++t, ++n) {
             const int j0 = w.start(t);
             if (!warp_wait_for(&sh.s_full, n & 1, &sh.abort)) return;
-            float s[kTile];
-            if (work) {
+            if (!work) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_empty);
+                if (n > 0 && !warp_wait_for(&sh.o_done, (n - 1) & 1, &sh.abort)) return;
+            } else {
+                float s[kTile];
                 tc_fence_after();
                 tmem_ld32(lanes + Lay::kS, reinterpret_cast<uint32_t*>(s));
                 tmem_ld32(lanes + Lay::kS + 32, reinterpret_cast<uint32_t*>(s) + 32);
                 tc_wait_ld();
                 tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty);   // the next tile's S may be written
-            float scale_o = 1.f, base = 0.f;
-            if (work) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_empty);   // the next tile's S may be written
                 const bool clean = j0 + kTile - 1 <= at_first &&
                                    (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
                 if (!clean) {
@@ -366,96 +473,38 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, float4* su
 #pragma unroll
                 for (int c = 0; c < kTile; c += 2) x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], s[c]), s[c + 1]);
                 const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
+                float scale_o = 1.f;
                 if (mine && top > m + 8.f) {
                     scale_o = m == -kInf ? 0.f : ex2(m - top);
                     m = top;
                     l *= scale_o;
                 }
-                base = m == -kInf ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float base = m == -kInf ? 0.f : m;
+                const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[kPlanes][kTile / 2];
 #pragma unroll
-                for (int c = 0; c < kTile; ++c) {
-                    s[c] = ex2(fmaf(s[c], p.scale_log2, -base));
-                    sum[c & 3] += s[c];
+                for (int c = 0; c < kTile; c += 2) {
+                    float2 y = ffma2(make_float2(s[c], s[c + 1]), sc, nb);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], y);
+                    uint32_t u[kPlanes];
+                    split(y, u);
+#pragma unroll
+                    for (int i = 0; i < kPlanes; ++i) pk[i][c / 2] = u[i];
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            }
-            // the product before: P's planes are used up, and O may be scaled
-            if (n > 0 && !warp_wait_for(&sh.o_done, (n - 1) & 1, &sh.abort)) return;
-            if (work) {
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                // the product before: P's planes are used up
+                if (n > 0 && !warp_wait_for(&sh.o_done, (n - 1) & 1, &sh.abort)) return;
                 tc_fence_after();
 #pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    uint32_t pk[kPlanes][16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        uint32_t u[kPlanes];
-                        split(s[c0 + c], s[c0 + c + 1], u);
-#pragma unroll
-                        for (int i = 0; i < kPlanes; ++i) pk[i][c / 2] = u[i];
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < kPlanes; ++i) tmem_st16(lanes + Lay::kP + i * 32 + c0 / 2, pk[i]);
-                }
-                if (t > w.t0) {   // O of the tile before joins the sums (scaled to its maximum), or begins them
-                    const bool more = t - w.t0 > 1;
-#pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(lanes + Lay::kO + c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float4* at = sums + (c + i) / 4 * kTcRows + tid;
-                            float4 x = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-                            if (more) {
-                                const float4 y = *at;
-                                x = make_float4(fmaf(y.x, before, x.x), fmaf(y.y, before, x.y), fmaf(y.z, before, x.z), fmaf(y.w, before, x.w));
-                            }
-                            *at = x;
-                        }
-                    }
-                }
-                before = scale_o;
+                for (int i = 0; i < kPlanes; ++i) tmem_st32(lanes + Lay::kP + i * 32, pk[i]);
+                tmem_st4(lanes + Lay::kScale + (n & 1) * 4, __float_as_uint(scale_o), __float_as_uint(m), __float_as_uint(l), 0);
                 tc_wait_st();
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full);
-        }
-        if (!warp_wait_for(&sh.o_done, (n - 1) & 1, &sh.abort)) return;
-        if (work) {
-            tc_fence_after();
-            float* const to = reinterpret_cast<float*>(p.a.out) + ((w.row0 + token) * p.a.Hq + w.head * p.G + rr - token * p.G) * (int64_t)p.a.D;
-            float4* const part = p.part + (int64_t)w.slot * (p.a.D / 4) * p.rows + tid;
-            const float inv = 1.f / l;
-            if (mine && !w.whole) __stcg(p.ml + (int64_t)w.slot * p.rows + tid, make_float2(m, l));
-            const bool summed = w.t1 - w.t0 > 1;
-#pragma unroll 1
-            for (int c0 = 0; c0 < p.a.D; c0 += 32) {
-                uint32_t o[32];
-                __syncwarp();
-                tmem_ld32(lanes + Lay::kO + c0, o);
-                tc_wait_ld();
-                if (mine) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        if (c0 + c >= p.a.D) break;
-                        float4 x = make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]), __uint_as_float(o[c + 3]));
-                        if (summed) {
-                            const float4 y = sums[(c0 + c) / 4 * kTcRows + tid];
-                            x = make_float4(fmaf(y.x, before, x.x), fmaf(y.y, before, x.y), fmaf(y.z, before, x.z), fmaf(y.w, before, x.w));
-                        }
-                        if (w.whole)
-                            put4(to + c0 + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-                        else
-                            __stcg(part + (c0 + c) / 4 * p.rows, x);
-                    }
-                }
-            }
-            __syncwarp();
-            tc_fence_before();
+            if (lane == 0) mbar_arrive(&sh.p_full[n & 1]);
         }
     }
 }
@@ -466,7 +515,6 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     extern __shared__ __align__(1024) char smem[];
     char* const planes = smem;
     char* const raw = smem + 2 * kPlanes * Lay::kPlane;
-    float4* const sums = reinterpret_cast<float4*>(raw + Lay::kRaws * Lay::kRaw);
     F32Shared& sh = *reinterpret_cast<F32Shared*>(smem + Lay::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
     if (warp == 13) {
@@ -477,15 +525,17 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     if (tid == 0) {
         for (int i = 0; i < Lay::kRaws; ++i) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 4);
+            mbar_init(&sh.raw_empty[i], 8);
         }
-        uint64_t* four[] = {&sh.k_full, &sh.v_full, &sh.q_full, &sh.s_empty, &sh.p_full};   // four warps arrive
-        for (int i = 0; i < 5; ++i) mbar_init(four[i], 4);
-        uint64_t* one[] = {&sh.k_empty, &sh.v_empty, &sh.q_empty, &sh.s_full, &sh.o_done, &sh.drain};
-        for (int i = 0; i < 6; ++i) mbar_init(one[i], 1);
+        uint64_t* eight[] = {&sh.k_full, &sh.v_full, &sh.q_full};   // warps that arrive
+        for (int i = 0; i < 3; ++i) mbar_init(eight[i], 8);
+        uint64_t* four[] = {&sh.s_empty, &sh.p_full[0], &sh.p_full[1]};
+        for (int i = 0; i < 3; ++i) mbar_init(four[i], 4);
+        uint64_t* one[] = {&sh.k_empty, &sh.q_empty, &sh.s_full, &sh.o_done, &sh.drain};
+        for (int i = 0; i < 5; ++i) mbar_init(one[i], 1);
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 13);   // twelve warps and the products'
+            mbar_init(&sh.seg_empty[i], 21);   // softmax 4, keys 8, values 8, products 1
         }
         mbar_init_fence();
         sh.abort = 0;
@@ -497,17 +547,20 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) {
-        f32_copy_role<DP>(p, raw, sh);
-        write_status<float>(p, cta, sh.start.valid);
-    } else if (warp == 13) {
-        f32_mma_role<DP>(p, planes, sh);
-    } else if (warp >= 8) {
-        f32_split_role<DP, 1>(p, planes, raw, sh);
+    if (warp >= 12) {
+        registers_down<kRegsRest>();
+        if (warp == 12) {
+            f32_copy_role<DP>(p, raw, sh);
+            write_status<float>(p, cta, sh.start.valid);
+        } else if (warp == 13) {
+            f32_mma_role<DP>(p, planes, sh);
+        }
     } else if (warp >= 4) {
-        f32_split_role<DP, 0>(p, planes, raw, sh);
+        registers_up<kRegsSplit>();
+        f32_split_role<DP>(p, planes, raw, sh);
     } else {
-        f32_softmax_role<DP>(p, sums, sh);
+        registers_up<kRegsSoftmax>();
+        f32_softmax_role<DP>(p, sh);
     }
     tc_fence_before();
     __syncthreads();
@@ -527,6 +580,10 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || ready[dev].load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes of;
+        e = cudaFuncGetAttributes(&of, attention_f32_kernel<DP>);
+        if (e != cudaSuccess) return e;
+        if (of.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // the warpgroups' shares would not add up
         e = cudaFuncSetAttribute(attention_f32_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_release);

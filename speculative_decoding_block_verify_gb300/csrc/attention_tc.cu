@@ -5,7 +5,8 @@
 // with up to 128 rows (the tokens of a block times the query heads of a key head), which is the M of one
 // tcgen05.mma: the block's few rows leave most of it empty, but at 64 positions a tile takes 32 KB from
 // memory (about 1,400 cycles of an SM's share of the measured copy bandwidth) and the two products at M
-// = 128 about 512, so the tensor cores wait for memory whatever the number of rows is.
+// = 128 about 640 (8 of 48 cycles, which is what their operands take from shared memory, and 4 of 64 with P in
+// tensor memory), so the tensor cores wait for memory whatever the number of rows is.
 //
 // A CTA has six warps in three roles.  Warp 4 copies: the pages of K and V by TMA, 128-byte swizzled, into
 // a ring of 64-position slots, and the rows of Q once per item.  Warp 5 issues the products.  Warps 0 to 3

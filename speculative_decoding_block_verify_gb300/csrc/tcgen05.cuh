@@ -39,16 +39,16 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for the phase; false when the wait (or another one of the CTA) gave up.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, int* abort) {
-    for (int n = 0; !mbar_try_wait(bar, parity); ++n) {
-        if (n > kTcSpinLimit) *reinterpret_cast<volatile int*>(abort) = 1;
-        if (*reinterpret_cast<volatile int*>(abort)) return false;
+// Waits for the phase; false when the wait (or another one of the CTA) gave up.  The whole warp decides: a loop that each lane
+// leaves for itself costs twice as much when the phase is already there (heads of 64: 61 us against 57 for 64 streams).
+__device__ __forceinline__ bool warp_wait_for(uint64_t* bar, unsigned parity, int* abort) {
+    for (int n = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++n) {
+        if ((n & 15) == 0) {
+            if (n > kTcSpinLimit) *reinterpret_cast<volatile int*>(abort) = 1;
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort) != 0)) return false;
+        }
     }
     return true;
-}
-__device__ __forceinline__ bool warp_wait_for(uint64_t* bar, unsigned parity, int* abort) {
-    return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle, strides in units of 16 bytes.  K-major (Q, K): 8 rows of 128
@@ -105,15 +105,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
         SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24), "r"(addr)
         : "memory");
 }
-// ... 16 columns
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::SV_W8(r, 0),
-        SV_W8(r, 8), "r"(addr)
-        : "memory");
+// ... eight, four columns
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::SV_W8(r, 0), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(a), "r"(b), "r"(c), "r"(d), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 #undef SV_R8
 #undef SV_W8
+
+// Registers of a warpgroup, all of whose warps ask together; what all ask for is at most what the CTA was launched with.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // 32 bytes in one store
 __device__ __forceinline__ void store32(void* to, const uint32_t* x) {
