@@ -8,8 +8,8 @@
 // = 128 about 640 (8 of 48 cycles, which is what their operands take from shared memory, and 4 of 64 with P in
 // tensor memory), so the tensor cores wait for memory whatever the number of rows is.
 //
-// A CTA has six warps in three roles.  Warp 4 copies: the pages of K and V by TMA, 128-byte swizzled, into
-// a ring of 64-position slots, and the rows of Q once per item.  Warp 5 issues the products.  Warps 0 to 3
+// A CTA has seven warps in four roles.  Warp 4 copies: the pages of K and V by TMA, 128-byte swizzled, into
+// a ring of 64-position slots, and the rows of Q once per item.  Warps 5 and 6 issue the products.  Warps 0 to 3
 // hold one row per thread (TMEM lane = row): they read S, keep the row's maximum and sum, write P as bf16
 // over S, and scale O when the maximum has risen by more than 8 (2^8 of headroom is nothing to float32, and
 // most tiles then leave O alone).  S is double-buffered, so the product of the next tile runs during the
@@ -26,7 +26,7 @@
 
 namespace sv {
 
-constexpr int kTcThreads = 192;
+constexpr int kTcThreads = 224;
 constexpr int kQPlace = kTcRows / 2 * 128;   // bytes to Q's second place: up to 64 rows, the next item's rows fit behind
 
 // DP: the head padded to 64, 128 or 256 columns (TMA fills the rest with zeros).
@@ -43,7 +43,7 @@ struct TcLayout {
 };
 
 struct TcShared {
-    uint64_t q_full[2], q_empty[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], o_done[2], drain[2];
     uint64_t full[10], empty[10];
     uint64_t s_full[2], p_full[2];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
@@ -195,12 +195,19 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     }
 }
 
-// ---- warp 5: products ------------------------------------------------------------------
-// Whichever product has its operands first: S of tile n (its keys, the item's Q, and P of tile n - 2, whose
-// place S takes, used up) or O += P V of tile n (P, and the tile's values).  The whole warp runs the loop, on votes, so
-// that descriptors and addresses are uniform; one lane issues.
+// ---- warps 5 and 6: products -----------------------------------------------------------------
+// Warp 5: S of tile n (its keys, the item's Q, and P of tile n - 2, whose place S takes, used up); warp 6: O += P V (P, and the
+// tile's values).  A whole warp runs each loop, so that descriptors and addresses are uniform; one lane issues.  One warp that
+// looked for either product's operands in turn noticed them later where the softmax is what takes the time (16 streams of 33
+// tokens 51.6 us against 49.4, heads of 256 183 against 179, short streams 20.6 against 20.0; heads of 64 57 against 59).
+// P beside S instead of over it, so that S need not wait for the product two tiles back, gained nothing (heads of 64: 63).
+__device__ __forceinline__ void drain(uint64_t* bar) {   // gave up: what was issued has to end before the CTA's memory is given back
+    if (elected()) mma_commit(bar);
+    __syncwarp();
+    for (int n = 0; n < kTcSpinLimit / 64 && !all_test(bar, 0); ++n) {}
+}
 template <int DP>
-__device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShared& sh) {
+__device__ __forceinline__ bool keys_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
     const SlotLayout<DP> lay(p);
     const uint32_t group = lay.group >> 4, panel = lay.panel >> 4;
@@ -210,127 +217,95 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, char* smem, TcShar
     const int q_places = p.rows <= kTcRows / 2 ? 2 : 1;
     // a negative scale is a negated Q (bit 13) and its magnitude
     const uint32_t qk = mma_desc(kTile, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
-    constexpr uint32_t pv = mma_desc(DP, true);
-    int items = 0, left = 0;       // of the S products: items begun, tiles of the present one not yet issued
-    int q = 0;                     // the present item's place of Q
-    unsigned q_phase = 0;
-    bool first = false, done = false;
-    unsigned n_qk = 0, n_pv = 0;   // products issued
-    unsigned firsts = 0;           // bit (tile & 1): the tile is its item's first
-    int seen_tile = 0, seen_high = 0, seen_low = 0, seen_sink = 0, seen_sinks = 0, seen_first = 0;   // the item of the S products
-    int hide_from[2] = {kTile, kTile}, hide_low[2] = {0, 0}, hide_sink[2] = {0, 0};   // of tile n: rows from hide_from on, and [hide_sink, hide_low)
-    int kslot = 0, vslot = 1;
-    unsigned kphase = 0, vphase = 0;
-    int spins = 0;
-    while (!done || n_pv != n_qk) {
-        bool did = false;
-        if (n_pv != n_qk) {
-            const unsigned buf = n_pv & 1;
-            if (all_test(&sh.p_full[buf], (n_pv >> 1) & 1) && all_test(&sh.full[vslot], vphase)) {
-                tc_fence_after();
-                const bool begin = (firsts >> buf) & 1;
-                const int from = buf ? hide_from[1] : hide_from[0], low = buf ? hide_low[1] : hide_low[0], sink = buf ? hide_sink[1] : hide_sink[0];
-                if (from < kTile || sink < low) {
-                    // values of positions that no row of the item sees: zeros, whatever the cache holds there
-                    char* const at = smem + Lay::kQBytes + vslot * Lay::kSlotBytes;
-                    constexpr int kChunks = Lay::kHalves * 8;   // 16 bytes each, of a row
-                    for (int u = threadIdx.x & 31; u < kTile * kChunks; u += 32) {
-                        const int row = u / kChunks, c = u % kChunks;
-                        if (row >= from || (row >= sink && row < low))
-                            *reinterpret_cast<uint4*>(at + (row >> 3) * lay.group + (c >> 3) * lay.panel + (row & 7) * 128 + (c & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t v = desc_lo(ring + vslot * Lay::kSlotBytes, panel);
-                if (elected()) {
+    int slot = 0;
+    unsigned phase = 0, n = 0;
+    for (int item = 0;; ++item) {
+        const int at = item % kSegments;
+        if (!warp_wait_for(&sh.seg_full[at], (item / kSegments) & 1, &sh.abort)) return false;
+        int left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+        if (elected()) mbar_arrive(&sh.seg_empty[at]);
+        __syncwarp();
+        if (left == 0) return true;
+        const int q = item % q_places;
+        if (!warp_wait_for(&sh.q_full[q], (item / q_places) & 1, &sh.abort)) return false;
+        const uint32_t a = desc_lo(q_at + q * kQPlace, 1);
+        for (; left > 0; --left, ++n) {
+            const unsigned buf = n & 1;
+            if (!warp_wait_for(&sh.full[slot], phase, &sh.abort)) return false;
+            if (n >= 2 && !warp_wait_for(&sh.o_done[buf], ((n >> 1) - 1) & 1, &sh.abort)) return false;
+            tc_fence_after();
+            const uint32_t b = desc_lo(ring + slot * Lay::kSlotBytes, 1);
+            if (elected()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, desc(v + 2 * k * group, group), pv, !(begin && k == 0));
-                    mma_commit(&sh.o_done[buf]);
-                    mma_commit(&sh.empty[vslot]);
-                }
-                __syncwarp();
-                vslot += 2;
-                if (vslot >= Lay::kSlots) {
-                    vslot -= Lay::kSlots;
-                    vphase ^= 1;
-                }
-                ++n_pv;
-                did = true;
+                for (int k = 0; k < Lay::kHalves * 4; ++k)
+                    if (k < ksteps)
+                        mma_ss(tmem + buf * kTile, desc(a + (k >> 2) * (kTcRows * 128 >> 4) + (k & 3) * 2, 1024 >> 4),
+                               desc(b + (k >> 2) * panel + (k & 3) * 2, group), qk, k > 0);
+                mma_commit(&sh.s_full[buf]);
+                mma_commit(&sh.empty[slot]);
+                if (left == 1) mma_commit(&sh.q_empty[q]);
             }
-        }
-        if (left == 0 && !done) {   // the next item
-            const int at = items % kSegments;
-            if (all_test(&sh.seg_full[at], (items / kSegments) & 1)) {
-                const Segment& seg = sh.seg[at];
-                left = __reduce_max_sync(0xffffffffu, seg.t1 - seg.t0);
-                seen_tile = seg.t0;
-                seen_high = seg.high;
-                seen_low = seg.low;
-                seen_sink = seg.sink;
-                seen_sinks = seg.sink_tiles;
-                seen_first = seg.first_tile;
-                __syncwarp();
-                if (elected()) mbar_arrive(&sh.seg_empty[at]);
-                __syncwarp();
-                done = left == 0;
-                first = true;
-                q = items % q_places;
-                q_phase = (items / q_places) & 1;
-                ++items;
-                did = true;
-            }
-        }
-        if (left > 0 && n_qk - n_pv < 2) {
-            const unsigned buf = n_qk & 1;
-            if ((n_qk < 2 || all_test(&sh.o_done[buf], ((n_qk >> 1) - 1) & 1)) && all_test(&sh.full[kslot], kphase) &&
-                (!first || all_test(&sh.q_full[q], q_phase))) {
-                tc_fence_after();
-                firsts = (firsts & ~(1u << buf)) | (unsigned)first << buf;
-                first = false;
-                --left;
-                const int j0 = (seen_tile < seen_sinks ? seen_tile : seen_first + seen_tile - seen_sinks) * kTile;
-                ++seen_tile;
-                const int from = min(kTile, seen_high - j0), low = min(kTile, max(0, seen_low - j0)), sink = max(0, seen_sink - j0);
-                if (buf) {
-                    hide_from[1] = from;
-                    hide_low[1] = low;
-                    hide_sink[1] = sink;
-                } else {
-                    hide_from[0] = from;
-                    hide_low[0] = low;
-                    hide_sink[0] = sink;
-                }
-                const uint32_t a = desc_lo(q_at + q * kQPlace, 1), b = desc_lo(ring + kslot * Lay::kSlotBytes, 1);
-                if (elected()) {
-#pragma unroll
-                    for (int k = 0; k < Lay::kHalves * 4; ++k)
-                        if (k < ksteps)
-                            mma_ss(tmem + buf * kTile, desc(a + (k >> 2) * (kTcRows * 128 >> 4) + (k & 3) * 2, 1024 >> 4),
-                                   desc(b + (k >> 2) * panel + (k & 3) * 2, group), qk, k > 0);
-                    mma_commit(&sh.s_full[buf]);
-                    mma_commit(&sh.empty[kslot]);
-                    if (left == 0) mma_commit(&sh.q_empty[q]);
-                }
-                __syncwarp();
-                kslot += 2;
-                if (kslot >= Lay::kSlots) {
-                    kslot -= Lay::kSlots;
-                    kphase ^= 1;
-                }
-                ++n_qk;
-                did = true;
-            }
-        }
-        spins = did ? 0 : spins + 1;
-        if (spins == kTcSpinLimit) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        if ((spins & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
-            if (elected()) mma_commit(&sh.drain);
             __syncwarp();
-            for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}
-            return;
+            slot += 2;
+            if (slot >= Lay::kSlots) {
+                slot -= Lay::kSlots;
+                phase ^= 1;
+            }
+        }
+    }
+}
+template <int DP>
+__device__ __forceinline__ bool values_role(const AttnParams& p, char* smem, TcShared& sh) {
+    using Lay = TcLayout<DP>;
+    const SlotLayout<DP> lay(p);
+    const uint32_t group = lay.group >> 4, panel = lay.panel >> 4;
+    const uint32_t ring = smem_u32(smem) + Lay::kQBytes;
+    const uint32_t tmem = __reduce_or_sync(0xffffffffu, sh.tmem);
+    constexpr uint32_t pv = mma_desc(DP, true);
+    int slot = 1;
+    unsigned phase = 0, n = 0;
+    for (int item = 0;; ++item) {
+        const int at = item % kSegments;
+        if (!warp_wait_for(&sh.seg_full[at], (item / kSegments) & 1, &sh.abort)) return false;
+        const Segment w = sh.seg[at];
+        const int tiles = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
+        if (elected()) mbar_arrive(&sh.seg_empty[at]);
+        __syncwarp();
+        if (tiles == 0) return true;
+        for (int t = 0; t < tiles; ++t, ++n) {
+            const unsigned buf = n & 1;
+            if (!warp_wait_for(&sh.full[slot], phase, &sh.abort)) return false;
+            const int j0 = w.start(w.t0 + t);
+            const int from = min(kTile, w.high - j0), low = min(kTile, max(0, w.low - j0)), sink = max(0, w.sink - j0);
+            if (from < kTile || sink < low) {
+                // values of positions that no row of the item sees: zeros, whatever the cache holds there
+                char* const to = smem + Lay::kQBytes + slot * Lay::kSlotBytes;
+                constexpr int kChunks = Lay::kHalves * 8;   // 16 bytes each, of a row
+                for (int u = threadIdx.x & 31; u < kTile * kChunks; u += 32) {
+                    const int row = u / kChunks, c = u % kChunks;
+                    if (row >= from || (row >= sink && row < low))
+                        *reinterpret_cast<uint4*>(to + (row >> 3) * lay.group + (c >> 3) * lay.panel + (row & 7) * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (!warp_wait_for(&sh.p_full[buf], (n >> 1) & 1, &sh.abort)) return false;
+            tc_fence_after();
+            const uint32_t v = desc_lo(ring + slot * Lay::kSlotBytes, panel);
+            if (elected()) {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(tmem + Lay::kOCol, tmem + buf * kTile + k * 8, desc(v + 2 * k * group, group), pv, t > 0 || k > 0);
+                mma_commit(&sh.o_done[buf]);
+                mma_commit(&sh.empty[slot]);
+            }
+            __syncwarp();
+            slot += 2;
+            if (slot >= Lay::kSlots) {
+                slot -= Lay::kSlots;
+                phase ^= 1;
+            }
         }
     }
 }
@@ -496,7 +471,8 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         for (int i = 0; i < Lay::kSlots; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
@@ -510,7 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         }
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 5);   // the products' thread and four warps
+            mbar_init(&sh.seg_empty[i], 6);   // softmax 4, products 2
         }
         mbar_init_fence();
         sh.abort = 0;
@@ -526,7 +502,9 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
         copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
         write_status<unsigned short>(p, cta, sh.start.valid);   // while the last tiles are computed
     } else if (warp == 5) {
-        mma_role<DP>(p, smem, sh);
+        if (!keys_role<DP>(p, smem, sh)) drain(&sh.drain[0]);
+    } else if (warp == 6) {
+        if (!values_role<DP>(p, smem, sh)) drain(&sh.drain[1]);
     } else {
         softmax_role<DP>(p, sh);
     }
