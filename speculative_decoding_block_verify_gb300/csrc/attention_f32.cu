@@ -8,7 +8,7 @@
 //
 // One CTA per SM, sixteen warps: copies (warp 12) bring pages as they lie into a ring; warps 4 to 11 split the item's rows of
 // Q into tensor memory and keys and values into swizzled bf16 planes (zeros where no row of the item sees a position,
-// whatever the cache holds there); warp 13 issues the products; warps 0 to 3 hold a row per thread: softmax, and P split
+// whatever the cache holds there); warps 13 and 14 issue the products; warps 0 to 3 hold a row per thread: softmax, and P split
 // into three planes in tensor memory.
 // There is one set of planes each for keys and values: a tile's keys are split during the product of the values before,
 // and its values during its keys' product, so the tensor cores do not wait for either.
@@ -56,7 +56,7 @@ struct F32Layout {
 struct F32Shared {
     uint64_t raw_full[8], raw_empty[8];
     uint64_t k_full, k_empty, v_full;   // the planes; those of V are used up when O is there
-    uint64_t q_full, q_empty, s_full, s_empty, p_full[2], o_done, drain;
+    uint64_t q_full, q_empty, s_full, s_empty, p_full[2], o_done, drain[2];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     Segment seg[kSegments];
     int there[8];   // bit i: page i of the slot's tile is in the pool
@@ -344,82 +344,77 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
     }
 }
 
-// ---- warp 13: products ------------------------------------------------------------------
+// ---- warps 13 (S) and 14 (P V): products ----------------------------------------------------
+// terms unrolled; measured at DP = 128 1 / 2 / 3 / 6: 101 / 99 / 101 / 106 us, at DP = 64 1 / 3 / 6: 82 / 69 / 69
+constexpr int terms_unrolled(int dp) { return dp == 64 ? kTerms : 2; }
 template <int DP>
-__device__ __forceinline__ void f32_mma_role(const AttnParams& p, char* planes, F32Shared& sh) {
+__device__ __forceinline__ bool f32_keys_role(const AttnParams& p, char* planes, F32Shared& sh) {
     using Lay = F32Layout<DP>;
     const uint32_t tmem = __reduce_or_sync(0xffffffffu, sh.tmem);
-    const uint32_t k_at = desc_lo(smem_u32(planes), 1), v_at = desc_lo(smem_u32(planes) + kPlanes * Lay::kPlane, kTile * 128 >> 4);
+    const uint32_t k_at = desc_lo(smem_u32(planes), 1);
     const int ksteps = (p.a.D + 15) / 16;
     const uint32_t qk = mma_desc(kTile, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
+    unsigned n = 0;
+    for (int item = 0;; ++item) {
+        const int at = item % kSegments;
+        if (!warp_wait_for(&sh.seg_full[at], (item / kSegments) & 1, &sh.abort)) return false;
+        int left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+        if (elected()) mbar_arrive(&sh.seg_empty[at]);
+        __syncwarp();
+        if (left == 0) return true;
+        if (!warp_wait_for(&sh.q_full, item & 1, &sh.abort)) return false;
+        for (; left > 0; --left, ++n) {
+            // S of tile n goes where S of tile n - 1 was, once that has been read
+            if (n > 0 && !warp_wait_for(&sh.s_empty, (n - 1) & 1, &sh.abort)) return false;
+            if (!warp_wait_for(&sh.k_full, n & 1, &sh.abort)) return false;
+            tc_fence_after();
+            if (elected()) {
+#pragma unroll(terms_unrolled(DP))
+                for (int term = 0; term < kTerms; ++term) {
+                    const uint32_t a = tmem + Lay::kQ + term_a(term) * (DP / 2), b = k_at + term_b(term) * (Lay::kPlane >> 4);
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        if (k < ksteps)
+                            mma_ts(tmem + Lay::kS, a + k * 8, desc(b + (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2, 1024 >> 4), qk,
+                                   term > 0 || k > 0);
+                }
+                mma_commit(&sh.s_full);
+                mma_commit(&sh.k_empty);
+                if (left == 1) mma_commit(&sh.q_empty);
+            }
+            __syncwarp();
+        }
+    }
+}
+template <int DP>
+__device__ __forceinline__ bool f32_values_role(char* planes, F32Shared& sh) {
+    using Lay = F32Layout<DP>;
+    const uint32_t tmem = __reduce_or_sync(0xffffffffu, sh.tmem);
+    const uint32_t v_at = desc_lo(smem_u32(planes) + kPlanes * Lay::kPlane, kTile * 128 >> 4);
     constexpr uint32_t pv = mma_desc(DP, true);
-    constexpr int kTermsUnrolled = DP == 64 ? kTerms : 2;   // measured: 1 / 2 / 3 / 6 terms unrolled 101 / 99 / 101 / 106 us, at DP = 64 82 / - / 69 / 69
-    int items = 0, left = 0;
-    bool done = false;
-    unsigned n_qk = 0, n_pv = 0;
-    // S of a tile, then P V of the tile before: the order in which their operands come
-    auto keys = [&]() {
-        bool first = false;
-        if (left == 0) {
-            const int at = items % kSegments;
-            if (!warp_wait_for(&sh.seg_full[at], (items / kSegments) & 1, &sh.abort)) return false;
-            left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
-            if (elected()) mbar_arrive(&sh.seg_empty[at]);
-            __syncwarp();
-            done = left == 0;
-            if (done) return true;
-            first = true;
-            ++items;
-        }
-        // S of tile n goes where S of tile n - 1 was, once that has been read
-        if (n_qk > 0 && !warp_wait_for(&sh.s_empty, (n_qk - 1) & 1, &sh.abort)) return false;
-        if (first && !warp_wait_for(&sh.q_full, (items - 1) & 1, &sh.abort)) return false;
-        if (!warp_wait_for(&sh.k_full, n_qk & 1, &sh.abort)) return false;
-        tc_fence_after();
-        --left;
-        if (elected()) {
-#pragma unroll(kTermsUnrolled)
-            for (int term = 0; term < kTerms; ++term) {
-                const uint32_t a = tmem + Lay::kQ + term_a(term) * (DP / 2), b = k_at + term_b(term) * (Lay::kPlane >> 4);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    if (k < ksteps)
-                        mma_ts(tmem + Lay::kS, a + k * 8, desc(b + (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2, 1024 >> 4), qk,
-                               term > 0 || k > 0);
-            }
-            mma_commit(&sh.s_full);
-            mma_commit(&sh.k_empty);
-            if (left == 0) mma_commit(&sh.q_empty);
-        }
+    unsigned n = 0;
+    for (int item = 0;; ++item) {
+        const int at = item % kSegments;
+        if (!warp_wait_for(&sh.seg_full[at], (item / kSegments) & 1, &sh.abort)) return false;
+        int left = __reduce_max_sync(0xffffffffu, sh.seg[at].t1 - sh.seg[at].t0);
+        if (elected()) mbar_arrive(&sh.seg_empty[at]);
         __syncwarp();
-        ++n_qk;
-        return true;
-    };
-    auto values = [&]() {
-        if (!warp_wait_for(&sh.v_full, n_pv & 1, &sh.abort) || !warp_wait_for(&sh.p_full[n_pv & 1], (n_pv >> 1) & 1, &sh.abort)) return false;
-        tc_fence_after();
-        if (elected()) {
-#pragma unroll(kTermsUnrolled)
-            for (int term = 0; term < kTerms; ++term) {
-                const uint32_t a = tmem + Lay::kP + term_a(term) * 32, b = v_at + term_b(term) * (Lay::kPlane >> 4);
+        if (left == 0) return true;
+        for (; left > 0; --left, ++n) {
+            if (!warp_wait_for(&sh.p_full[n & 1], (n >> 1) & 1, &sh.abort)) return false;
+            if (!warp_wait_for(&sh.v_full, n & 1, &sh.abort)) return false;
+            tc_fence_after();
+            if (elected()) {
+#pragma unroll(terms_unrolled(DP))
+                for (int term = 0; term < kTerms; ++term) {
+                    const uint32_t a = tmem + Lay::kP + term_a(term) * 32, b = v_at + term_b(term) * (Lay::kPlane >> 4);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, term > 0 || k > 0);
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + Lay::kO, a + k * 8, desc(b + k * (2048 >> 4), 1024 >> 4), pv, term > 0 || k > 0);
+                }
+                mma_commit(&sh.o_done);
             }
-            mma_commit(&sh.o_done);
-        }
-        __syncwarp();
-        ++n_pv;
-        return true;
-    };
-    while (!done || n_pv != n_qk) {
-        bool ok = done || keys();
-        if (ok && (done ? n_pv != n_qk : n_qk - n_pv == 2)) ok = values();
-        if (!ok) {   // gave up: what was issued has to end before the CTA's memory is given back
-            if (elected()) mma_commit(&sh.drain);
             __syncwarp();
-            for (int n = 0; n < kTcSpinLimit / 64 && !all_test(&sh.drain, 0); ++n) {}
-            return;
         }
     }
 }
@@ -531,11 +526,11 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
         for (int i = 0; i < 3; ++i) mbar_init(eight[i], 8);
         uint64_t* four[] = {&sh.s_empty, &sh.p_full[0], &sh.p_full[1]};
         for (int i = 0; i < 3; ++i) mbar_init(four[i], 4);
-        uint64_t* one[] = {&sh.k_empty, &sh.q_empty, &sh.s_full, &sh.o_done, &sh.drain};
-        for (int i = 0; i < 5; ++i) mbar_init(one[i], 1);
+        uint64_t* one[] = {&sh.k_empty, &sh.q_empty, &sh.s_full, &sh.o_done, &sh.drain[0], &sh.drain[1]};
+        for (int i = 0; i < 6; ++i) mbar_init(one[i], 1);
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 21);   // softmax 4, keys 8, values 8, products 1
+            mbar_init(&sh.seg_empty[i], 22);   // softmax 4, keys 8, values 8, products 2
         }
         mbar_init_fence();
         sh.abort = 0;
@@ -553,7 +548,9 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
             f32_copy_role<DP>(p, raw, sh);
             write_status<float>(p, cta, sh.start.valid);
         } else if (warp == 13) {
-            f32_mma_role<DP>(p, planes, sh);
+            if (!f32_keys_role<DP>(p, planes, sh)) drain(&sh.drain[0]);
+        } else if (warp == 14) {
+            if (!f32_values_role<DP>(planes, sh)) drain(&sh.drain[1]);
         }
     } else if (warp >= 4) {
         registers_up<kRegsSplit>();

@@ -201,11 +201,6 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
 // looked for either product's operands in turn noticed them later where the softmax is what takes the time (16 streams of 33
 // tokens 51.6 us against 49.4, heads of 256 183 against 179, short streams 20.6 against 20.0; heads of 64 57 against 59).
 // P beside S instead of over it, so that S need not wait for the product two tiles back, gained nothing (heads of 64: 63).
-__device__ __forceinline__ void drain(uint64_t* bar) {   // gave up: what was issued has to end before the CTA's memory is given back
-    if (elected()) mma_commit(bar);
-    __syncwarp();
-    for (int n = 0; n < kTcSpinLimit / 64 && !all_test(bar, 0); ++n) {}
-}
 template <int DP>
 __device__ __forceinline__ bool keys_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;

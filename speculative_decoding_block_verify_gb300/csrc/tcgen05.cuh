@@ -141,5 +141,11 @@ __device__ __forceinline__ bool elected() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
     return yes != 0;
 }
+// A warp of products gave up: what it issued has to end before the CTA's memory is given back.
+__device__ __forceinline__ void drain(uint64_t* bar) {
+    if (elected()) mma_commit(bar);
+    __syncwarp();
+    for (int n = 0; n < kTcSpinLimit / 64 && !all_test(bar, 0); ++n) {}
+}
 
 }  // namespace sv
