@@ -18,12 +18,12 @@
 // thread in DP / 2 registers, and the softmax hands them its scales through tensor memory.  (Sums in shared memory,
 // added by the softmax's warps, took a third of a tile's time.)
 //
-// What bounds it: a tile takes about 4,700 cycles.  No pipe is full (issue slots a third, tensor cores two thirds); what it
+// What bounds it: a tile takes about 4,600 cycles.  No pipe is full (issue slots a third, tensor cores two thirds); what it
 // waits for is instructions.  Four different pieces of code run on each quarter of an SM, together more than is kept where
 // instructions are fetched from, and every line of it that is not there costs a trip.  What made the code shorter made it
 // faster: one piece of code for keys and values (122 -> 109 us for 16 streams of 2,100 and 5 tokens of 4 rows a key head), a
 // subtraction of bf16 from float32 in one instruction (107 -> 103), waits that look for a given-up one every 16th time
-// (103 -> 101), and products partly unrolled.  The same kernel with keys and values in warps of their own took 123 us.
+// (103 -> 101), one wait less (98 -> 96), and products partly unrolled.  The same kernel with keys and values in warps of their own took 123 us.
 // An infinite key or value counts as NaN here (the difference to its rounding is).
 
 #include <atomic>
@@ -254,7 +254,7 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
             end = wv.t0 == wv.t1;
             if (nv > 0) {
                 const unsigned before = nv - 1;
-                if (!warp_wait_for(&sh.p_full[before & 1], (before >> 1) & 1, &sh.abort)) return;   // the row's scale
+                // O, and the row's scale: its writers arrived before the product was issued
                 if (!warp_wait_for(&sh.o_done, before & 1, &sh.abort)) return;
                 write = first;
                 if (warp * 32 < (first ? was.rows : wv.rows)) {
