@@ -16,12 +16,17 @@ calls; nothing is timed or checked here - bench.py and the tests do that):
   pick_adaptive128         adaptive_pick_k, B = 128, kmax = 5, H = 7168, bf16, per-stream mode
   pick_batch_adaptive128   the same in batch mode (the sort of the entries in pick_batch_kernel)
   pipeline_adaptive128     SpecPipeline.launch (pick -> verify -> counters -> step + 1)
+  cache_NAME               case NAME of perf/operators.py: cache_verify_64 and cache_window_64
+                           (attention_tc_kernel, join_kernel), cache_window_f32
+                           (attention_f32_kernel), cache_append_256, cache_resize_1024, ...
 
 A profiler filters the launches it captures by kernel name and skips the warm-up calls.
 """
 
 import argparse
+import importlib.util
 import sys
+from pathlib import Path
 
 
 def _bf(torch, a, dev):
@@ -96,6 +101,18 @@ def main(argv=None):
                 pl.launch()
             torch.cuda.synchronize()
             pl.close()
+    elif a.case.startswith("cache_"):
+        spec = importlib.util.spec_from_file_location("operators", Path(__file__).parents[1] / "perf" / "operators.py")
+        operators = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(operators)
+        operators.own = True
+        case = [c for c in operators.listed() if c["name"] == a.case[len("cache_"):]]
+        if not case:
+            print(f"unknown case {a.case}", file=sys.stderr)
+            return 2
+        state = operators.prepare(case[0], 1)
+        for _ in range(total):
+            operators.run(state)
     else:
         print(f"unknown case {a.case}", file=sys.stderr)
         return 2
