@@ -21,6 +21,9 @@ namespace sv {
 // a thread owns RM rows and 64 / TK keys of a tile.  Q, K, V tiles and the weights are in shared memory, rows padded by
 // 4 floats, so that the 16-byte loads of eight neighbouring threads fall into different banks.  The copies are
 // asynchronous: the next tile's keys arrive during this tile's second product, its values during the next one's first.
+// It is bound by shared memory and the float pipes: a tile of 64 positions and 256 columns takes 12,300 cycles of the latter for 48 rows.
+// Products two at a time (even and odd columns) 427 -> 369 us for 16 streams of 2,100 and 5 tokens of 8 rows a key head; groups of 48 rows
+// for what 32 do not hold, instead of 64, 369 -> 248; one CTA an SM where two do not fit, one token each 118 -> 107.
 constexpr int kFloatThreads = 256;
 
 static size_t float_smem(int rows, int D) {
@@ -33,7 +36,7 @@ __device__ __forceinline__ void cp_async16_or_zero(void* to, const void* from, b
 }
 
 template <int R, int TK, int ND>
-__global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float_kernel(const AttnParams p, int q_vec) {
+__global__ void __launch_bounds__(kFloatThreads, R < 48 ? 2 : 1) attention_float_kernel(const AttnParams p, int q_vec) {
     constexpr int TR = kFloatThreads / TK, RM = R / TR, KN = kTile / TK;
     extern __shared__ __align__(16) float fsm[];
     __shared__ Start s_start;
@@ -110,11 +113,11 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
             const int64_t at_after = look_up(t + 2);
             cp_async_wait<1>();   // the keys
             __syncthreads();
-            float s[RM][KN];
+            float2 pair[RM][KN];   // of even and odd columns
 #pragma unroll
             for (int a = 0; a < RM; ++a)
 #pragma unroll
-                for (int b = 0; b < KN; ++b) s[a][b] = 0.f;
+                for (int b = 0; b < KN; ++b) pair[a][b] = make_float2(0.f, 0.f);
 #pragma unroll 2
             for (int c = 0; c < D; c += 4) {
                 float4 x[RM], y[KN];
@@ -126,14 +129,16 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
                 for (int a = 0; a < RM; ++a)
 #pragma unroll
                     for (int b = 0; b < KN; ++b)
-                        s[a][b] = fmaf(x[a].x, y[b].x, fmaf(x[a].y, y[b].y, fmaf(x[a].z, y[b].z, fmaf(x[a].w, y[b].w, s[a][b]))));
+                        pair[a][b] = ffma2(make_float2(x[a].x, x[a].y), make_float2(y[b].x, y[b].y),
+                                           ffma2(make_float2(x[a].z, x[a].w), make_float2(y[b].z, y[b].w), pair[a][b]));
             }
+            float s[RM][KN];
 #pragma unroll
             for (int a = 0; a < RM; ++a) {
                 float hi = -kInf;
 #pragma unroll
                 for (int b = 0; b < KN; ++b) {
-                    s[a][b] = visible(p, at[a], j0 + tk + b * TK) ? s[a][b] * p.scale_log2 : -kInf;
+                    s[a][b] = visible(p, at[a], j0 + tk + b * TK) ? (pair[a][b].x + pair[a][b].y) * p.scale_log2 : -kInf;
                     hi = fmaxf(hi, s[a][b]);
                 }
 #pragma unroll
@@ -179,10 +184,9 @@ __global__ void __launch_bounds__(kFloatThreads, R < 64 ? 2 : 1) attention_float
 #pragma unroll
                             for (int a = 0; a < RM; ++a) {
                                 const float f = kk == 0 ? e[a].x : kk == 1 ? e[a].y : kk == 2 ? e[a].z : e[a].w;
-                                o[a][d].x = fmaf(f, y.x, o[a][d].x);
-                                o[a][d].y = fmaf(f, y.y, o[a][d].y);
-                                o[a][d].z = fmaf(f, y.z, o[a][d].z);
-                                o[a][d].w = fmaf(f, y.w, o[a][d].w);
+                                const float2 u = ffma2(make_float2(f, f), make_float2(y.x, y.y), make_float2(o[a][d].x, o[a][d].y));
+                                const float2 v = ffma2(make_float2(f, f), make_float2(y.z, y.w), make_float2(o[a][d].z, o[a][d].w));
+                                o[a][d] = make_float4(u.x, u.y, v.x, v.y);
                             }
                         }
                     }
@@ -396,8 +400,14 @@ constexpr int kTensorF32 = 128;   // float32 heads up to here go to the tensor c
 static void cut(const spec_attention_args* a, int sms, int* rows, int* ctas) {
     const int64_t need = (int64_t)(a->kmax + 1) * (a->Hq / a->Hkv);
     const bool bf16 = a->dtype == SPEC_DTYPE_BF16, tensor = bf16 || a->D <= kTensorF32;
-    *rows = tensor ? tensor_rows(a) : need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-    int64_t n = (bf16 ? tensor_ctas_per_sm(a) : !tensor && *rows < 64 ? 2 : 1) * (int64_t)sms;   // as many as are resident
+    if (tensor) {
+        *rows = tensor_rows(a);
+    } else {   // as few groups as hold the rows, and those alike
+        const int64_t each = (need + (need + 63) / 64 - 1) / ((need + 63) / 64);
+        *rows = each <= 8 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 48 ? 48 : 64;
+    }
+    const bool two = !tensor && *rows < 48 && 2 * (float_smem(*rows, a->D) + 1024) <= 228 * 1024;
+    int64_t n = (bf16 ? tensor_ctas_per_sm(a) : two ? 2 : 1) * (int64_t)sms;   // as many as are resident
     // no more CTAs than the longest possible contexts have tiles
     const int64_t groups = (need + *rows - 1) / *rows;
     const int64_t tiles = groups * a->B * a->Hkv * (((int64_t)a->max_pages * a->page_size + kTile - 1) / kTile);
@@ -468,6 +478,7 @@ static cudaError_t launch_float_r(const AttnParams& p, cudaStream_t s, bool q_ve
     if (p.rows == 8) return launch_float<8, 32, 2>(p, s, q_vec);
     if (p.rows == 16) return launch_float<16, 16, 4>(p, s, q_vec);
     if (p.rows == 32) return launch_float<32, 16, 4>(p, s, q_vec);
+    if (p.rows == 48) return launch_float<48, 16, 4>(p, s, q_vec);
     return launch_float<64, 16, 4>(p, s, q_vec);
 }
 

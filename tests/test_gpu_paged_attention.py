@@ -150,6 +150,22 @@ def test_many_short_streams():
     check(make(7, [int(x) for x in rng.integers(0, 90, 700)], [int(x) for x in rng.integers(0, 3, 700)], 4, 2, 64, 8))
 
 
+@pytest.mark.parametrize("D", [128, 64, 72])
+def test_many_short_streams_in_float32(D):
+    # items of one to five tiles, several to a CTA: keys are split two tiles ahead of values, into the next items
+    rng = np.random.default_rng(1)
+    lengths = [int(x) for x in rng.integers(0, 310, 230)]
+    check(make(23, lengths, [int(x) for x in rng.integers(0, 4, 230)], 6, 3, D, 16, torch.float32))
+
+
+@pytest.mark.parametrize("Hq,kmax", [(1, 7), (9, 0), (1, 15), (17, 0), (32, 0), (11, 2), (8, 5), (7, 6), (8, 7), (13, 4), (8, 8), (8, 9),
+                                     (8, 32)])
+@pytest.mark.parametrize("D", [144, 256])
+def test_rows_of_wide_float32_heads(Hq, kmax, D):
+    # 8 to 264 rows a key head: every number of rows a group can have, and groups that are not full
+    check(make(24, [70, 0, 333], [kmax, 0, kmax // 2], Hq, 1, D, 32, torch.float32, kmax=kmax))
+
+
 def test_scores_far_apart():
     # one key carries the row, then another: the running maximum moves by hundreds
     c = make(8, [700], [2], 4, 1, 64, 16, q_gain=40.0)
