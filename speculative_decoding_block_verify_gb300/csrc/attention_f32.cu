@@ -6,7 +6,7 @@
 // product.  At M = 128 a tile of 64 positions costs 48 of 32 cycles and 24 of 64, 3,072 tensor cycles, against about 2,800
 // that its 64 KB take from memory; on the float pipes 32 rows alone take 8,192.
 //
-// One CTA per SM, sixteen warps: copies (warp 12) bring pages as they lie into a ring; warps 4 to 11 split the item's rows of
+// One CTA per SM, sixteen warps: copies (warp 15, beside those of the softmax's warps that have rows last) bring pages as they lie into a ring; warps 4 to 11 split the item's rows of
 // Q into tensor memory and keys and values into swizzled bf16 planes (zeros where no row of the item sees a position,
 // whatever the cache holds there); warps 13 and 14 issue the products; warps 0 to 3 hold a row per thread: softmax, and P split
 // into three planes in tensor memory.
@@ -85,7 +85,7 @@ __device__ __forceinline__ void split(float2 x, uint32_t (&w)[kPlanes]) {
     w[2] = pack_bf16(x.x, x.y);
 }
 
-// ---- warp 12: the walk over the CTA's items, and the copies --------------------------------
+// ---- warp 15: the walk over the CTA's items, and the copies --------------------------------
 template <int DP>
 __device__ __forceinline__ void f32_copy_role(const AttnParams& p, char* raw, F32Shared& sh) {
     using Lay = F32Layout<DP>;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void f32_split_role(const AttnParams& p, char* planes
     }
 }
 
-// ---- warps 13 (S) and 14 (P V): products ----------------------------------------------------
+// ---- warps 14 (S) and 13 (P V): products ----------------------------------------------------
 // terms unrolled; measured at DP = 128 1 / 2 / 3 / 6: 101 / 99 / 101 / 106 us, at DP = 64 1 / 3 / 6: 82 / 69 / 69
 constexpr int terms_unrolled(int dp) { return dp == 64 ? kTerms : 2; }
 template <int DP>
@@ -544,12 +544,12 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     tc_fence_after();
     if (warp >= 12) {
         registers_down<kRegsRest>();
-        if (warp == 12) {
+        if (warp == 15) {
             f32_copy_role<DP>(p, raw, sh);
             write_status<float>(p, cta, sh.start.valid);
-        } else if (warp == 13) {
-            if (!f32_keys_role<DP>(p, planes, sh)) drain(&sh.drain[0]);
         } else if (warp == 14) {
+            if (!f32_keys_role<DP>(p, planes, sh)) drain(&sh.drain[0]);
+        } else if (warp == 13) {
             if (!f32_values_role<DP>(planes, sh)) drain(&sh.drain[1]);
         }
     } else if (warp >= 4) {

@@ -8,13 +8,16 @@
 // = 128 about 640 (8 of 48 cycles, which is what their operands take from shared memory, and 4 of 64 with P in
 // tensor memory), so the tensor cores wait for memory whatever the number of rows is.
 //
-// A CTA has seven warps in four roles.  Warp 4 copies: the pages of K and V by TMA, 128-byte swizzled, into
+// A CTA has seven warps in four roles.  Warp 7 copies: the pages of K and V by TMA, 128-byte swizzled, into
 // a ring of 64-position slots, and the rows of Q once per item.  Warps 5 and 6 issue the products.  Warps 0 to 3
 // hold one row per thread (TMEM lane = row): they read S, keep the row's maximum and sum, write P as bf16
 // over S, and scale O when the maximum has risen by more than 8 (2^8 of headroom is nothing to float32, and
 // most tiles then leave O alone).  S is double-buffered, so the product of the next tile runs during the
 // softmax of this one.  Two such CTAs share an SM (256 TMEM columns and half the shared memory each): the
 // start and the end of an item in one overlap with the tiles of the other.
+// Warps go to the quarters of an SM by their number, and a quarter's warps share what fetches their instructions.  With few rows
+// the softmax's warps 2 and 3 have none: copies beside warp 3 instead of beside warp 0 (as warp 4, which is idle now)
+// bring heads of 64 from 59.2 to 56.1 us for 64 streams, of 80 from 75.2 to 70.5, and no shape loses.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -26,7 +29,7 @@
 
 namespace sv {
 
-constexpr int kTcThreads = 224;
+constexpr int kTcThreads = 256;
 constexpr int kQPlace = kTcRows / 2 * 128;   // bytes to Q's second place: up to 64 rows, the next item's rows fit behind
 
 // DP: the head padded to 64, 128 or 256 columns (TMA fills the rest with zeros).
@@ -82,7 +85,7 @@ struct SlotLayout {
     }
 };
 
-// ---- warp 4: the walk over the CTA's items, and the copies --------------------------------
+// ---- warp 7: the walk over the CTA's items, and the copies --------------------------------
 template <int DP>
 __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap, char* smem, TcShared& sh) {
@@ -199,8 +202,8 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
 // Warp 5: S of tile n (its keys, the item's Q, and P of tile n - 2, whose place S takes, used up); warp 6: O += P V (P, and the
 // tile's values).  A whole warp runs each loop, so that descriptors and addresses are uniform; one lane issues.  One warp that
 // looked for either product's operands in turn noticed them later where the softmax is what takes the time (16 streams of 33
-// tokens 51.6 us against 49.4, heads of 256 183 against 179, short streams 20.6 against 20.0; heads of 64 57 against 59).
-// P beside S instead of over it, so that S need not wait for the product two tiles back, gained nothing (heads of 64: 63).
+// tokens 51.6 us against 49.4, heads of 256 183 against 179, short streams 20.6 against 20.0).
+// P beside S instead of over it, so that S need not wait for the product two tiles back, cost 7% (heads of 64).
 template <int DP>
 __device__ __forceinline__ bool keys_role(const AttnParams& p, char* smem, TcShared& sh) {
     using Lay = TcLayout<DP>;
@@ -493,14 +496,14 @@ __global__ void __launch_bounds__(kTcThreads, TcLayout<DP>::kCtasPerSm)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) {
+    if (warp == 7) {
         copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
         write_status<unsigned short>(p, cta, sh.start.valid);   // while the last tiles are computed
     } else if (warp == 5) {
         if (!keys_role<DP>(p, smem, sh)) drain(&sh.drain[0]);
     } else if (warp == 6) {
         if (!values_role<DP>(p, smem, sh)) drain(&sh.drain[1]);
-    } else {
+    } else if (warp < 4) {
         softmax_role<DP>(p, sh);
     }
     tc_fence_before();
