@@ -233,20 +233,20 @@ __global__ void __launch_bounds__(kTrimThreads) trim_kernel(const spec_resize_ar
     }
 }
 
-// Exclusive prefix sums over the block of one int per thread (returns the block's total).
-template <int kThreads>
-__device__ __forceinline__ int block_scan(int v, int* before, int* scratch /* [kThreads / 32 + 1] */) {
+// Exclusive prefix sums over the block of one number per thread (returns the block's total).
+template <int kThreads, typename N>
+__device__ __forceinline__ N block_scan(N v, N* before, N* scratch /* [kThreads / 32] */) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    N x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const N y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    int base = 0, total = 0;
+    N base = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) base += scratch[w];
@@ -273,13 +273,15 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
     extern __shared__ Planned planned[];   // [per][kResizeThreads]
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ int scratch[kResizeThreads / 32];
-    __shared__ int s_need[kResizeCtas], s_copies[kResizeCtas], s_asks[kResizeCtas];
+    // pages asked for: up to 2^28 by each of 65,535 streams, so their sums take 64 bits (what the pool has fits 32)
+    __shared__ int64_t wide_scratch[kResizeThreads / 32], s_need[kResizeCtas];
+    __shared__ int s_copies[kResizeCtas], s_asks[kResizeCtas];
     __shared__ int s_count[2][kResizeCtas];
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = (int)cluster.block_rank();
     const int b0 = (rank * kResizeThreads + tid) * per;
     const ResizeSpace w = resize_space(a.workspace, a.B);
-    auto tell = [&](int* slots, int value) {   // every CTA of the cluster learns this CTA's value
+    auto tell = [&](auto* slots, auto value) {   // every CTA of the cluster learns this CTA's value
         if (tid < kResizeCtas) *cluster.map_shared_rank(slots + rank, tid) = value;
     };
     cluster.sync();   // every CTA's shared memory is there
@@ -337,15 +339,17 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
         }
     }
     // ranks of the streams' new pages and copies, in stream order
-    int need = 0, copies = 0, begin, nth;
+    int64_t need = 0, begin;
+    int copies = 0, nth;
     for (int i = 0; i < per; ++i) {
         need += planned[i * kResizeThreads + tid].need;
         copies += planned[i * kResizeThreads + tid].copy;
     }
-    tell(s_need, block_scan<kResizeThreads>(need, &begin, scratch));
+    tell(s_need, block_scan<kResizeThreads>(need, &begin, wide_scratch));
     tell(s_copies, any_asks ? block_scan<kResizeThreads>(copies, &nth, scratch) : (nth = 0));
     cluster.sync();   // (and every reference given up is given up)
-    int total = 0, pairs = 0;
+    int64_t total = 0;
+    int pairs = 0;
     for (int c = 0; c < kResizeCtas; ++c) {
         if (c < rank) {
             begin += s_need[c];
@@ -394,9 +398,9 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
     for (int i = 0; i < per; ++i) {
         const int b = b0 + i;
         const Planned q = planned[i * kResizeThreads + tid];
-        const bool fits = q.need == 0 || (int64_t)begin + q.need <= found;
+        const bool fits = q.need == 0 || begin + q.need <= found;
         int32_t* row = a.page_table + (int64_t)b * a.max_pages;
-        const int grow = fits ? q.want - q.keep : 0, from = begin + q.copy;
+        const int grow = fits ? q.want - q.keep : 0, from = grow > 0 ? (int)begin + q.copy : 0;
         if (grow <= kOwnPages) {
             for (int j = 0; j < grow; ++j) {
                 const int p = __ldcg(w.list + from + j);
