@@ -56,6 +56,10 @@ struct Item {
     int sink;
     int sink_tiles, first_tile, tiles;
 };
+// Tiles of n positions, and the first position of a tile.  A table row may reach to 2^31 - 8 positions: a number rounded up to
+// whole tiles, and the start of a tile that is looked for past the last one, do not fit an int.
+__device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
+__device__ __forceinline__ int tile_at(int tile) { return (int)((unsigned)tile * kTile); }
 __device__ __forceinline__ Item make_item(const AttnParams& p, int len, int block_rows, int group) {
     Item it;
     it.r0 = group * p.rows;
@@ -64,14 +68,14 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int len, int bloc
     it.high = len + i1 + 1;
     it.low = p.a.window > 0 ? max(0, len + i0 + 1 - p.a.window) : 0;
     it.sink = min(p.a.sinks, it.low);
-    it.sink_tiles = (it.sink + kTile - 1) / kTile;
+    it.sink_tiles = tiles_of(it.sink);
     it.first_tile = max(it.low / kTile, it.sink_tiles);
-    it.tiles = it.sink_tiles + (it.high + kTile - 1) / kTile - it.first_tile;
+    it.tiles = it.sink_tiles + tiles_of(it.high) - it.first_tile;
     return it;
 }
 // First position of tile t of the item.
 __device__ __forceinline__ int tile_start(const Item& it, int t) {
-    return (t < it.sink_tiles ? t : it.first_tile + t - it.sink_tiles) * kTile;
+    return tile_at(t < it.sink_tiles ? t : it.first_tile + t - it.sink_tiles);
 }
 
 __device__ __forceinline__ bool length_ok(const AttnParams& p, int len, int n) {
@@ -274,8 +278,8 @@ __device__ __forceinline__ void write_status(const AttnParams& p, int cta, int v
                 for (int64_t i = lane; i < (int64_t)n * p.a.Hq * p.a.D; i += 32) put(to + i, __int_as_float(0x7fffffff));
             } else {
                 const int low = p.a.window > 0 ? max(0, len + 1 - p.a.window) : 0;
-                const int sp = (min(p.a.sinks, low) + p.a.page_size - 1) >> p.page_shift, lp = low >> p.page_shift;
-                const int hp = (len + n + p.a.page_size - 1) >> p.page_shift;
+                const int sp = (int)(((unsigned)min(p.a.sinks, low) + p.a.page_size - 1) >> p.page_shift), lp = low >> p.page_shift;
+                const int hp = (int)(((unsigned)(len + n) + p.a.page_size - 1) >> p.page_shift);
                 const int32_t* table = p.a.page_table + (int64_t)b * p.a.max_pages;
                 bool bad = false;
                 for (int j = lane; j < sp && j < lp; j += 32) bad |= (unsigned)*(table + j) >= (unsigned)p.a.num_pages;

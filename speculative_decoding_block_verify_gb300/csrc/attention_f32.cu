@@ -114,7 +114,7 @@ __device__ __forceinline__ void f32_copy_role(const AttnParams& p, char* raw, F3
     };
     auto look_up = [&](int t) -> int64_t {   // lane i: where page i of tile t lies in the pool (bytes), or -1
         const int j = tile_start(w.it, t) + lane * box;
-        if (lane >= pages || j >= w.it.high || (j + box <= w.it.low && j >= w.it.sink)) return -1;
+        if (lane >= pages || j >= w.it.high || (j <= w.it.low - box && j >= w.it.sink)) return -1;
         const int page = p.a.page_table[(int64_t)w.b * p.a.max_pages + (j >> p.page_shift)];
         if ((unsigned)page >= (unsigned)p.a.num_pages) return -1;
         return ((((int64_t)page * p.a.Hkv + w.h) * p.a.page_size + (j & (p.a.page_size - 1) & ~(box - 1))) * p.a.D) * 4;
@@ -457,7 +457,7 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.s_empty);   // the next tile's S may be written
                 const bool clean = j0 + kTile - 1 <= at_first &&
-                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
+                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 <= p.a.sinks - kTile);
                 if (!clean) {
                     const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll

@@ -127,7 +127,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
         const int tile = t + lane / pages;
         const int j = tile_start(w.it, tile) + (lane % pages) * box;
         int page = -1;
-        if (tile < w.t1 && j < w.it.high && (j + box > w.it.low || j < w.it.sink))
+        if (tile < w.t1 && j < w.it.high && (j > w.it.low - box || j < w.it.sink))
             page = p.a.page_table[(int64_t)w.b * p.a.max_pages + (j >> p.page_shift)];
         return (unsigned)page < (unsigned)p.a.num_pages ? page * p.a.Hkv + w.h : p.a.num_pages * p.a.Hkv;
     };
@@ -350,7 +350,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) 
                 tc_wait_ld();
                 // a tile that every row sees whole needs no mask
                 const bool clean = j0 + kTile - 1 <= at_first &&
-                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
+                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 <= p.a.sinks - kTile);
                 if (!clean) {
                     const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll
