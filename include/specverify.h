@@ -482,7 +482,8 @@ void spec_cost_curve_destroy(void* curve);
  * that reports TIMEOUT); calls that share it must be ordered.
  * Errors: SPEC_ERR_ARG (NULL pointer, a pool or out that is not 16-byte aligned, scale not finite),
  * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of
- * Hkv or more than 128 times it, q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31), SPEC_ERR_WORKSPACE,
+ * Hkv or more than 128 times it, q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31,
+ * in bf16 num_pages * Hkv >= 2^31 - 1), SPEC_ERR_WORKSPACE,
  * SPEC_ERR_CUDA.  B == 0 launches nothing.
  */
 typedef struct {

@@ -430,6 +430,8 @@ static int check(const spec_attention_args* a) {
         a->max_pages < 1 || (int64_t)a->max_pages * a->page_size > INT32_MAX)
         return set_error(SPEC_ERR_SHAPE, "spec_paged_attention: page_size = %d, num_pages = %d, max_pages = %d",
                          a->page_size, a->num_pages, a->max_pages);
+    if (a->dtype == SPEC_DTYPE_BF16 && (int64_t)a->num_pages * a->Hkv > INT32_MAX - 1)   // the copies' last coordinate
+        return set_error(SPEC_ERR_SHAPE, "spec_paged_attention: num_pages * Hkv = %lld", (long long)a->num_pages * a->Hkv);
     if (a->window < 0 || a->sinks < 0)
         return set_error(SPEC_ERR_SHAPE, "spec_paged_attention: window = %d, sinks = %d", a->window, a->sinks);
     return SPEC_OK;
