@@ -516,9 +516,10 @@ size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
  * spec_cache_append - the block's new keys and values into their pages.
  *   k_pages[page_table[b, p / page_size], h, p % page_size] = k[row, h],   p = length[b] + i
  * and the same for v.  k, v [rows, Hkv, D] with row strides in elements (slices of a wider
- * projection); dtype as the pool.  The pages written must belong to the stream alone (ref_count 1,
- * as spec_cache_resize leaves them).  status [B]: SPEC_ST_OK, BAD_OFFSETS or BAD_LENGTH (nothing
- * of the stream is written), BAD_PAGE (the rows whose page is not in the pool are not written).
+ * projection); dtype as the pool.  The pages written must belong to the stream alone (ref_count 1, as
+ * spec_cache_resize leaves them in a call that reports SPEC_ST_OK for every stream).  status [B]: SPEC_ST_OK,
+ * BAD_OFFSETS or BAD_LENGTH (nothing of the stream is written), BAD_PAGE (the rows whose page is not in the pool
+ * are not written).
  * Errors: SPEC_ERR_ARG, SPEC_ERR_DTYPE, SPEC_ERR_SHAPE, SPEC_ERR_CUDA as in spec_paged_attention.
  */
 typedef struct {
@@ -539,6 +540,16 @@ typedef struct {
 } spec_append_args;
 
 int spec_cache_append(const spec_append_args* args, void* stream);
+/*
+ * spec_cache_append_reserved - the same for the streams whose room spec_cache_resize has reserved: reserved [B] is
+ * that call's status, read on the device.  A stream whose entry is not SPEC_ST_OK is not written and reports the entry (after
+ * BAD_OFFSETS, before the others).  A loop that does not read statuses back needs it: a stream that found no free page
+ * (NO_PAGES) may still hold a page with another stream, whose tokens a plain append would overwrite.  And the stream
+ * that may write into such a page (the lowest of those that asked for a copy) reports NO_PAGES as well, unwritten,
+ * where one that got none has more tokens kept in it.
+ * Errors: also SPEC_ERR_ARG for a NULL reserved.
+ */
+int spec_cache_append_reserved(const spec_append_args* args, const int32_t* reserved, void* stream);
 
 /*
  * spec_cache_resize - gives every stream the pages it needs, no more.
@@ -557,7 +568,8 @@ int spec_cache_append(const spec_append_args* args, void* stream);
  * status [B]: SPEC_ST_OK; BAD_LENGTH (the stream is left as it was: the new length is negative or
  * beyond held * page_size, room is negative, length + room is beyond max_pages * page_size, or held
  * is outside [0, max_pages]); NO_PAGES (streams before it in the batch left too few pages: the new
- * length and step 1 hold, but the stream got no page and must not be appended to); BAD_PAGE (left as
+ * length and step 1 hold, but the stream got no page and must not be appended to: a page of step 2 is then still
+ * shared, see spec_cache_append_reserved); BAD_PAGE (left as
  * it was: a page that the call must look at is not in the pool).
  * k_pool, v_pool: [layers, num_pages, Hkv * page_size * D] in units of page_bytes (a multiple of 16)
  * per page.  workspace: spec_cache_resize_workspace_bytes(B, num_pages) bytes, 16-byte aligned, any contents.

@@ -57,7 +57,7 @@ EXPORTED = ["dspark_markov_bias", "dspark_markov_walk", "dspark_markov_walk_work
             "spec_cost_curve_end", "spec_cost_curve_poll", "spec_cost_curve_observe",
             "spec_cost_curve_table", "spec_cost_curve_upload", "spec_cost_curve_destroy",
             "spec_paged_attention", "spec_paged_attention_workspace_bytes", "spec_cache_append",
-            "spec_cache_resize", "spec_cache_resize_workspace_bytes", "spec_cache_fork",
+            "spec_cache_append_reserved", "spec_cache_resize", "spec_cache_resize_workspace_bytes", "spec_cache_fork",
             "spec_last_error", "spec_version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -157,6 +157,7 @@ def lib():
     L.spec_paged_attention_workspace_bytes.argtypes = [vp]
     L.spec_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     L.spec_cache_append.argtypes = [vp, vp]
+    L.spec_cache_append_reserved.argtypes = [vp, vp, vp]
     L.spec_cache_resize.argtypes = [vp, vp]
     L.spec_cache_resize_workspace_bytes.argtypes = [i32, i32]
     L.spec_cache_resize_workspace_bytes.restype = ctypes.c_size_t
@@ -169,8 +170,8 @@ def lib():
                  "spec_accept_counters", "spec_pipeline_create", "spec_pipeline_launch",
                  "spec_pipeline_destroy", "spec_cost_curve_begin", "spec_cost_curve_end",
                  "spec_cost_curve_poll", "spec_cost_curve_observe", "spec_cost_curve_table",
-                 "spec_cost_curve_upload", "spec_paged_attention", "spec_cache_append", "spec_cache_resize",
-                 "spec_cache_fork"):
+                 "spec_cost_curve_upload", "spec_paged_attention", "spec_cache_append", "spec_cache_append_reserved",
+                 "spec_cache_resize", "spec_cache_fork"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -724,10 +725,12 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     return out
 
 
-def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kmax, out=None, stream=None):
+def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kmax, out=None, stream=None, reserved=None):
     """Writes the block's k and v [rows, Hkv, D] (slices of a wider projection may be passed) to their
-    positions in one layer's pages; the other arguments as in spec_paged_attention.  Returns (and
-    reuses) ``out`` with status [B]."""
+    positions in one layer's pages; the other arguments as in spec_paged_attention.  With ``reserved`` (the status of
+    the spec_cache_resize that made the room) a stream that has none there is left alone and reports that status: what
+    keeps one that found no free page (NO_PAGES) off a page that it still shares.  Returns (and reuses) ``out`` with
+    status [B]."""
     torch = _T or _cache_torch()
     device, code, kp, vp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
     dtype = k_pages.dtype
@@ -739,9 +742,13 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     if out is None:
         out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
-    rc = (_lib or lib()).spec_cache_append(_APPEND.pack(
-        B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, nk, nv, ks, vs, rows, kp, vp,
-        _on(out["status"], "status", device, _I32, (B,))), _raw_stream(stream, device))
+    args = _APPEND.pack(B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, nk, nv, ks, vs, rows, kp, vp,
+                        _on(out["status"], "status", device, _I32, (B,)))
+    L = _lib or lib()
+    if reserved is None:
+        rc = L.spec_cache_append(args, _raw_stream(stream, device))
+    else:
+        rc = L.spec_cache_append_reserved(args, _on(reserved, "reserved", device, _I32, (B,)), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out

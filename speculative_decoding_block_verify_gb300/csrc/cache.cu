@@ -23,23 +23,29 @@ namespace cg = cooperative_groups;
 // searches for its stream.  A thread moves 16 bytes of K and of V (or one element of each, where a
 // base or a row stride is not a multiple of 16 bytes).  Bound by latency at decode sizes (one stream's block: 3.1 us);
 // 256 streams with up to 33 tokens of 8 heads of 128 (52.8 MB): 9.2 us, 5.7 TB/s.
+// With resize's statuses, a stream that it had no room for is passed over: where a copy was not to be had, the table still
+// has the shared page.  Of that page's holders one at most was told OK; it is passed over too where one that was not has
+// tokens behind its own there (it was rolled back further).
 constexpr int kAppendThreads = 256;
 
 template <typename U>   // the unit moved by a thread: uint4, or one element
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_append_args a, int units_per_head) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_append_args a, const int32_t* reserved, int units_per_head) {
     __shared__ int s_first;
     __shared__ int s_page[SPEC_MAX_KMAX + 1];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_others;
     const int b = blockIdx.x, tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = __ldcg(a.length + b);
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s_bad = s_others = 0;
+    const int refused = reserved != nullptr ? __ldcg(reserved + b) : SPEC_ST_OK;
     const bool offsets_ok = valid_prefix(a.cu_drafts, a.B, a.kmax, a.rows, b + 1, &s_first) > b;
     int status = SPEC_ST_OK, n = 0;
     int64_t row0 = 0;
     if (!offsets_ok) {
         status = SPEC_ST_BAD_OFFSETS;
+    } else if (refused != SPEC_ST_OK) {
+        status = refused;
     } else {
         n = block_rows(a.cu_drafts, b, a.kmax);
         row0 = first_row(a.cu_drafts, b, a.kmax);
@@ -56,11 +62,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const spec_appen
             }
             s_page[i] = page;
         }
+        if (reserved != nullptr && (len & (a.page_size - 1)) != 0) {
+            const int32_t* table = a.page_table + (len >> shift);
+            const int mine = *(table + (int64_t)b * a.max_pages);
+            for (int o = tid; o < a.B; o += kAppendThreads)
+                if (__ldcg(reserved + o) == SPEC_ST_NO_PAGES && __ldcg(a.length + o) > len && *(table + (int64_t)o * a.max_pages) == mine)
+                    s_others = 1;
+        }
     }
     __syncthreads();
-    if (status == SPEC_ST_OK && s_bad) status = SPEC_ST_BAD_PAGE;
-    if (blockIdx.y == 0 && tid == 0) a.status[b] = status;
-    if (status == SPEC_ST_BAD_OFFSETS || status == SPEC_ST_BAD_LENGTH) return;
+    if (s_others) status = SPEC_ST_NO_PAGES;
+    const bool bad_page = status == SPEC_ST_OK && s_bad;
+    if (blockIdx.y == 0 && tid == 0) a.status[b] = bad_page ? SPEC_ST_BAD_PAGE : status;
+    if (status != SPEC_ST_OK) return;
     const U* k = reinterpret_cast<const U*>(a.k);
     const U* v = reinterpret_cast<const U*>(a.v);
     U* kp = reinterpret_cast<U*>(a.k_pages);
@@ -533,8 +547,7 @@ static bool table_ok(int max_pages, int page_size) { return (int64_t)max_pages *
 
 using namespace sv;
 
-extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
-    clear_error();
+static int append(const spec_append_args* a, const int32_t* reserved, void* stream) {
     if (a == nullptr) return set_error(SPEC_ERR_ARG, "spec_cache_append: args is NULL");
     if (!valid_dtype(a->dtype)) return set_error(SPEC_ERR_DTYPE, "spec_cache_append: dtype %d", a->dtype);
     if (a->B < 0 || a->B > SPEC_MAX_STREAMS || a->kmax < 0 || a->kmax > SPEC_MAX_KMAX)
@@ -561,10 +574,22 @@ extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
     const int64_t want = (units + 2 * kAppendThreads - 1) / (2 * kAppendThreads);   // two units a thread
     const dim3 grid((unsigned)a->B, (unsigned)(want < 1 ? 1 : want > 64 ? 64 : want));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = vec       ? launch_after(append_kernel<uint4>, grid, dim3(kAppendThreads), 0, s, *a, upb)
-                          : es == 2 ? launch_after(append_kernel<unsigned short>, grid, dim3(kAppendThreads), 0, s, *a, upb)
-                                    : launch_after(append_kernel<float>, grid, dim3(kAppendThreads), 0, s, *a, upb);
+    const cudaError_t e = vec       ? launch_after(append_kernel<uint4>, grid, dim3(kAppendThreads), 0, s, *a, reserved, upb)
+                          : es == 2 ? launch_after(append_kernel<unsigned short>, grid, dim3(kAppendThreads), 0, s, *a, reserved, upb)
+                                    : launch_after(append_kernel<float>, grid, dim3(kAppendThreads), 0, s, *a, reserved, upb);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_append");
+}
+
+extern "C" int spec_cache_append(const spec_append_args* a, void* stream) {
+    clear_error();
+    return append(a, nullptr, stream);
+}
+
+extern "C" int spec_cache_append_reserved(const spec_append_args* a, const int32_t* reserved, void* stream) {
+    clear_error();
+    if (a != nullptr && a->B > 0 && reserved == nullptr)
+        return set_error(SPEC_ERR_ARG, "spec_cache_append_reserved: reserved is NULL");
+    return append(a, reserved, stream);
 }
 
 extern "C" size_t spec_cache_resize_workspace_bytes(int32_t B, int32_t num_pages) {

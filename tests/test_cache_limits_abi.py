@@ -4,7 +4,7 @@ import pytest
 
 import speculative_decoding_block_verify_gb300 as sv
 from speculative_decoding_block_verify_gb300 import build as svbuild
-from tests.test_cache_abi import attention
+from tests.test_cache_abi import P, append, attention
 
 
 @pytest.fixture(scope="module")
@@ -20,3 +20,12 @@ def test_pages_times_heads_is_a_coordinate(L):
         rc = L.spec_paged_attention(args, None)
         # without a device the call that passes the sizes' checks ends at the device's attributes
         assert rc == code or (code == -6 and rc == -4), (pages, Hkv, dtype, rc)
+
+
+def test_append_reserved_errors(L):
+    assert L.spec_cache_append_reserved(None, None, None) == -1
+    assert L.spec_cache_append_reserved(append(), None, None) == -1
+    assert b"reserved" in L.spec_last_error()
+    for change, code in [(dict(dtype=-1), -2), (dict(kmax=33), -3), (dict(page=20), -3), (dict(rows=-1), -3), (dict(kp=0), -1)]:
+        assert L.spec_cache_append_reserved(append(**change), P, None) == code, change
+    assert L.spec_cache_append_reserved(append(B=0), None, None) == 0
