@@ -9,7 +9,8 @@ written into).  Each step then
      (spec_cache_append) and the block attends over the whole context (spec_paged_attention),
   3. verifies the block (spec_verify_block), and
   4. keeps the emitted tokens' pages and reserves room for the next block (spec_cache_resize).
-Nothing is read back to the host inside a step.  The target is a small random transformer whose projections
+Nothing is read back to the host inside a step: what a call reports for a stream goes into the next one on the device.  A
+stream that finds no page in step 4 is passed over by the next step's append, keeps nothing of that step and asks again.  The target is a small random transformer whose projections
 are plain torch products: it stands for a user's model.
 """
 
@@ -51,42 +52,58 @@ class Cache:
         i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
         self.table, self.held, self.length, self.refs = i32(streams, width) - 1, i32(streams), i32(streams), i32(pages)
         self._resize = self._fork = None
+        self.reserved = None   # the status of the resize that made the room for the next block
 
     def resize(self, advance=None, room=None):
         self._resize = sv.spec_cache_resize(self.k, self.v, self.table, self.held, self.length, self.refs, advance=advance,
                                             room=room, out=self._resize)
-        return self._resize["status"]
+        self.reserved = self._resize["status"]
+        return self.reserved
 
     def fork(self, src, dst):
         self._fork = sv.spec_cache_fork(src, dst, self.table, self.held, self.length, self.refs, self.page)
         return self._fork["status"]
 
 
+def first_of(torch, *statuses):
+    """Per stream, the first status that is not OK."""
+    worst = statuses[0].clone()
+    for s in statuses[1:]:
+        worst = torch.where(worst == 0, s, worst)
+    return worst
+
+
 def forward(torch, target, cache, tokens, cu, kmax, state):
-    """Logits [rows, V] of the packed block rows ``tokens``; their keys and values are appended."""
+    """Logits [rows, V] of the packed block rows ``tokens``; their keys and values are appended.  ``state["status"]`` is
+    what the block's calls report for each stream, that of the resize before them included."""
     rows = tokens.numel()
     stream = torch.searchsorted(cu + torch.arange(cu.numel(), device=cu.device), torch.arange(rows, device=cu.device), right=True) - 1
     at = cache.length[stream] + torch.arange(rows, device=cu.device) - cu[stream] - stream
     x = target.embedding[tokens.long()] + target.position[at]
     H, G, D = target.q_heads, target.kv_heads, target.head
+    status = cache.reserved
     for i in range(target.layers):
         qkv = (x @ target.qkv[i]).view(rows, H + 2 * G, D)
         # slices of the projection go in as they lie
         state["append"] = sv.spec_cache_append(qkv[:, H:H + G], qkv[:, H + G:], cache.k[i], cache.v[i], cache.table,
-                                               cache.length, cu, kmax, out=state.get("append"))
+                                               cache.length, cu, kmax, out=state.get("append"), reserved=cache.reserved)
         key = ("attention", rows, kmax)
         state[key] = sv.spec_paged_attention(qkv[:, :H], cache.k[i], cache.v[i], cache.table, cache.length, cu, kmax,
                                              D ** -0.5, out=state.get(key))
+        status = first_of(torch, status, state["append"]["status"], state[key]["status"])
         x = x + state[key]["out"].view(rows, H * D) @ target.o[i]
         x = x * torch.rsqrt((x.float() ** 2).mean(dim=1, keepdim=True)).to(x.dtype)
+    state["status"] = status
     W1, W2 = target.table
     return (x @ target.logits).float() + W1[tokens.long()] @ W2
 
 
 def prefill(torch, target, cache, prompt, state, kmax=sv.MAX_DRAFTS):
-    """The prompt but its last token into stream 0's pages, a block of kmax + 1 tokens at a time."""
+    """The prompt but its last token into stream 0's pages, a block of kmax + 1 tokens at a time.  Returns the first
+    status [1] that is not OK."""
     B, dev = cache.length.numel(), prompt.device
     n = prompt.numel() - 1
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
     for at in range(0, n, kmax + 1):
         part = prompt[at:min(n, at + kmax + 1)]
         one = torch.zeros(B, dtype=torch.int32, device=dev)
@@ -95,20 +112,25 @@ def prefill(torch, target, cache, prompt, state, kmax=sv.MAX_DRAFTS):
         # the other streams have no tokens yet: the block belongs to stream 0 alone
         view = _OneStream(cache)
         cu = torch.tensor([0, part.numel() - 1], dtype=torch.int32, device=dev)
-        forward(torch, target, view, part, cu, kmax, {})
+        mine = {}
+        forward(torch, target, view, part, cu, kmax, mine)
+        status = first_of(torch, status, mine["status"])
+        one[0] = torch.where(status[0] == 0, one[0], 0)
         cache.resize(advance=one)
+    return status
 
 
 class _OneStream:
     """Stream 0 of a cache."""
 
     def __init__(self, cache):
-        self.k, self.v, self.table, self.length = cache.k, cache.v, cache.table[:1], cache.length[:1]
+        self.k, self.v, self.table, self.length, self.reserved = cache.k, cache.v, cache.table[:1], cache.length[:1], cache.reserved[:1]
 
 
 def decode(torch, target, cache, anchor, steps, drafts, temperature, drafter, seed=0):
     """``steps`` verify steps from the tokens ``anchor`` [B].  Returns (tokens [B, steps * (drafts + 1)] with
-    -1 past the emitted ones, emitted counts [steps, B], statuses [steps, B])."""
+    -1 past the emitted ones, emitted counts [steps, B], statuses [steps, B]): 0 tokens and the first status of the step's calls
+    that is not OK where a stream could not take part."""
     dev, B, N = anchor.device, anchor.numel(), drafts
     W1, W2 = drafter
     cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * N
@@ -129,15 +151,18 @@ def decode(torch, target, cache, anchor, steps, drafts, temperature, drafter, se
         block = torch.cat([anchor[:, None], x.view(B, N)], dim=1).view(-1)
         logits = forward(torch, target, cache, block, cu, N, state)
         out = sv.spec_verify_block(cu, q, logits, x, temperature, N, seed, step, out=out)
-        cache.resize(advance=out["n_emitted"], room=room)
-        n = out["n_emitted"].long()
-        anchor = out["out_tokens"].gather(1, (n - 1).clamp(min=0)[:, None])[:, 0].contiguous()
+        status[step] = first_of(torch, state["status"], out["status"])
+        kept = torch.where(status[step] == 0, out["n_emitted"], 0)
+        cache.resize(advance=kept, room=room)
+        n = kept.long()
+        last = out["out_tokens"].gather(1, (n - 1).clamp(min=0)[:, None])[:, 0]
+        anchor = torch.where(n > 0, last, anchor).contiguous()
         col = torch.arange(N + 1, device=dev)
         here = col < n[:, None]
         where = torch.where(here, ends[:, None] + col, tokens.shape[1] - 1)
         tokens.scatter_(1, where, torch.where(here, out["out_tokens"], tokens.gather(1, where)))
         ends += n
-        counts[step], status[step] = out["n_emitted"], out["status"]
+        counts[step] = kept
     return tokens, counts, status
 
 
@@ -156,15 +181,15 @@ def main():
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     prompt = torch.randint(0, target.V, (a.prompt,), generator=g, device="cuda", dtype=torch.int32)
-    prefill(torch, target, cache, prompt, {})
+    seen = [prefill(torch, target, cache, prompt, {})]
     if a.streams > 1:
         others = torch.arange(1, a.streams, dtype=torch.int32, device="cuda")
-        cache.fork(torch.zeros_like(others), others)
+        seen.append(cache.fork(torch.zeros_like(others), others))
     temperature = torch.full((a.streams,), a.temperature, device="cuda")
     tokens, counts, status = decode(torch, target, cache, prompt[-1:].repeat(a.streams), a.steps, a.drafts, temperature, target.table)
     torch.cuda.synchronize()
     print(f"{a.streams} streams, {a.steps} steps of {a.drafts} drafts: {counts.float().mean().item():.2f} tokens a step, "
-          f"statuses {sorted(set(status.view(-1).tolist()))}, pages held {int(cache.held.sum())} of {cache.refs.numel()}")
+          f"statuses {sorted(set(torch.cat(seen + [status.view(-1)]).tolist()))}, pages held {int(cache.held.sum())} of {cache.refs.numel()}")
     for b in range(min(3, a.streams)):
         print(" ", tokens[b, :16].tolist())
 
