@@ -76,10 +76,14 @@ def first_of(torch, *statuses):
 def forward(torch, target, cache, tokens, cu, kmax, state):
     """Logits [rows, V] of the packed block rows ``tokens``; their keys and values are appended.  ``state["status"]`` is
     what the block's calls report for each stream, that of the resize before them included."""
+    if cache.table.shape[1] * cache.page > target.position.shape[0]:
+        raise ValueError(f"the cache has room for {cache.table.shape[1] * cache.page} tokens a stream, the model for "
+                         f"{target.position.shape[0]}")
     rows = tokens.numel()
     stream = torch.searchsorted(cu + torch.arange(cu.numel(), device=cu.device), torch.arange(rows, device=cu.device), right=True) - 1
     at = cache.length[stream] + torch.arange(rows, device=cu.device) - cu[stream] - stream
-    x = target.embedding[tokens.long()] + target.position[at]
+    # a block that does not fit its stream's table row is refused by the calls below, and its rows stand for nothing
+    x = target.embedding[tokens.long()] + target.position[at.clamp(max=target.position.shape[0] - 1)]
     H, G, D = target.q_heads, target.kv_heads, target.head
     status = cache.reserved
     for i in range(target.layers):
@@ -125,6 +129,7 @@ class _OneStream:
 
     def __init__(self, cache):
         self.k, self.v, self.table, self.length, self.reserved = cache.k, cache.v, cache.table[:1], cache.length[:1], cache.reserved[:1]
+        self.page = cache.page
 
 
 def decode(torch, target, cache, anchor, steps, drafts, temperature, drafter, seed=0):
@@ -132,6 +137,10 @@ def decode(torch, target, cache, anchor, steps, drafts, temperature, drafter, se
     -1 past the emitted ones, emitted counts [steps, B], statuses [steps, B]): 0 tokens and the first status of the step's calls
     that is not OK where a stream could not take part."""
     dev, B, N = anchor.device, anchor.numel(), drafts
+    # resize leaves a stream whose next block does not fit its row as it was, kept tokens and all: rows are long enough
+    most = int(cache.length.max()) + (steps + 1) * (N + 1)
+    if most > cache.table.shape[1] * cache.page:
+        raise ValueError(f"{steps} steps may need {most} tokens a stream, the cache has room for {cache.table.shape[1] * cache.page}")
     W1, W2 = drafter
     cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * N
     room = torch.full((B,), N + 1, dtype=torch.int32, device=dev)
@@ -176,8 +185,9 @@ def main():
     ap.add_argument("--prompt", type=int, default=100)
     ap.add_argument("--temperature", type=float, default=0.8)
     a = ap.parse_args()
-    target = Target(torch)
-    cache = Cache(torch, target, a.streams, a.prompt + (a.steps + 1) * (a.drafts + 1))
+    tokens = a.prompt + (a.steps + 1) * (a.drafts + 1)
+    target = Target(torch, positions=-(-tokens // 16) * 16)
+    cache = Cache(torch, target, a.streams, tokens)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     prompt = torch.randint(0, target.V, (a.prompt,), generator=g, device="cuda", dtype=torch.int32)

@@ -51,3 +51,19 @@ def test_a_prompt_that_does_not_fit_is_reported():
     prompt = torch.arange(50, dtype=torch.int32, device="cuda")
     assert ex.prefill(torch, target, cache, prompt, {}).tolist() == [8]
     assert int(cache.length[0]) == 0
+
+
+def test_rows_that_are_too_short_are_refused_or_reported():
+    target = ex.Target(torch, positions=64)
+    cache = ex.Cache(torch, target, 2, 64, page=16)
+    anchor, zero = torch.tensor([3, 4], dtype=torch.int32, device="cuda"), torch.zeros(2, device="cuda")
+    with pytest.raises(ValueError, match="68 tokens a stream"):
+        ex.decode(torch, target, cache, anchor, 16, 3, zero, target.table)
+    _, counts, status = ex.decode(torch, target, cache, anchor, 15, 3, zero, target.table)
+    assert (status == 0).all() and torch.equal(cache.length.long(), counts.long().sum(dim=0))
+    # a prompt longer than the row: nothing is read past the model's positions
+    target = ex.Target(torch, positions=64)
+    cache = ex.Cache(torch, target, 2, 64, page=16)
+    prompt = torch.arange(101, dtype=torch.int32, device="cuda")
+    assert ex.prefill(torch, target, cache, prompt, {}).tolist() == [9]
+    assert cache.length.tolist() == [33, 0]
