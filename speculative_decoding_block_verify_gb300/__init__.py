@@ -22,10 +22,14 @@ Entry points (same names as the C ABI):
 * ``spec_cache_fork``        - a stream's pages shared with other streams
 * ``spec_philox_uniforms``   - the verify calls' uniforms (for checking)
 
+Every call takes ``stream`` (None: the current one).  What it makes for the caller when ``out`` is None belongs to that
+stream, as if made under ``torch.cuda.stream(stream)``: a caller that reads it on another stream orders the two.
+
 Build the library first: ``python -m speculative_decoding_block_verify_gb300.build`` (or
 ``__graft_entry__.build()``).
 """
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -211,6 +215,12 @@ def _stream(stream):
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _made_on(stream):
+    """Buffers that a call makes are its stream's: filled there, in order with the kernels, and free again for its work
+    alone (the caller cannot order a fill inside the call on another stream)."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
 def _ptr(t):
@@ -712,9 +722,10 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
         need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(
             B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows,
             kp, vp, 0, 0, 0, 0))
-        out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
-               "status": torch.empty(B, dtype=torch.int32, device=q.device),
-               "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
+        with _made_on(stream):
+            out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
+                   "status": torch.empty(B, dtype=torch.int32, device=q.device),
+                   "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
     ws = out["workspace"]
     rc = L.spec_paged_attention(_ATTENTION.pack(
         B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows, kp, vp,
@@ -741,7 +752,8 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
         raise ValueError("k and v must have the same rows")
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     if out is None:
-        out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
+        with _made_on(stream):
+            out = {"status": torch.empty(B, dtype=torch.int32, device=k.device)}
     args = _APPEND.pack(B, kmax, Hkv, D, page_size, num_pages, max_pages, code, cu, lp, tp, nk, nv, ks, vs, rows, kp, vp,
                         _on(out["status"], "status", device, _I32, (B,)))
     L = _lib or lib()
@@ -789,8 +801,9 @@ def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advan
     L = _lib or lib()
     if out is None:
         need = max(int(L.spec_cache_resize_workspace_bytes(B, num_pages)), 16)
-        out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
-               "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
+        with _made_on(stream):
+            out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
+                   "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
     ws = out["workspace"]
     rc = L.spec_cache_resize(_RESIZE.pack(
         B, page_size, num_pages, max_pages, shape[0], page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
@@ -810,7 +823,8 @@ def spec_cache_fork(src, dst, page_table, held, length, ref_count, page_size, ou
     sp = _on(src, "src", device, _I32, (n,))
     dp = _on(dst, "dst", device, _I32, (n,))
     if out is None:
-        out = {"status": torch.empty(n, dtype=torch.int32, device=page_table.device)}
+        with _made_on(stream):
+            out = {"status": torch.empty(n, dtype=torch.int32, device=page_table.device)}
     rc = (_lib or lib()).spec_cache_fork(sp, dp, n, B, page_size, num_pages, max_pages, tp, hp, lp, rp,
                                          _on(out["status"], "status", device, _I32, (n,)), _raw_stream(stream, device))
     if rc != 0:
