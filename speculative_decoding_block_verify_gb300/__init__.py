@@ -245,7 +245,8 @@ def dspark_markov_bias(draft_logits, prev_tokens, W1, W2, out=None, stream=None)
     if prev_tokens.shape != (rows,):
         raise ValueError("prev_tokens must be [rows]")
     if out is None:
-        out = torch.empty((rows, V), dtype=torch.float32, device=draft_logits.device)
+        with _made_on(stream):
+            out = torch.empty((rows, V), dtype=torch.float32, device=draft_logits.device)
     _dev(out, "out", torch.float32)
     _check(lib().dspark_markov_bias(_ptr(draft_logits), _dtype_code(draft_logits), rows, V,
                                     _ptr(prev_tokens), _ptr(W1), _ptr(W2), _dtype_code(W1), R,
@@ -271,11 +272,12 @@ def dspark_markov_walk(draft_logits, anchor, W1, W2, temperature, seed, step, ou
         raise ValueError("anchor and temperature must be [B]")
     dev = draft_logits.device
     if out is None:
-        out = {"tokens": torch.empty((B, N), dtype=torch.int32, device=dev),
-               "logits": torch.empty((B, N, V), dtype=torch.float32, device=dev),
-               "status": torch.empty(B, dtype=torch.int32, device=dev),
-               "workspace": torch.empty(max(int(lib().dspark_markov_walk_workspace_bytes(B)), 16),
-                                        dtype=torch.uint8, device=dev)}
+        with _made_on(stream):
+            out = {"tokens": torch.empty((B, N), dtype=torch.int32, device=dev),
+                   "logits": torch.empty((B, N, V), dtype=torch.float32, device=dev),
+                   "status": torch.empty(B, dtype=torch.int32, device=dev),
+                   "workspace": torch.empty(max(int(lib().dspark_markov_walk_workspace_bytes(B)), 16),
+                                            dtype=torch.uint8, device=dev)}
     _check(lib().dspark_markov_walk(_ptr(draft_logits), _dtype_code(draft_logits), B, N, V, _ptr(anchor),
                                     _ptr(W1), _ptr(W2), _dtype_code(W1), R, _ptr(temperature),
                                     int(seed) & 0xFFFFFFFFFFFFFFFF, int(step) & 0xFFFFFFFFFFFFFFFF,
@@ -311,22 +313,24 @@ def _verify(fn, cu_drafts, draft_logits, target_logits, draft_tokens, temperatur
         raise ValueError("temperature must be [B]")
     dev = target_logits.device
     if out is None:
-        out = {
-            "accepted_len": torch.empty(B, dtype=torch.int32, device=dev),
-            "out_tokens": torch.empty((B, kmax + 1), dtype=torch.int32, device=dev),
-            "n_emitted": torch.empty(B, dtype=torch.int32, device=dev),
-            "status": torch.empty(B, dtype=torch.int32, device=dev),
-        }
-        if diag:
-            out["diag"] = torch.empty((target_logits.shape[0], DIAG_COLS), dtype=torch.float32,
-                                      device=dev)
+        with _made_on(stream):
+            out = {
+                "accepted_len": torch.empty(B, dtype=torch.int32, device=dev),
+                "out_tokens": torch.empty((B, kmax + 1), dtype=torch.int32, device=dev),
+                "n_emitted": torch.empty(B, dtype=torch.int32, device=dev),
+                "status": torch.empty(B, dtype=torch.int32, device=dev),
+            }
+            if diag:
+                out["diag"] = torch.empty((target_logits.shape[0], DIAG_COLS), dtype=torch.float32,
+                                          device=dev)
     ws = None
     if workspace:
         need = spec_verify_workspace_bytes(B, kmax)
         ws = out.get("workspace")
         if ws is None or ws.numel() < need:
             # zero-filled once: every call leaves the row counters it used at zero
-            ws = out["workspace"] = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
+            with _made_on(stream):
+                ws = out["workspace"] = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
     a = VerifyArgs()
     a.B, a.V, a.kmax = B, V, kmax
     a.cu_drafts = cu_drafts.data_ptr()
@@ -404,10 +408,11 @@ def adaptive_pick_k(hidden, w, bias, verify_ms, mode=0, out=None, stream=None):
         raise ValueError("w must be [H]")
     dev = hidden.device
     if out is None:
-        out = {"c": torch.empty((B, kmax), dtype=torch.float32, device=dev),
-               "a": torch.empty((B, kmax), dtype=torch.float32, device=dev),
-               "k": torch.empty(B, dtype=torch.int32, device=dev),
-               "cu": torch.empty(B + 1, dtype=torch.int32, device=dev)}
+        with _made_on(stream):
+            out = {"c": torch.empty((B, kmax), dtype=torch.float32, device=dev),
+                   "a": torch.empty((B, kmax), dtype=torch.float32, device=dev),
+                   "k": torch.empty(B, dtype=torch.int32, device=dev),
+                   "cu": torch.empty(B + 1, dtype=torch.int32, device=dev)}
     _check(lib().adaptive_pick_k(_ptr(hidden), _ptr(w), _dtype_code(hidden), float(bias), B, kmax,
                                  H, _ptr(verify_ms), verify_ms.numel() - 1, int(mode),
                                  _ptr(out["c"]), _ptr(out["a"]), _ptr(out["k"]), _ptr(out["cu"]),
@@ -425,7 +430,8 @@ def spec_accept_counters(accepted_len, status, cu_drafts, kmax, counts=None, str
     _dev(cu_drafts, "cu_drafts", torch.int32)
     B = status.numel()
     if counts is None:
-        counts = torch.zeros(2 * kmax + 1, dtype=torch.int64, device=status.device)
+        with _made_on(stream):
+            counts = torch.zeros(2 * kmax + 1, dtype=torch.int64, device=status.device)
     _dev(counts, "counts", torch.int64)
     if counts.numel() != 2 * kmax + 1:
         raise ValueError("counts must have 2 kmax + 1 entries")
@@ -600,7 +606,8 @@ def spec_verify_launch_info(B, V, kmax, draft_dtype=DTYPE_BF16, target_dtype=DTY
 def spec_philox_uniforms(seed, step, n_streams, n_slots, device="cuda", stream=None):
     """[n_streams, n_slots, 2] float64: (acceptance, sampling) uniforms of every (stream, slot)."""
     torch = _torch()
-    out = torch.empty((n_streams, n_slots, 2), dtype=torch.float64, device=device)
+    with _made_on(stream):
+        out = torch.empty((n_streams, n_slots, 2), dtype=torch.float64, device=device)
     _check(lib().spec_philox_uniforms(int(seed) & 0xFFFFFFFFFFFFFFFF, int(step) & 0xFFFFFFFFFFFFFFFF,
                                       n_streams, n_slots, _ptr(out), _stream(stream)))
     return out

@@ -46,7 +46,68 @@ def fork():
     return lambda stream: sv.spec_cache_fork(src, dst, *book, 8, stream=stream)
 
 
-CALLS = [attention, append, resize, fork]
+def verify_inputs():
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    cu = torch.tensor([0, 3, 5], dtype=torch.int32, device=DEV)
+    q, p = (torch.randn((n, 512), generator=g, device=DEV) for n in (5, 7))
+    x = torch.randint(0, 512, (5,), generator=g, device=DEV, dtype=torch.int32)
+    return cu, q, p, x, torch.ones(2, device=DEV)
+
+
+def verify(call, **kw):
+    def make():
+        cu, q, p, x, T = verify_inputs()
+        return lambda stream: call(cu, q, p, x, T, 3, 11, 0, diag=True, stream=stream, **kw)
+    make.__name__ = call.__name__
+    return make
+
+
+def verify_reduced():
+    cu, q, p, x, T = verify_inputs()
+    t2d = torch.arange(512, dtype=torch.int32, device=DEV)
+    return lambda stream: sv.spec_verify_block_reduced(cu, q, t2d, p, x, T, 3, 11, 0, stream=stream)
+
+
+def markov():
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    base, W1, W2 = (torch.randn(s, generator=g, device=DEV) for s in ((2, 3, 512), (512, 16), (16, 512)))
+    return base, torch.tensor([5, 9], dtype=torch.int32, device=DEV), W1, W2, torch.ones(2, device=DEV)
+
+
+def walk():
+    base, anchor, W1, W2, T = markov()
+    return lambda stream: sv.dspark_markov_walk(base, anchor, W1, W2, T, 4, 0, stream=stream)
+
+
+def bias():
+    base, anchor, W1, W2, _ = markov()
+    rows = base[:, 0].contiguous()
+    return lambda stream: {"out": sv.dspark_markov_bias(rows, anchor, W1, W2, stream=stream)}
+
+
+def pick():
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    hidden, w = torch.randn((3, 4, 64), generator=g, device=DEV), torch.randn(64, generator=g, device=DEV)
+    ms = torch.linspace(1.0, 2.0, 32, device=DEV)
+    return lambda stream: sv.adaptive_pick_k(hidden, w, 0.1, ms, stream=stream)
+
+
+def counters():
+    cu = torch.tensor([0, 3, 5], dtype=torch.int32, device=DEV)
+    accepted = torch.tensor([2, 1], dtype=torch.int32, device=DEV)
+    status = i32(2)
+    return lambda stream: {"counts": sv.spec_accept_counters(accepted, status, cu, 3, stream=stream)}
+
+
+def philox():
+    return lambda stream: {"out": sv.spec_philox_uniforms(1, 2, 3, 4, stream=stream)}
+
+
+CALLS = [attention, append, resize, fork, verify(sv.spec_verify_block), verify(sv.spec_verify_tokenwise),
+         verify(sv.spec_verify_block_static), verify_reduced, walk, bias, pick, counters, philox]
 
 
 @pytest.mark.parametrize("make", CALLS, ids=lambda m: m.__name__)
@@ -71,7 +132,7 @@ def test_buffers_are_made_on_the_calls_stream(make, monkeypatch):
 
 @pytest.mark.parametrize("make", CALLS, ids=lambda m: m.__name__)
 def test_a_busy_current_stream_does_not_matter(make):
-    want = {n: t.clone() for n, t in make()(None).items() if n != "workspace"}
+    want = {n: t.float() if t.dtype == torch.bfloat16 else t.clone() for n, t in make()(None).items() if n != "workspace"}
     call = make()
     side = torch.cuda.Stream()
     busy = torch.empty(1 << 28, device=DEV)
@@ -84,6 +145,6 @@ def test_a_busy_current_stream_does_not_matter(make):
         busy.add_(1.0)
     got = call(side)
     side.synchronize()
-    got = {n: t.cpu() for n, t in got.items() if n != "workspace"}
+    got = {n: t.float().cpu() if t.dtype == torch.bfloat16 else t.cpu() for n, t in got.items() if n != "workspace"}
     for n, t in want.items():
-        assert torch.equal(got[n], t.cpu()), n
+        assert got[n].numpy().tobytes() == t.cpu().numpy().tobytes(), n   # bit for bit, NaN too
