@@ -703,7 +703,22 @@ def _blocks_of(device, page_table, length, cu_drafts, rows, kmax):
 
 
 def _raw_stream(stream, device):
-    return _T._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    """The stream to launch on.  Launches go to the current device, so the tensors and the stream have to be its."""
+    current = _T._C._cuda_getDevice()
+    if device != current:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
+    if stream is None:
+        return _T._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the stream on cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _space(ws, device):
+    """(pointer, bytes) of a workspace."""
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor on the cache's device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kmax, scale, window=0, sinks=0,
@@ -733,11 +748,11 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
             out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
                    "status": torch.empty(B, dtype=torch.int32, device=q.device),
                    "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
-    ws = out["workspace"]
+    raw = _raw_stream(stream, device)
     rc = L.spec_paged_attention(_ATTENTION.pack(
         B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows, kp, vp,
-        _on(out["out"], "out", device, q.dtype, shape), _on(out["status"], "status", device, _I32, (B,)), ws.data_ptr(),
-        ws.numel()), _raw_stream(stream, device))
+        _on(out["out"], "out", device, q.dtype, shape), _on(out["status"], "status", device, _I32, (B,)),
+        *_space(out["workspace"], device)), raw)
     if rc != 0:
         _check(rc)
     return out
@@ -811,10 +826,10 @@ def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advan
         with _made_on(stream):
             out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
                    "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
-    ws = out["workspace"]
+    raw = _raw_stream(stream, device)
     rc = L.spec_cache_resize(_RESIZE.pack(
         B, page_size, num_pages, max_pages, shape[0], page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
-        _on(out["status"], "status", device, _I32, (B,)), ws.data_ptr(), ws.numel()), _raw_stream(stream, device))
+        _on(out["status"], "status", device, _I32, (B,)), *_space(out["workspace"], device)), raw)
     if rc != 0:
         _check(rc)
     return out
