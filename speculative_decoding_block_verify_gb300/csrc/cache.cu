@@ -9,6 +9,8 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "blocks.cuh"
 #include "host_util.h"
 
@@ -597,6 +599,21 @@ extern "C" size_t spec_cache_resize_workspace_bytes(int32_t B, int32_t num_pages
     return resize_workspace(B, num_pages);
 }
 
+// The kernel's limit of dynamic shared memory, once a device and to the largest batch's: it is the function's and not
+// the call's, so another host thread's smaller batch must not lower it before this one's launch.
+static cudaError_t resize_limit() {
+    static std::atomic<int> ready[64];
+    constexpr int per = (SPEC_MAX_STREAMS + kResizeCtas * kResizeThreads - 1) / (kResizeCtas * kResizeThreads);
+    constexpr int bytes = per * kResizeThreads * (int)sizeof(Planned);
+    static_assert(bytes <= 200 * 1024, "shared memory of an SM");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 64 && ready[dev].load(std::memory_order_acquire) != 0)) return e;
+    e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_release);
+    return e;
+}
+
 extern "C" int spec_cache_resize(const spec_resize_args* a, void* stream) {
     clear_error();
     if (a == nullptr) return set_error(SPEC_ERR_ARG, "spec_cache_resize: args is NULL");
@@ -621,12 +638,9 @@ extern "C" int spec_cache_resize(const spec_resize_args* a, void* stream) {
         return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_cache_resize");
     }
     const int per = (a->B + kResizeCtas * kResizeThreads - 1) / (kResizeCtas * kResizeThreads);
-    const size_t smem = (size_t)per * kResizeThreads * sizeof(Planned);   // up to 192 KB
+    const size_t smem = (size_t)per * kResizeThreads * sizeof(Planned);
     cudaError_t e = cudaSuccess;
-    if (smem > 40000) {
-        e = cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
-    }
+    if (smem > 40000 && (e = resize_limit()) != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
     e = launch_after(resize_kernel, dim3(kResizeCtas), dim3(kResizeThreads), smem, s, *a, per);
     if (e != cudaSuccess) return set_cuda_error(e, "spec_cache_resize");
     // as many CTAs as the largest number of copies (one per stream) can keep busy, two per SM at most

@@ -1,8 +1,12 @@
 """The cache calls at the ends of the sizes that they accept."""
 
+import threading
+
+import numpy as np
 import pytest
 
 import speculative_decoding_block_verify_gb300 as sv
+from tests import cache_reference as ref
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -57,3 +61,56 @@ def test_lengths_just_below_2_31(D, dtype, back):
     length += back
     out = sv.spec_paged_attention(q, k, v, table, length, None, kmax, D ** -0.5, window=window, sinks=sinks)
     assert out["status"].tolist() == [9] and torch.isnan(out["out"].float()).all()
+
+
+def test_batches_of_different_sizes_from_several_threads():
+    # above 12,288 streams the kernel needs its limit of shared memory raised, which is one for all threads
+    failed = []
+
+    def work(B):
+        k = torch.zeros((1, 64, 1, 8, 8), dtype=torch.bfloat16, device=DEV)
+        args = (k, k.clone(), i32(B, 1) - 1, i32(B), i32(B), i32(64))
+        room = i32(B)
+        out = sv.spec_cache_resize(*args, room=room)
+        for _ in range(2000):
+            try:
+                sv.spec_cache_resize(*args, room=room, out=out)
+            except sv.SpecError as e:
+                failed.append((B, str(e)))
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (16000, 65000, 30000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), failed[0])
+
+
+@pytest.mark.parametrize("B,width", [(12289, 3), (20001, 2), (65535, 1)])
+def test_resize_of_many_streams(B, width):
+    # against the page-by-page model; several streams a thread, and shared memory above the default limit
+    P, rng = 8, np.random.default_rng(B)
+    pages = int(1.2 * B)
+    k = torch.arange(pages, dtype=torch.float32, device=DEV).view(1, pages, 1, 1, 1).expand(1, pages, 1, P, 8).contiguous()
+    v = -k
+    book = (i32(B, width) - 1, i32(B), i32(B), i32(pages))
+    model = ref.Book(book[0].tolist(), [0] * B, [0] * B, [0] * pages, P, range(pages))
+
+    def same(advance, room):
+        d = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+        got = sv.spec_cache_resize(k, v, *book, advance=d(advance), room=d(room))["status"].tolist()
+        assert got == model.resize(advance, room)
+        for t, m in zip(book, (model.table, model.held, model.length, model.refs)):
+            assert t.tolist() == m
+        contents = torch.tensor(model.contents, dtype=torch.float32, device=DEV)
+        assert torch.equal(k[0, :, 0, 0, 0], contents) and torch.equal(v, -k)
+
+    same(None, (rng.random(B) < 0.5).astype(int).tolist())
+    same([int(h > 0) for h in model.held], None)
+    src = [b for b in range(B) if model.length[b]][:300]
+    dst = [b for b in range(B) if not model.length[b]][-300:]
+    d = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    assert sv.spec_cache_fork(d(src), d(dst), *book, P)["status"].tolist() == model.fork(src, dst)
+    same(None, rng.integers(0, (width - 1) * P + 4, B).tolist())
+    same([-n for n in model.length], [1] * B)
