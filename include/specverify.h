@@ -476,7 +476,7 @@ void spec_cost_curve_destroy(void* curve);
  * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before
  * they meet the values, and the same rounded weights are summed.  A value that is not finite at a
  * position that one row of a block sees may reach the block's earlier rows; one that no row sees
- * reaches none.  In float32 an infinite key or value of a head up to 128 counts as NaN.  The result does not depend on the call before it, and is the same from run to run.
+ * reaches none.  In float32 an infinite query, key or value of a head up to 128 counts as NaN.  The result does not depend on the call before it, and is the same from run to run.
  * workspace: spec_paged_attention_workspace_bytes(args) bytes, 16-byte aligned, its first
  * SPEC_ATTENTION_ZERO_BYTES zero-filled once before its first use (a call leaves them so, except one
  * that reports TIMEOUT); calls that share it must be ordered.

@@ -24,7 +24,7 @@
 // faster: one piece of code for keys and values (122 -> 109 us for 16 streams of 2,100 and 5 tokens of 4 rows a key head), a
 // subtraction of bf16 from float32 in one instruction (107 -> 103), waits that look for a given-up one every 16th time
 // (103 -> 101), one wait less (98 -> 96), and products partly unrolled.  The same kernel with keys and values in warps of their own took 123 us.
-// An infinite key or value counts as NaN here (the difference to its rounding is).
+// An infinite query, key or value counts as NaN here (the difference to its rounding is).
 
 #include <atomic>
 
@@ -76,9 +76,10 @@ __device__ __forceinline__ float2 less(float2 x, uint32_t w) {
         : "r"(w), "f"(x.x), "f"(x.y));
     return y;
 }
-// Two floats as three bf16 pairs.
+// Two floats as three bf16 pairs.  The first rounding stops at bf16's largest number: a finite float above it, rounded to
+// infinity, would leave NaN.
 __device__ __forceinline__ void split(float2 x, uint32_t (&w)[kPlanes]) {
-    w[0] = pack_bf16(x.x, x.y);
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(x.y), "f"(x.x));
     x = less(x, w[0]);
     w[1] = pack_bf16(x.x, x.y);
     x = less(x, w[1]);
