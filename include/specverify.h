@@ -480,7 +480,8 @@ void spec_cost_curve_destroy(void* curve);
  * workspace: spec_paged_attention_workspace_bytes(args) bytes, 16-byte aligned, its first
  * SPEC_ATTENTION_ZERO_BYTES zero-filled once before its first use (a call leaves them so, except one
  * that reports TIMEOUT); calls that share it must be ordered.
- * Errors: SPEC_ERR_ARG (NULL pointer, a pool or out that is not 16-byte aligned, scale not finite),
+ * Errors: SPEC_ERR_ARG (NULL pointer, a pool or out that is not 16-byte aligned, scale
+ * or scale * log2(e) not finite),
  * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (a size outside the limits, Hq not a multiple of
  * Hkv or more than 128 times it, q_row_stride < Hq * D, q_rows < 0 or below B * (kmax + 1) without cu_drafts, window or sinks < 0, max_pages * page_size >= 2^31,
  * in bf16 num_pages * Hkv >= 2^31 - 1), SPEC_ERR_WORKSPACE,

@@ -530,7 +530,8 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
     if (((uintptr_t)a->k_pages | (uintptr_t)a->v_pages) & 15)
         return set_error(SPEC_ERR_ARG, "spec_paged_attention: the pool is not 16-byte aligned");
     if ((uintptr_t)a->out & 15) return set_error(SPEC_ERR_ARG, "spec_paged_attention: out is not 16-byte aligned");
-    if (!std::isfinite(a->scale)) return set_error(SPEC_ERR_ARG, "spec_paged_attention: scale is not finite");
+    if (!std::isfinite(a->scale) || !std::isfinite((float)((double)a->scale * kLog2e)))   // scores are taken to base 2
+        return set_error(SPEC_ERR_ARG, "spec_paged_attention: scale is not finite");
     int sms = 0;
     AttnParams p;
     if ((rc = sm_count(&sms)) != SPEC_OK) return rc;

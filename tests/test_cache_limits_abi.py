@@ -29,3 +29,9 @@ def test_append_reserved_errors(L):
     for change, code in [(dict(dtype=-1), -2), (dict(kmax=33), -3), (dict(page=20), -3), (dict(rows=-1), -3), (dict(kp=0), -1)]:
         assert L.spec_cache_append_reserved(append(**change), P, None) == code, change
     assert L.spec_cache_append_reserved(append(B=0), None, None) == 0
+
+
+def test_scales_that_overflow_to_base_2(L):
+    for scale, ok in [(2.3e38, True), (2.5e38, False), (-3.4e38, False), (-2.3e38, True)]:
+        rc = L.spec_paged_attention(attention(scale=scale, ws=0), None)
+        assert (rc in (-4, -6)) if ok else rc == -1, (scale, rc)
