@@ -625,11 +625,13 @@ _RESIZE = struct.Struct("@5i q 10P N")           # spec_resize_args
 _T = None       # torch, once a cache call has run
 _I32 = None
 _CODES = {}     # dtype -> SPEC_DTYPE_*
+_ONE_DEVICE = False   # every CUDA tensor and stream is the current device's
 
 
 def _cache_torch():
-    global _T, _I32, _CODES
+    global _T, _I32, _CODES, _ONE_DEVICE
     import torch
+    _ONE_DEVICE = torch.cuda.device_count() == 1
     _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
     _I32 = torch.int32
     _T = torch
@@ -704,21 +706,20 @@ def _blocks_of(device, page_table, length, cu_drafts, rows, kmax):
 
 def _raw_stream(stream, device):
     """The stream to launch on.  Launches go to the current device, so the tensors and the stream have to be its."""
-    current = _T._C._cuda_getDevice()
-    if device != current:
-        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
-    if stream is None:
-        return _T._C._cuda_getCurrentRawStream(device)
-    if stream.device_index != device:
-        raise ValueError(f"the tensors are on cuda:{device}, the stream on cuda:{stream.device_index}")
-    return stream.cuda_stream
+    if not _ONE_DEVICE:
+        current = _T._C._cuda_getDevice()
+        if device != current:
+            raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"the tensors are on cuda:{device}, the stream on cuda:{stream.device_index}")
+    return _T._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _space(ws, device):
     """(pointer, bytes) of a workspace."""
     if ws.get_device() != device or not ws.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor on the cache's device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kmax, scale, window=0, sinks=0,
@@ -748,11 +749,11 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
             out = {"out": torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device),
                    "status": torch.empty(B, dtype=torch.int32, device=q.device),
                    "workspace": torch.zeros(max(int(need), 16), dtype=torch.uint8, device=q.device)}
-    raw = _raw_stream(stream, device)
+    ws, size = _space(out["workspace"], device)
     rc = L.spec_paged_attention(_ATTENTION.pack(
         B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows, kp, vp,
         _on(out["out"], "out", device, q.dtype, shape), _on(out["status"], "status", device, _I32, (B,)),
-        *_space(out["workspace"], device)), raw)
+        ws, size), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out
@@ -826,10 +827,10 @@ def spec_cache_resize(k_pool, v_pool, page_table, held, length, ref_count, advan
         with _made_on(stream):
             out = {"status": torch.empty(B, dtype=torch.int32, device=page_table.device),
                    "workspace": torch.empty(need, dtype=torch.uint8, device=page_table.device)}
-    raw = _raw_stream(stream, device)
+    ws, size = _space(out["workspace"], device)
     rc = L.spec_cache_resize(_RESIZE.pack(
         B, page_size, num_pages, max_pages, shape[0], page_bytes, ap, mp, tp, hp, lp, rp, kp, vp,
-        _on(out["status"], "status", device, _I32, (B,)), *_space(out["workspace"], device)), raw)
+        _on(out["status"], "status", device, _I32, (B,)), ws, size), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out

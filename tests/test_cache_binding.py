@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 def test_launches_go_to_the_current_device(monkeypatch):
     fake = SimpleNamespace(_C=SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda d: 100 + d))
     monkeypatch.setattr(sv, "_T", fake)
+    monkeypatch.setattr(sv, "_ONE_DEVICE", False, raising=False)
     side = SimpleNamespace(device_index=0, cuda_stream=7)
     assert sv._raw_stream(None, 0) == 100 and sv._raw_stream(side, 0) == 7
     with pytest.raises(ValueError, match="current device is cuda:0"):
@@ -20,6 +21,9 @@ def test_launches_go_to_the_current_device(monkeypatch):
         sv._raw_stream(SimpleNamespace(device_index=1, cuda_stream=7), 1)
     with pytest.raises(ValueError, match="stream on cuda:1"):
         sv._raw_stream(SimpleNamespace(device_index=1, cuda_stream=7), 0)
+    # with a single device there is nothing to compare
+    monkeypatch.setattr(sv, "_ONE_DEVICE", True)
+    assert sv._raw_stream(None, 0) == 100 and sv._raw_stream(side, 0) == 7
 
 
 def test_a_workspace_has_to_be_on_the_device():
