@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(kFloatThreads, R < 48 ? 2 : 1) attention_float
         const int32_t* table = p.a.page_table + (int64_t)w.b * p.a.max_pages;
         // where the thread's position of tile t lies in the pool, or -1
         auto look_up = [&](int t) -> int64_t {
+            if (t >= w.t1) return -1;
             const int j = tile_start(w.it, t) + my_row;
             // positions that no row of the item sees are zeros, whatever the cache holds there
-            if (t >= w.t1 || j >= w.it.high || (j < w.it.low && j >= w.it.sink)) return -1;
+            if (j >= w.it.high || (j < w.it.low && j >= w.it.sink)) return -1;
             const int page = *(table + (j >> p.page_shift));
             if ((unsigned)page >= (unsigned)p.a.num_pages) return -1;
             return (((int64_t)page * p.a.Hkv + w.h) * p.a.page_size + (j & (p.a.page_size - 1))) * D;

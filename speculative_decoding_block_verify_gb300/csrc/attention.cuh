@@ -56,10 +56,8 @@ struct Item {
     int sink;
     int sink_tiles, first_tile, tiles;
 };
-// Tiles of n positions, and the first position of a tile.  A table row may reach to 2^31 - 8 positions: a number rounded up to
-// whole tiles, and the start of a tile that is looked for past the last one, do not fit an int.
+// Tiles of n positions.  A table row may reach to 2^31 - 8 positions: rounded up to whole tiles they do not fit an int.
 __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
-__device__ __forceinline__ int tile_at(int tile) { return (int)((unsigned)tile * kTile); }
 __device__ __forceinline__ Item make_item(const AttnParams& p, int len, int block_rows, int group) {
     Item it;
     it.r0 = group * p.rows;
@@ -73,9 +71,12 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int len, int bloc
     it.tiles = it.sink_tiles + tiles_of(it.high) - it.first_tile;
     return it;
 }
-// First position of tile t of the item.
+// First position of tile t of the item.  Past the last tile it may not fit an int: the second form is for tiles that may be.
 __device__ __forceinline__ int tile_start(const Item& it, int t) {
-    return tile_at(t < it.sink_tiles ? t : it.first_tile + t - it.sink_tiles);
+    return (t < it.sink_tiles ? t : it.first_tile + t - it.sink_tiles) * kTile;
+}
+__device__ __forceinline__ int tile_start_past(const Item& it, int t) {
+    return (int)((unsigned)(t < it.sink_tiles ? t : it.first_tile + t - it.sink_tiles) * kTile);
 }
 
 __device__ __forceinline__ bool length_ok(const AttnParams& p, int len, int n) {

@@ -458,7 +458,7 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.s_empty);   // the next tile's S may be written
                 const bool clean = j0 + kTile - 1 <= at_first &&
-                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 <= p.a.sinks - kTile);
+                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
                 if (!clean) {
                     const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll

@@ -125,7 +125,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& p, const CUtensorMap
     int z_now = 0, z_next = 0, z_base = 0;
     auto look_up = [&](int t) {
         const int tile = t + lane / pages;
-        const int j = tile_start(w.it, tile) + (lane % pages) * box;
+        const int j = tile_start_past(w.it, tile) + (lane % pages) * box;
         int page = -1;
         if (tile < w.t1 && j < w.it.high && (j > w.it.low - box || j < w.it.sink))
             page = p.a.page_table[(int64_t)w.b * p.a.max_pages + (j >> p.page_shift)];
@@ -350,7 +350,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, TcShared& sh) 
                 tc_wait_ld();
                 // a tile that every row sees whole needs no mask
                 const bool clean = j0 + kTile - 1 <= at_first &&
-                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 <= p.a.sinks - kTile);
+                                   (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kTile <= p.a.sinks);
                 if (!clean) {
                     const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll

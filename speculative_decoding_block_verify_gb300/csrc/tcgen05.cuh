@@ -15,7 +15,7 @@ struct Segment {
     int32_t len, r0, rows, head;
     int32_t whole, slot;       // the whole item, or the slot of its part
     int64_t row0;              // the block's first packed row
-    __device__ __forceinline__ int start(int t) const { return tile_at(t < sink_tiles ? t : first_tile + t - sink_tiles); }
+    __device__ __forceinline__ int start(int t) const { return (t < sink_tiles ? t : first_tile + t - sink_tiles) * kTile; }
 };
 constexpr int kSegments = 4;   // told ahead
 __device__ __forceinline__ Segment segment_of(const AttnParams& p, const Walk& w, int cta) {
