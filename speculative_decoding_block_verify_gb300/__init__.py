@@ -17,7 +17,8 @@ Entry points (same names as the C ABI):
 * ``SpecPipeline``           - pick k -> ragged verify -> counters as one CUDA graph
 * ``CostCurve``              - the online verify-cost table adaptive_pick_k reads
 * ``spec_paged_attention``   - a verify block's attention over a paged key-value cache
-* ``spec_cache_append``      - the block's keys and values into their pages
+* ``spec_cache_append``      - the block's keys and values into their pages (``reserved``: of the streams that
+                               spec_cache_resize had room for)
 * ``spec_cache_resize``      - pages reserved before a block and given back after its verify
 * ``spec_cache_fork``        - a stream's pages shared with other streams
 * ``spec_philox_uniforms``   - the verify calls' uniforms (for checking)
@@ -730,7 +731,8 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     page_size, D] of q's dtype (float32/bf16), page_table [B, max_pages], length [B] (tokens before the
     block) and cu_drafts [B + 1] int32 (None: kmax drafts each; kmax = 0 is plain decoding).  window > 0
     keeps the last ``window`` positions of each row and the first ``sinks`` of its stream.  Returns
-    (and reuses) ``out`` with out [rows, Hq, D], status [B], workspace."""
+    (and reuses) ``out`` with out [rows, Hq, D], status [B], workspace.  A call that reports TIMEOUT leaves a mark in the
+    workspace: the calls after it report TIMEOUT as well until the first 256 bytes are zeroed."""
     torch = _T or _cache_torch()
     device, code, kp, vp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
     shape = q.shape
@@ -741,7 +743,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     L = _lib or lib()
     if out is None:
-        # the first 256 bytes of the workspace start at zero and every call leaves them so
+        # the first 256 bytes of the workspace start at zero and every call leaves them so (but one that reports TIMEOUT)
         need = L.spec_paged_attention_workspace_bytes(_ATTENTION.pack(
             B, kmax, Hq, Hkv, D, page_size, num_pages, max_pages, code, window, sinks, scale, cu, lp, tp, qp, stride, rows,
             kp, vp, 0, 0, 0, 0))

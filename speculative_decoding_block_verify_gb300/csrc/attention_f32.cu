@@ -4,7 +4,8 @@
 // leave.  A product of two such sums needs the six terms x0 y0, x0 y1, x1 y0, x1 y1, x0 y2, x2 y0 (the other three are
 // below 2^-24 of x0 y0), each exact in float32, so six bf16 products with a float32 accumulator stand for a float32
 // product.  At M = 128 a tile of 64 positions costs 48 of 32 cycles and 24 of 64, 3,072 tensor cycles, against about 2,800
-// that its 64 KB take from memory; on the float pipes 32 rows alone take 8,192.
+// that its 64 KB take from memory; on the float pipes (128 products a cycle) 32 rows take 4,096 and 128 rows 16,384.  The price here is the same for
+// any number of rows: up to about 20 the float pipes alone would need less (8 rows 1,024 cycles), which is not built for these heads.
 //
 // One CTA per SM, sixteen warps: copies (warp 15, beside those of the softmax's warps that have rows last) bring pages as they lie into a ring; warps 4 to 11 split the item's rows of
 // Q into tensor memory and keys and values into swizzled bf16 planes (zeros where no row of the item sees a position,

@@ -28,6 +28,8 @@ namespace cg = cooperative_groups;
 // With resize's statuses, a stream that it had no room for is passed over: where a copy was not to be had, the table still
 // has the shared page.  Of that page's holders one at most was told OK; it is passed over too where one that was not has
 // tokens behind its own there (it was rolled back further).
+// Every CTA checks the offsets up to its own stream, so the work of all grows with the square of the streams: one token each of one
+// head of 64, from Python, takes 15.5 us for 1,024 streams (13.5 without offsets), 26 (18) for 4,096, 139 (38) for 16,384.
 constexpr int kAppendThreads = 256;
 
 template <typename U>   // the unit moved by a thread: uint4, or one element
@@ -333,7 +335,8 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
         }
         cluster.sync();
         // A copy for every holder that asks, but the lowest one where all of them ask.  The askers (a fork's
-        // continuations, next to one another) are spread over the cluster's warps.
+        // continuations, next to one another) are spread over the cluster's warps; each looks through all streams:
+        // from Python 18 us for 129 askers of 256 streams, 29 for 513 of 1,024, 133 for 2,049 of 4,096, 1,630 for 8,193 of 16,384.
         for (int b = rank * (kResizeThreads / 32) + (tid >> 5); b < a.B; b += kResizeCtas * kResizeThreads / 32) {
             const int p = __ldcg(w.ask + b);
             if (p < 0) continue;
@@ -496,7 +499,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const spec_res
 // ---------------------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------------------
-// One CTA per pair.  A destination is nobody's source, so the rows that are read are not written.
+// One CTA per pair.  A destination is nobody's source, so the rows that are read are not written.  Each CTA looks through all
+// pairs for that: 14 us from Python for 512 pairs, 22 for 2,048, 50 for 8,192.
 constexpr int kForkThreads = 256;
 __global__ void __launch_bounds__(kForkThreads)
     fork_kernel(const int32_t* src, const int32_t* dst, int n, int B, int page_size, int num_pages, int max_pages,

@@ -17,8 +17,8 @@ calls; nothing is timed or checked here - bench.py and the tests do that):
   pick_batch_adaptive128   the same in batch mode (the sort of the entries in pick_batch_kernel)
   pipeline_adaptive128     SpecPipeline.launch (pick -> verify -> counters -> step + 1)
   cache_NAME               case NAME of perf/operators.py: cache_verify_64 and cache_window_64
-                           (attention_tc_kernel, join_kernel), cache_window_f32
-                           (attention_f32_kernel), cache_append_256, cache_resize_1024, ...
+                           (attention_tc_kernel, attention_join_kernel; attention_join_spread_kernel
+                           in cache_verify_long), cache_window_f32 (attention_f32_kernel), cache_append_256, cache_resize_1024, ...
 
 A profiler filters the launches it captures by kernel name and skips the warm-up calls.
 """
