@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 // One CTA column per stream: the stream's rows are known from two words of cu_drafts, so no row
 // searches for its stream.  A thread moves 16 bytes of K and of V (or one element of each, where a
 // base or a row stride is not a multiple of 16 bytes).  Bound by latency at decode sizes (one stream's block: 2.8 us);
-// 256 streams with up to 33 tokens of 8 heads of 128 (52.8 MB): 9.2 to 10.8 us by the box, 4.9 to 5.7 TB/s.
+// 256 streams with up to 33 tokens of 8 heads of 128 (52.8 MB): 9.2 to 10.8 us from card to card, 4.9 to 5.7 TB/s.
 // With resize's statuses, a stream that it had no room for is passed over: where a copy was not to be had, the table still
 // has the shared page.  Of that page's holders one at most was told OK; it is passed over too where one that was not has
 // tokens behind its own there (it was rolled back further).
