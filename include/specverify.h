@@ -14,6 +14,10 @@
  *   spec_cache_append      - the block's keys and values written into their pages
  *   spec_cache_resize      - pages reserved before a block, and given back after its verify
  *   spec_cache_fork        - a stream's pages shared with another stream
+ * And three for the prompt before it:
+ *   spec_prompt_attention  - causal attention over whole prompts
+ *   spec_cache_append_rotated - a prompt's (or a block's) keys rotated into their pages, its queries rotated on the way
+ *   spec_rotate            - rotary positions of packed rows
  * Sources (web pages, cited by title and section):
  *   [P1] "MTP, DSpark and Block Verification, Explained: Six Tokens per Step" (al-engr.com)
  *   [P2] "MTP Heads and Confidence Heads: Linking Three Self-Drafting Routes into One Chain"
@@ -62,6 +66,12 @@ extern "C" {
 /* dtypes */
 #define SPEC_DTYPE_F32 0
 #define SPEC_DTYPE_BF16 1
+
+/* scalings of rotary frequencies */
+#define SPEC_ROTARY_PLAIN 0
+#define SPEC_ROTARY_LINEAR 1
+#define SPEC_ROTARY_NTK 2
+#define SPEC_ROTARY_YARN 3
 
 /* host-visible return codes */
 #define SPEC_OK 0
@@ -514,6 +524,40 @@ int spec_paged_attention(const spec_attention_args* args, void* stream);
 size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
 
 /*
+ * spec_prompt_attention - causal softmax attention over whole prompts, packed one behind the other.
+ * Prompt b has the rows cu_rows[b] .. cu_rows[b + 1] - 1 of q, k and v (maybe none); its row i sees the rows j <= i of its own, and with
+ * window > 0 only those with j > i - window or j < sinks (as in spec_paged_attention, which carries on behind the prompt):
+ *   out[i, h] = sum_j e_j v[j, g] / sum_j e_j,   e_j = exp(scale q[i, h] . k[j, g]),   g = h / (Hq / Hkv).
+ * q [rows, Hq, D], k and v [rows, Hkv, D] with row strides in elements (slices of a wider projection), out [rows, Hq, D] dense, one dtype.
+ * cu_rows [B + 1] int32 (NULL: B prompts of rows / B).  Rows behind the last prompt's are neither read nor written.
+ * status [B]: SPEC_ST_OK, or BAD_OFFSETS for the first prompt whose offsets are broken (cu_rows[0] not 0, a negative count, rows
+ * beyond `rows`) and all behind it, whose rows are not written.  Rows that a bounded wait left unfinished are NaN.
+ * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before they meet the values, and the same
+ * rounded weights are summed.  A value that is not finite reaches the rows that see it and may reach earlier rows of its prompt, up to 255
+ * tokens before it; it reaches no other prompt.  In float32 infinite queries, keys and values count as NaN.  Results are the same from run to run.
+ * Errors: SPEC_ERR_ARG (NULL pointer, scale or scale * log2(e) not finite, q, k, v, out or a row stride not a multiple of 16 bytes),
+ * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (B outside [0, SPEC_MAX_STREAMS], Hq not a multiple of Hkv or more than 128 times it, D not a
+ * multiple of 8 up to SPEC_MAX_HEAD, in float32 up to 128, a row stride below heads * D, rows outside [0, 2^31), without cu_rows not a multiple of B, window or sinks
+ * < 0), SPEC_ERR_CUDA.  B == 0 launches nothing.
+ */
+typedef struct {
+    int32_t B, Hq, Hkv, D;
+    int32_t dtype;
+    int32_t window, sinks;
+    float scale;
+    int64_t rows;
+    const int32_t* cu_rows;      /* [B + 1] or NULL */
+    const void* q;               /* [rows, Hq, D] */
+    const void* k;               /* [rows, Hkv, D] */
+    const void* v;
+    int64_t q_row_stride, k_row_stride, v_row_stride;   /* elements */
+    void* out;                   /* [rows, Hq, D] */
+    int32_t* status;             /* [B] */
+} spec_prompt_args;
+
+int spec_prompt_attention(const spec_prompt_args* args, void* stream);
+
+/*
  * spec_cache_append - the block's new keys and values into their pages.
  *   k_pages[page_table[b, p / page_size], h, p % page_size] = k[row, h],   p = length[b] + i
  * and the same for v.  k, v [rows, Hkv, D] with row strides in elements (slices of a wider
@@ -551,6 +595,95 @@ int spec_cache_append(const spec_append_args* args, void* stream);
  * Errors: also SPEC_ERR_ARG for a NULL reserved.
  */
 int spec_cache_append_reserved(const spec_append_args* args, const int32_t* reserved, void* stream);
+
+/*
+ * Rotary positions.  The first `dim` elements of a head are dim / 2 pairs, (j, j + dim / 2) or, interleaved, (2 j, 2 j + 1).
+ * At position p pair j turns by the angle p f_j and is multiplied by `magnitude`:
+ *   a' = magnitude (a cos(p f_j) - b sin(p f_j)),   b' = magnitude (b cos(p f_j) + a sin(p f_j));
+ * the rest of the head stays as it is.  The calls take the frequencies as turns [dim / 2] in device memory: 2^64 f_j / 2 pi
+ * modulo 2^64, so that position times turns modulo 2^64 is the exact fraction of a turn.  Angles are therefore as good at far positions as at near ones,
+ * and negative positions turn back.  Arithmetic is float32, rounded once to the output's type.
+ *
+ * spec_rotary_frequencies - f_j = base^(-2 j / dim), scaled for contexts `factor` times as long, into frequency [dim / 2] (host):
+ *   SPEC_ROTARY_PLAIN   as they are;
+ *   SPEC_ROTARY_LINEAR  f_j / factor (position interpolation);
+ *   SPEC_ROTARY_NTK     with base factor^(dim / (dim - 2)) instead of base;
+ *   SPEC_ROTARY_YARN    g f_j + (1 - g) f_j / factor, g = (r - slow) / (fast - slow) cut off at 0 and 1, where r = original
+ *                       f_j / 2 pi is how often the pair turns in the original context (Peng et al. 2023, with slow 1 and fast 32).
+ * magnitude (host): 0.1 ln(factor) + 1 for YARN, otherwise 1.  Errors: SPEC_ERR_ARG (NULL, an unknown scaling, base not
+ * finite and above 1, and of what the scaling uses factor below 1, original below 1, fast not above slow, or one not finite),
+ * SPEC_ERR_SHAPE (dim odd or outside [2, SPEC_MAX_HEAD]).
+ * spec_rotary_turns - turns [n] (host) of any finite frequencies [n] (host).  Errors: SPEC_ERR_ARG, SPEC_ERR_SHAPE (n outside
+ * [1, SPEC_MAX_HEAD / 2]).  Neither call touches a device.
+ */
+int spec_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor, double original, double slow, double fast,
+                            double* frequency, float* magnitude);
+int spec_rotary_turns(const double* frequency, int32_t n, uint64_t* turns);
+
+/*
+ * spec_rotate - rows [rows, heads, D] turned by their positions [rows] int32 (any values).
+ * x and out have row strides in elements (slices of a wider projection); out may be x itself (with the same stride), and overlaps it in no
+ * other way.  Queries and keys that lie beside each other are one call with the heads of both.
+ * Errors: SPEC_ERR_ARG (NULL pointer, turns not 8-byte aligned, magnitude not finite), SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (heads outside [1, 4096], D not a multiple of 8 up to
+ * SPEC_MAX_HEAD, dim odd or outside [2, D], rows outside [0, 2^31), a row stride below heads * D, in place with two strides),
+ * SPEC_ERR_CUDA.  rows == 0 launches nothing.
+ */
+typedef struct {
+    int32_t heads, D, dim, interleaved;
+    int32_t dtype;
+    float magnitude;
+    int64_t rows;
+    const uint64_t* turns;       /* [dim / 2] */
+    const int32_t* positions;    /* [rows] */
+    const void* x;               /* [rows, heads, D] */
+    int64_t x_row_stride;        /* elements */
+    void* out;
+    int64_t out_row_stride;
+} spec_rotate_args;
+
+int spec_rotate(const spec_rotate_args* args, void* stream);
+
+/*
+ * spec_cache_append_rotated - spec_cache_append with the rotation on the way, for blocks and for whole prompts.
+ * Token i of stream b stands at position p = length[b] + i.  Its key goes turned to its place in k_pages (and, with k_out, to
+ * the packed row as well: what spec_prompt_attention reads), its value as it is to v_pages, and its queries turned to q_out.
+ *   - Rows: stream b has the packed rows cu[b] + b * extra_rows up to cu[b + 1] + (b + 1) * extra_rows (not included), at most max_rows of them.
+ *     extra_rows = 0: cu is the rows' own prefix sum, and a stream may have none; extra_rows = 1: cu is cu_drafts, a block being one
+ *     token more than its drafts, any number of them.  cu NULL: max_rows each.  Rows behind the last stream's are left alone.
+ *   - reserved [B] (or NULL): the status of the spec_cache_resize that made the room, as in spec_cache_append_reserved.
+ *   - Hq = 0: no queries.  q_out may be q, and k_out may be k (with the same strides); otherwise nothing overlaps.
+ * status [B]: SPEC_ST_OK, BAD_OFFSETS, the entry of reserved, BAD_LENGTH, NO_PAGES as in spec_cache_append_reserved (nothing of
+ * the stream is written, its rows of q_out and k_out neither), BAD_PAGE (rows whose page is not in the pool are written to q_out and k_out only).
+ * Errors: SPEC_ERR_ARG (NULL pointer, a pool that is not 16-byte aligned, turns not 8-byte aligned, magnitude not finite), SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (as in spec_cache_append and
+ * spec_rotate; Hq outside [0, 1024], max_rows < 0, extra_rows not 0 or 1, rows outside [0, 2^31) or below B * max_rows without cu),
+ * SPEC_ERR_CUDA.  B == 0 launches nothing.
+ */
+typedef struct {
+    int32_t B, max_rows, extra_rows;
+    int32_t Hq, Hkv, D;
+    int32_t page_size, num_pages, max_pages;
+    int32_t dtype;
+    int32_t dim, interleaved;
+    float magnitude;
+    const uint64_t* turns;       /* [dim / 2] */
+    const int32_t* cu;           /* [B + 1] or NULL */
+    const int32_t* length;       /* [B] */
+    const int32_t* page_table;   /* [B, max_pages] */
+    const int32_t* reserved;     /* [B] or NULL */
+    const void* q;               /* [rows, Hq, D] */
+    const void* k;               /* [rows, Hkv, D] */
+    const void* v;
+    int64_t q_row_stride, k_row_stride, v_row_stride;   /* elements */
+    int64_t rows;                /* rows of q, k and v; a stream beyond them is BAD_OFFSETS */
+    void* q_out;                 /* [rows, Hq, D] */
+    void* k_out;                 /* [rows, Hkv, D] or NULL */
+    int64_t q_out_row_stride, k_out_row_stride;
+    void* k_pages;               /* [num_pages, Hkv, page_size, D] */
+    void* v_pages;
+    int32_t* status;             /* [B] */
+} spec_append_rotated_args;
+
+int spec_cache_append_rotated(const spec_append_rotated_args* args, void* stream);
 
 /*
  * spec_cache_resize - gives every stream the pages it needs, no more.

@@ -21,6 +21,9 @@ Entry points (same names as the C ABI):
                                spec_cache_resize had room for)
 * ``spec_cache_resize``      - pages reserved before a block and given back after its verify
 * ``spec_cache_fork``        - a stream's pages shared with other streams
+* ``spec_prompt_attention``  - causal attention over whole prompts, packed one behind the other
+* ``spec_rotate``            - rotary positions of packed rows (``RotaryTable``: their frequencies)
+* ``spec_cache_append_rotated`` - a block's or a whole prompt's keys rotated into their pages, its queries rotated on the way
 * ``spec_philox_uniforms``   - the verify calls' uniforms (for checking)
 
 Every call takes ``stream`` (None: the current one).  What it makes for the caller when ``out`` is None belongs to that
@@ -41,7 +44,8 @@ __all__ = [
     "adaptive_pick_k", "spec_accept_counters", "acceptance_rates", "SpecPipeline", "CostCurve",
     "spec_philox_uniforms", "spec_verify_launch_info",
     "spec_verify_workspace_bytes", "spec_verify_block_static",
-    "spec_paged_attention", "spec_cache_append", "spec_cache_resize", "spec_cache_fork", "lib", "lib_path", "SpecError",
+    "spec_paged_attention", "spec_cache_append", "spec_cache_resize", "spec_cache_fork", "spec_prompt_attention",
+    "RotaryTable", "spec_rotate", "spec_cache_append_rotated", "lib", "lib_path", "SpecError",
     "DTYPE_F32", "DTYPE_BF16", "STATUS_NAMES", "DIAG_COLS",
 ]
 
@@ -63,6 +67,7 @@ EXPORTED = ["dspark_markov_bias", "dspark_markov_walk", "dspark_markov_walk_work
             "spec_cost_curve_table", "spec_cost_curve_upload", "spec_cost_curve_destroy",
             "spec_paged_attention", "spec_paged_attention_workspace_bytes", "spec_cache_append",
             "spec_cache_append_reserved", "spec_cache_resize", "spec_cache_resize_workspace_bytes", "spec_cache_fork",
+            "spec_prompt_attention", "spec_rotary_frequencies", "spec_rotary_turns", "spec_rotate", "spec_cache_append_rotated",
             "spec_last_error", "spec_version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -167,6 +172,12 @@ def lib():
     L.spec_cache_resize_workspace_bytes.argtypes = [i32, i32]
     L.spec_cache_resize_workspace_bytes.restype = ctypes.c_size_t
     L.spec_cache_fork.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    f64 = ctypes.c_double
+    L.spec_prompt_attention.argtypes = [vp, vp]
+    L.spec_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    L.spec_rotary_turns.argtypes = [vp, i32, vp]
+    L.spec_rotate.argtypes = [vp, vp]
+    L.spec_cache_append_rotated.argtypes = [vp, vp]
     L.spec_last_error.restype = ctypes.c_char_p
     L.spec_version.restype = ctypes.c_int32
     for name in ("dspark_markov_bias", "dspark_markov_walk", "spec_verify_tokenwise", "spec_verify_block", "spec_verify_block_static",
@@ -176,7 +187,8 @@ def lib():
                  "spec_pipeline_destroy", "spec_cost_curve_begin", "spec_cost_curve_end",
                  "spec_cost_curve_poll", "spec_cost_curve_observe", "spec_cost_curve_table",
                  "spec_cost_curve_upload", "spec_paged_attention", "spec_cache_append", "spec_cache_append_reserved",
-                 "spec_cache_resize", "spec_cache_fork"):
+                 "spec_cache_resize", "spec_cache_fork", "spec_prompt_attention", "spec_rotary_frequencies",
+                 "spec_rotary_turns", "spec_rotate", "spec_cache_append_rotated"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -621,6 +633,9 @@ def spec_philox_uniforms(seed, step, n_streams, n_slots, device="cuda", stream=N
 _ATTENTION = struct.Struct("@11i f 4P 2q 5P N")  # spec_attention_args
 _APPEND = struct.Struct("@8i 5P 3q 3P")          # spec_append_args
 _RESIZE = struct.Struct("@5i q 10P N")           # spec_resize_args
+_PROMPT = struct.Struct("@7i f q 4P 3q 2P")      # spec_prompt_args
+_ROTATE = struct.Struct("@5i f q 3P q P q")      # spec_rotate_args
+_APPEND_ROTATED = struct.Struct("@12i f 8P 4q 2P 2q 3P")   # spec_append_rotated_args
 
 
 _T = None       # torch, once a cache call has run
@@ -852,6 +867,185 @@ def spec_cache_fork(src, dst, page_table, held, length, ref_count, page_size, ou
             out = {"status": torch.empty(n, dtype=torch.int32, device=page_table.device)}
     rc = (_lib or lib()).spec_cache_fork(sp, dp, n, B, page_size, num_pages, max_pages, tp, hp, lp, rp,
                                          _on(out["status"], "status", device, _I32, (n,)), _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Prompts and rotary positions
+# ---------------------------------------------------------------------------------------------
+def spec_prompt_attention(q, k, v, cu_rows, scale, window=0, sinks=0, out=None, stream=None):
+    """Causal attention over whole prompts, packed one behind the other.
+
+    q [rows, Hq, D], k and v [rows, Hkv, D] of one dtype (float32/bf16; rows may be slices of a wider projection, on 16-byte
+    boundaries); prompt b has rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows [B + 1] int32; None: one prompt of all rows).
+    window and sinks as in spec_paged_attention.  Returns (and reuses) ``out`` with out [rows, Hq, D], status [B]."""
+    torch = _T or _cache_torch()
+    shape, device, dtype = q.shape, q.get_device(), q.dtype
+    if device < 0:
+        raise TypeError("q must be a CUDA tensor")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    if len(shape) != 3 or len(k.shape) != 3:
+        raise ValueError("q must be [rows, Hq, D] and k [rows, Hkv, D]")
+    rows, Hq, D = shape
+    Hkv = k.shape[1]
+    qp, qs = _rows_of(q, "q", device, dtype, Hq, D)
+    kp, ks = _rows_of(k, "k", device, dtype, Hkv, D)
+    vp, vs = _rows_of(v, "v", device, dtype, Hkv, D)
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError("q, k and v must have the same rows")
+    if cu_rows is None:
+        B, cu = 1, 0
+    else:
+        B = cu_rows.numel() - 1
+        if B < 0:
+            raise ValueError("cu_rows must be [B + 1]")
+        cu = _on(cu_rows, "cu_rows", device, _I32, (B + 1,))
+    if out is None:
+        with _made_on(stream):
+            out = {"out": torch.empty((rows, Hq, D), dtype=dtype, device=q.device),
+                   "status": torch.empty(B, dtype=torch.int32, device=q.device)}
+    rc = (_lib or lib()).spec_prompt_attention(_PROMPT.pack(
+        B, Hq, Hkv, D, code, window, sinks, scale, rows, cu, qp, kp, vp, qs, ks, vs,
+        _on(out["out"], "out", device, dtype, shape), _on(out["status"], "status", device, _I32, (B,))), _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+class RotaryTable:
+    """The frequencies of rotary positions over the first ``dim`` elements of a head, on the device.
+
+    Pair j of dim / 2 turns by base^(-2 j / dim) radians a position; ``scaling`` stretches that for contexts ``factor``
+    times as long: "none", "linear" (position interpolation), "ntk" (a larger base), "yarn" (pairs that turn fewer than
+    ``slow`` times in the ``original`` context are stretched, those that turn more than ``fast`` times are not).
+    ``frequencies`` gives them (dim / 2 numbers, radians a position) instead.  ``magnitude`` multiplies what is turned
+    (None: 0.1 ln(factor) + 1 for "yarn", otherwise 1).  A pair is (j, j + dim / 2), or with ``interleaved`` (2 j, 2 j + 1)."""
+
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    def __init__(self, dim, base=10000.0, scaling="none", factor=1.0, original=4096, slow=1.0, fast=32.0, interleaved=False,
+                 magnitude=None, frequencies=None, device="cuda"):
+        torch = _T or _cache_torch()
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(self.SCALINGS)}, got {scaling!r}")
+        if dim < 2 or dim % 2 != 0:
+            raise ValueError(f"dim must be even and at least 2, got {dim}")
+        n = dim // 2
+        freq, mag = (ctypes.c_double * n)(), ctypes.c_float(1.0)
+        if frequencies is None:
+            _check(lib().spec_rotary_frequencies(dim, base, self.SCALINGS[scaling], factor, original, slow, fast, freq, ctypes.byref(mag)))
+        else:
+            if len(frequencies) != n:
+                raise ValueError(f"frequencies must be {n} numbers")
+            freq[:] = [float(f) for f in frequencies]
+        turns = (ctypes.c_int64 * n)()
+        _check(lib().spec_rotary_turns(freq, n, turns))
+        self.dim, self.interleaved = dim, bool(interleaved)
+        self.magnitude = float(mag.value if magnitude is None else magnitude)
+        self.frequencies = list(freq)
+        self.turns = torch.tensor(list(turns), dtype=torch.int64).to(device)
+        self._device, self._ptr = self.turns.get_device(), self.turns.data_ptr()
+
+    def _on(self, device):
+        if self._device != device:
+            raise ValueError("the rotary table is on another device")
+        return self._ptr
+
+
+def spec_rotate(x, positions, rotary, out=None, stream=None):
+    """x [rows, heads, D] (float32/bf16; rows may be slices of a wider projection) with every row turned by its position
+    (positions [rows] int32).  Queries and keys that lie beside each other are one call.  ``out`` [rows, heads, D] may be
+    such a slice too, or x itself.  Returns ``out``."""
+    torch = _T or _cache_torch()
+    shape, device, dtype = x.shape, x.get_device(), x.dtype
+    if device < 0:
+        raise TypeError("x must be a CUDA tensor")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    if len(shape) != 3:
+        raise ValueError("x must be [rows, heads, D]")
+    rows, heads, D = shape
+    xp, xs = _rows_of(x, "x", device, dtype, heads, D)
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+    op, os_ = _rows_of(out, "out", device, dtype, heads, D)
+    if out.shape[0] != rows:
+        raise ValueError("out must have x's rows")
+    rc = (_lib or lib()).spec_rotate(_ROTATE.pack(
+        heads, D, rotary.dim, rotary.interleaved, code, rotary.magnitude, rows, rotary._on(device),
+        _on(positions, "positions", device, _I32, (rows,)), xp, xs, op, os_), _raw_stream(stream, device))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+def spec_cache_append_rotated(q, k, v, k_pages, v_pages, page_table, length, rotary, cu_rows=None, cu_drafts=None, kmax=None,
+                              keep_keys=False, out=None, stream=None, reserved=None):
+    """spec_cache_append with rotary positions on the way, for blocks and for whole prompts.
+
+    Row i of stream b stands at position length[b] + i: its key goes turned, its value as it is, into one layer's pages, and its
+    queries turned to out["q"]; with ``keep_keys`` the turned key goes to out["k"] as well (for spec_prompt_attention).  q [rows, Hq, D]
+    (None: keys and values alone), k and v [rows, Hkv, D] may be slices of a wider projection.  The rows are packed by ``cu_rows`` [B + 1] int32 (their
+    prefix sum; streams without rows are fine), or as verify blocks by ``cu_drafts`` [B + 1] (one row more than drafts; None: ``kmax``
+    drafts each, where ``kmax`` is given: the most drafts of a stream).  ``reserved`` as in spec_cache_append.  Returns (and reuses) ``out``
+    with q, k (None without), status [B]; out["q"] may be q itself, and out["k"] k."""
+    torch = _T or _cache_torch()
+    device, code, kpp, vpp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
+    dtype = k_pages.dtype
+    nk, ks = _rows_of(k, "k", device, dtype, Hkv, D)
+    nv, vs = _rows_of(v, "v", device, dtype, Hkv, D)
+    rows = k.shape[0]
+    if v.shape[0] != rows or (q is not None and q.shape[0] != rows):
+        raise ValueError("q, k and v must have the same rows")
+    Hq = nq = qs = 0
+    if q is not None:
+        if len(q.shape) != 3:
+            raise ValueError("q must be [rows, Hq, D]")
+        Hq = q.shape[1]
+        nq, qs = _rows_of(q, "q", device, dtype, Hq, D)
+    shape = page_table.shape
+    if len(shape) != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B = shape[0]
+    if cu_rows is not None:
+        if cu_drafts is not None or kmax is not None:
+            raise ValueError("cu_rows or cu_drafts and kmax, not both")
+        cu, most, extra = _on(cu_rows, "cu_rows", device, _I32, (B + 1,)), rows, 0
+    elif kmax is None:
+        raise ValueError("cu_rows, or kmax (and cu_drafts), say how the rows are packed")
+    else:
+        most, extra = kmax + 1, 1
+        if cu_drafts is None:
+            cu = 0
+            if rows != B * most:
+                raise ValueError("without cu_drafts there are B * (kmax + 1) rows")
+        else:
+            cu = _on(cu_drafts, "cu_drafts", device, _I32, (B + 1,))
+    if out is None:
+        with _made_on(stream):
+            out = {"q": None if q is None else torch.empty(q.shape, dtype=dtype, device=q.device),
+                   "k": torch.empty(k.shape, dtype=dtype, device=k.device) if keep_keys else None,
+                   "status": torch.empty(B, dtype=torch.int32, device=k.device)}
+    oq = oqs = ok = oks = 0
+    if q is not None:
+        oq, oqs = _rows_of(out["q"], "out['q']", device, dtype, Hq, D)
+        if out["q"].shape[0] != rows:
+            raise ValueError("out['q'] must have q's rows")
+    if keep_keys:
+        ok, oks = _rows_of(out["k"], "out['k']", device, dtype, Hkv, D)
+        if out["k"].shape[0] != rows:
+            raise ValueError("out['k'] must have k's rows")
+    rc = (_lib or lib()).spec_cache_append_rotated(_APPEND_ROTATED.pack(
+        B, most, extra, Hq, Hkv, D, page_size, num_pages, shape[1], code, rotary.dim, rotary.interleaved, rotary.magnitude,
+        rotary._on(device), cu, _on(length, "length", device, _I32, (B,)), _on(page_table, "page_table", device, _I32, shape),
+        0 if reserved is None else _on(reserved, "reserved", device, _I32, (B,)), nq, nk, nv, qs, ks, vs, rows, oq, ok, oqs, oks,
+        kpp, vpp, _on(out["status"], "status", device, _I32, (B,))), _raw_stream(stream, device))
     if rc != 0:
         _check(rc)
     return out

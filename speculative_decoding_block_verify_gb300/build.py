@@ -19,8 +19,10 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspecverify.so"
 SOURCES = ["api.cu", "verify.cu", "markov_bias.cu", "pick_k.cu", "pipeline.cu", "walk.cu", "cost_curve.cu",
-           "cache.cu", "attention.cu", "attention_tc.cu", "attention_f32.cu"]
-HEADERS = ["common.cuh", "df.cuh", "draw.cuh", "host_util.h", "blocks.cuh", "attention.cuh", "tcgen05.cuh"]
+           "cache.cu", "attention.cu", "attention_tc.cu", "attention_f32.cu", "rotary.cu", "prompt.cu",
+           "prompt_tc.cu", "prompt_f32.cu"]
+HEADERS = ["common.cuh", "df.cuh", "draw.cuh", "host_util.h", "blocks.cuh", "divisor.cuh", "attention.cuh", "attention_f32.cuh",
+           "prompt.cuh", "tcgen05.cuh", "tensor_map.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -381,14 +381,14 @@ struct DeviceInfo {
 };
 static DeviceInfo g_device[64];
 
-static int sm_count(int* sms) {
+int sm_count(int* sms, const char* who) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return set_cuda_error(e, "spec_paged_attention");
+    if (e != cudaSuccess) return set_cuda_error(e, who);
     int n = dev >= 0 && dev < 64 ? g_device[dev].sms.load(std::memory_order_acquire) : 0;
     if (n == 0) {
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return set_cuda_error(e, "spec_paged_attention");
+        if (e != cudaSuccess) return set_cuda_error(e, who);
         if (dev >= 0 && dev < 64) g_device[dev].sms.store(n, std::memory_order_release);
     }
     *sms = n;
@@ -510,7 +510,7 @@ extern "C" size_t spec_paged_attention_workspace_bytes(const spec_attention_args
     clear_error();
     if (a == nullptr || check(a) != SPEC_OK || a->B == 0) return 0;
     int sms = 0, rows = 0, ctas = 0;
-    if (sm_count(&sms) != SPEC_OK) return 0;
+    if (sm_count(&sms, "spec_paged_attention") != SPEC_OK) return 0;
     cut(a, sms, &rows, &ctas);
     return layout(a, rows, ctas, nullptr, nullptr);
 }
@@ -535,7 +535,7 @@ extern "C" int spec_paged_attention(const spec_attention_args* a, void* stream) 
         return set_error(SPEC_ERR_ARG, "spec_paged_attention: scale is not finite");
     int sms = 0;
     AttnParams p;
-    if ((rc = sm_count(&sms)) != SPEC_OK) return rc;
+    if ((rc = sm_count(&sms, "spec_paged_attention")) != SPEC_OK) return rc;
     cut(a, sms, &p.rows, &p.ctas);
     const size_t need = layout(a, p.rows, p.ctas, nullptr, nullptr);
     if (a->workspace == nullptr || ((uintptr_t)a->workspace & 15) || a->workspace_bytes < need)

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "blocks.cuh"
+#include "divisor.cuh"
 
 namespace sv {
 
@@ -24,14 +25,6 @@ struct __align__(16) Unjoined {
     int64_t row0;          // the block's first packed row
     int64_t pad;
 };
-
-// Division by a number fixed for the call: the quotient is the high word of a product with 2^32 / d, rounded up (exact while
-// n * d < 2^32; a runtime division is about 150 cycles of dependent instructions).
-struct Divisor {
-    uint32_t d, magic;   // magic 0: d is 1
-    __device__ __forceinline__ int of(int n) const { return magic ? (int)__umulhi((uint32_t)n, magic) : n; }
-};
-inline Divisor divisor(int d) { return {(uint32_t)d, d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u}; }
 
 struct AttnParams {
     spec_attention_args a;

@@ -49,6 +49,9 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Multiprocessors of the current device (defined in attention.cu).
+int sm_count(int* sms, const char* who);
+
 inline bool valid_dtype(int d) { return d == SPEC_DTYPE_F32 || d == SPEC_DTYPE_BF16; }
 
 // The verify over the dense [B, kmax (+1), V] layout with the step read from device memory

@@ -1,0 +1,200 @@
+// How a batch of prompts is cut into pieces, shared by the kernels of spec_prompt_attention.
+//
+// An item is (prompt, key head, piece of consecutive tokens): the rows of a piece are its tokens times the G query heads of the key
+// head, row = token * G + query head, so that a product's 128 rows are full whatever G is and few of their scores lie above the
+// diagonal.  Piece number l of a prompt sees about l pieces of keys: the later, the more work.  The items of all prompts are ranked by
+// that number, the last pieces first, and the CTAs, as many as are resident, take them by turns, forwards and backwards (0 1 2 .. 2 1
+// 0 0 1 ..): long and short prompts in one batch give every CTA nearly the same work, without a counter in memory and without the host
+// knowing a length.  The rank of an item is not stored anywhere: a warp finds the item of a rank from how many pieces lie above a level.
+#pragma once
+
+#include "common.cuh"
+#include "divisor.cuh"
+
+namespace sv {
+
+struct PromptParams {
+    spec_prompt_args a;
+    int G;             // query heads per key head
+    int group;         // tokens of a group of up to 128 rows
+    int piece;         // tokens of a piece
+    Divisor by_G;
+    float scale_log2;  // |scale| * log2(e)
+};
+
+// One item, as the walking warp tells it to the others.
+struct Piece {
+    int b, head;       // prompt, key head
+    int n;             // tokens of the prompt
+    int at, tokens;    // the piece's first token, and how many
+    int64_t row0;      // the prompt's first packed row
+};
+
+// The keys that a piece's rows see, in tiles of kTile positions: those of the first tokens that stay visible, then the window's.
+struct Keys {
+    int low, high, sink;   // visible positions: [0, sink) and [low, high)
+    int sink_tiles, first_tile, tiles;
+};
+template <int kTile>
+__device__ __forceinline__ Keys keys_of(const PromptParams& p, int at, int tokens) {
+    Keys k;
+    k.high = at + tokens;
+    k.low = p.a.window > 0 ? max(0, at + 1 - p.a.window) : 0;
+    k.sink = min(p.a.sinks, k.low);
+    k.sink_tiles = (k.sink + kTile - 1) / kTile;
+    k.first_tile = max(k.low / kTile, k.sink_tiles);
+    k.tiles = k.sink_tiles + (int)(((unsigned)k.high + kTile - 1) / kTile) - k.first_tile;
+    return k;
+}
+template <int kTile>
+__device__ __forceinline__ int start_of(int sink_tiles, int first_tile, int t) {
+    return (t < sink_tiles ? t : first_tile + t - sink_tiles) * kTile;
+}
+
+__device__ __forceinline__ int64_t prompt_row(const spec_prompt_args& a, int b) {
+    return a.cu_rows == nullptr ? (int64_t)b * (a.rows / a.B) : (int64_t)*(a.cu_rows + b);
+}
+// Offsets that break the packing at prompt b: it and the prompts behind it are not defined.
+__device__ __forceinline__ bool prompt_broken(const spec_prompt_args& a, int b, int64_t row0, int64_t end) {
+    return end < row0 || (b == 0 && row0 != 0) || end > a.rows;
+}
+
+// The CTA's items, found by one warp together (all 32 lanes call, all know the result).  A batch of kBatch prompts at a time: ranks go
+// through the first batch's items, then the second's.
+struct PromptWalk {
+    static constexpr int kEach = 8, kBatch = 32 * kEach;
+    int pieces[kEach];   // of prompt first + 32 i + lane
+    int first;           // the batch's first prompt
+    int most, total;     // pieces of its longest prompt, and of all
+    int64_t base;        // items of the batches before
+    int64_t round;
+    bool ended;          // no batch behind this one
+
+    __device__ __forceinline__ int above(int level) const {   // pieces of the batch with a number of `level` or more
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) s += max(0, pieces[i] - level);
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
+    }
+    __device__ __forceinline__ void load(const PromptParams& p, int from) {
+        const int lane = threadIdx.x & 31;
+        int bad = INT32_MAX, top = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int b = from + 32 * i + lane;
+            pieces[i] = 0;
+            if (b < p.a.B) {
+                const int64_t row0 = prompt_row(p.a, b), end = prompt_row(p.a, b + 1);
+                if (prompt_broken(p.a, b, row0, end))
+                    bad = min(bad, b);
+                else
+                    pieces[i] = (int)((end - row0 + p.piece - 1) / p.piece);
+            }
+        }
+        bad = __reduce_min_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (from + 32 * i + lane >= bad) pieces[i] = 0;
+            top = max(top, pieces[i]);
+        }
+        first = from;
+        most = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+        total = above(0);
+        ended = bad != INT32_MAX || from + kBatch >= p.a.B;
+    }
+    __device__ __forceinline__ void start(const PromptParams& p) {
+        base = 0;
+        round = 0;
+        load(p, 0);
+    }
+    // The next item; false: there are no more.
+    __device__ __forceinline__ bool next(const PromptParams& p, Piece* out) {
+        const int lane = threadIdx.x & 31;
+        const int64_t rank = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        ++round;
+        while (rank >= base + (int64_t)total * p.a.Hkv) {
+            if (ended) return false;
+            base += (int64_t)total * p.a.Hkv;
+            load(p, first + kBatch);
+        }
+        const int64_t at = rank - base;
+        int r;
+        if (at >> 32)
+            r = (int)(at / p.a.Hkv);
+        else
+            r = (int)((uint32_t)at / (uint32_t)p.a.Hkv);
+        out->head = (int)(at - (int64_t)r * p.a.Hkv);
+        // the lowest level above which lie no more than r pieces
+        int lo = 0, hi = most - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (above(mid + 1) <= r)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        int nth = r - above(lo + 1), b = 0;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const unsigned has = __ballot_sync(0xffffffffu, pieces[i] > lo);
+            if (!found) {
+                const int n = __popc(has);
+                if (nth < n) {
+                    // the lane whose bit is number nth: the one that has nth bits below its own
+                    const bool me = ((has >> lane) & 1) && __popc(has & ((1u << lane) - 1)) == nth;
+                    b = first + 32 * i + __ffs((int)__ballot_sync(0xffffffffu, me)) - 1;
+                    found = true;
+                } else {
+                    nth -= n;
+                }
+            }
+        }
+        out->b = b;
+        out->row0 = prompt_row(p.a, b);
+        out->n = (int)(prompt_row(p.a, b + 1) - out->row0);
+        out->at = lo * p.piece;
+        out->tokens = min(p.piece, out->n - out->at);
+        return true;
+    }
+};
+
+// The statuses, by one warp of every CTA: CTA c has those of batches c, c + gridDim.x, .. of 32 prompts.
+__device__ __forceinline__ void prompt_statuses(const PromptParams& p) {
+    const int lane = threadIdx.x & 31;
+    if ((int64_t)blockIdx.x * 32 >= p.a.B) return;
+    int bad = INT32_MAX;
+    for (int b0 = 0; b0 < p.a.B && bad == INT32_MAX; b0 += 32) {
+        const int b = b0 + lane;
+        if (b < p.a.B && prompt_broken(p.a, b, prompt_row(p.a, b), prompt_row(p.a, b + 1))) bad = b;
+        bad = __reduce_min_sync(0xffffffffu, bad);
+    }
+    for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.a.B; b += (int64_t)gridDim.x * 32)
+        p.a.status[b] = b < bad ? SPEC_ST_OK : SPEC_ST_BAD_OFFSETS;
+}
+
+// A wait of this CTA gave up: one warp leaves NaN in the rows of all its items.
+template <typename T>
+__device__ __forceinline__ void prompt_gave_up(const PromptParams& p, T nan) {
+    const int lane = threadIdx.x & 31;
+    PromptWalk w;
+    Piece it;
+    w.start(p);
+    while (w.next(p, &it)) {
+        const int per = p.G * p.a.D;
+        for (int t = 0; t < it.tokens; ++t) {
+            T* to = reinterpret_cast<T*>(p.a.out) + ((it.row0 + it.at + t) * p.a.Hq + (int64_t)it.head * p.G) * p.a.D;
+            for (int i = lane; i < per; i += 32) to[i] = nan;
+        }
+    }
+}
+
+cudaError_t launch_prompt_tc(const PromptParams& p, int sms, cudaStream_t s);    // bf16 (prompt_tc.cu)
+cudaError_t launch_prompt_f32(const PromptParams& p, int sms, cudaStream_t s);   // float32 heads up to 128 (prompt_f32.cu)
+// CTAs of a grid: what is resident, or fewer where there cannot be as many items.
+inline int prompt_ctas(const PromptParams& p, int resident) {
+    const int64_t items = (p.a.rows / p.piece + p.a.B) * p.a.Hkv;
+    return (int)(items < resident ? items : resident);
+}
+
+}  // namespace sv

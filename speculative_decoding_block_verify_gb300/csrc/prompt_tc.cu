@@ -1,0 +1,543 @@
+// spec_prompt_attention on the tensor cores: bf16.
+//
+// One tile of an item (prompt.cuh) is two matrix products around a softmax step,
+//   S [rows x keys] = Q [rows x D] K^T,   P = 2^(scale S - m),   O [rows x D] += P V.
+// An item has two groups of 128 rows (heads above 128: one), which share every tile of keys and values in shared memory.  While the
+// softmax of one group runs, the tensor cores have the other group's products: O0 += P0 V, S0' = Q0 K'^T, O1 += P1 V, S1' = Q1
+// K'^T, and so on round.  At 128 rows, 128 keys and heads of 128 a product takes 512 tensor cycles, so a group's softmax has 1,024 to itself.
+// Each group's S and P share 128 columns of tensor memory (P, bf16, over S; what is issued to the tensor cores runs in its order, so
+// S' may be issued behind the product that reads P), and its O has D more.
+//
+// Warps 0 to 3 and 4 to 7 are a group's softmax, a row per thread (TMEM lane = row): the row's running maximum and sum in registers, O scaled in
+// tensor memory when the maximum has risen by more than 8 (2^8 of headroom is nothing to float32, and most tiles then leave O alone).
+// Warp 8 finds the items and copies by TMA, warp 9 issues the products.
+
+#include <atomic>
+
+#include "host_util.h"
+#include "prompt.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+namespace sv {
+
+constexpr int kPromptThreads = 384;
+// registers of a thread of the softmax's two warpgroups and of the last one, where the CTA was launched with kRegsStart each
+constexpr int kRegsRows = 208, kRegsOthers = 88, kRegsStart = 168;
+static_assert(2 * kRegsRows + kRegsOthers <= 3 * kRegsStart, "setmaxnreg would wait for ever");
+
+// DP: the head padded to 64, 128 or 256 columns (TMA fills the rest with zeros).
+template <int DP>
+struct PromptLayout {
+    static constexpr int kGroups = DP == 256 ? 1 : 2;
+    static constexpr int kKeys = DP == 256 ? 64 : 128;         // positions of a tile
+    static constexpr int kHalves = DP / 64;                    // 64-column panels (128 bytes a row)
+    static constexpr int kQPanel = kTcRows * 128;              // bytes
+    static constexpr int kQBytes = kHalves * kQPanel;          // of a group
+    static constexpr int kPanel = kKeys * 128;
+    static constexpr int kSlotBytes = kHalves * kPanel;        // K or V of one tile
+    static constexpr int kSlots = DP == 64 ? 10 : 5;
+    static constexpr int kBuffers = 2;                         // of S: a group's, or (one group) every other tile's
+    static constexpr int kOCol = kBuffers * kKeys;
+    static constexpr int kCols = 512;
+    static constexpr int kBytes = kGroups * kQBytes + kSlots * kSlotBytes;
+    static_assert(kOCol + kGroups * DP <= kCols, "columns of tensor memory");
+};
+
+struct PromptSegment {
+    int tiles;           // of the item, and of each of its groups; 0: the CTA is done
+    int group_tiles[2];
+    int sink_tiles, first_tile, low, high, sink;
+    int at, tokens, head;
+    int64_t row0;
+};
+
+struct PromptShared {
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t full[10], empty[10];
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
+    PromptSegment seg[kSegments];
+    uint32_t tmem;
+    int abort;
+};
+
+// ---- warp 8: the walk over the CTA's items, and the copies ------------------------------------
+template <int DP>
+__device__ __forceinline__ void prompt_copy_role(const PromptParams& p, const CUtensorMap* qmap, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                                 char* smem, PromptShared& sh) {
+    using Lay = PromptLayout<DP>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t q_at = smem_u32(smem), ring = q_at + Lay::kGroups * Lay::kQBytes;
+    const uint64_t stay = l2_evict_normal_policy();
+    PromptWalk w;
+    Piece it = {};
+    Keys keys = {};
+    int told = 0, slot = 0, q_copies[2] = {0, 0};
+    unsigned phase = 1;   // a fresh barrier: the phase before its first is done
+    bool ok = true;
+    auto tell = [&](bool any) {   // the next item, or that there is none
+        PromptSegment& seg = sh.seg[told % kSegments];
+        ok = ok && warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort);
+        if (any) keys = keys_of<Lay::kKeys>(p, it.at, it.tokens);
+        if (ok && lane == 0) {
+            seg.tiles = any ? keys.tiles : 0;
+            if (any) {
+#pragma unroll
+                for (int g = 0; g < Lay::kGroups; ++g) {
+                    const int mine = min(p.group, it.tokens - g * p.group), last = it.at + g * p.group + mine - 1;
+                    seg.group_tiles[g] = mine > 0 ? keys.sink_tiles + max(0, last / Lay::kKeys + 1 - keys.first_tile) : 0;
+                }
+                seg.sink_tiles = keys.sink_tiles, seg.first_tile = keys.first_tile;
+                seg.low = keys.low, seg.high = keys.high, seg.sink = keys.sink;
+                seg.at = it.at, seg.tokens = it.tokens, seg.head = it.head, seg.row0 = it.row0;
+            }
+            mbar_arrive(&sh.seg_full[told % kSegments]);
+        }
+        __syncwarp();
+        ++told;
+    };
+    auto copy = [&](const CUtensorMap* map, int head, int row) {
+        ok = ok && warp_wait_for(&sh.empty[slot], phase, &sh.abort);
+        if (!ok) return;
+        if (lane == 0) {
+            mbar_expect_tx(&sh.full[slot], Lay::kSlotBytes);
+#pragma unroll
+            for (int half = 0; half < Lay::kHalves; ++half)
+                tma_load_3d(ring + slot * Lay::kSlotBytes + half * Lay::kPanel, map, half * 64, head, row, &sh.full[slot], stay);
+        }
+        __syncwarp();
+        if (++slot == Lay::kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    w.start(p);
+    bool more = w.next(p, &it);
+    tell(more);
+    while (more && ok) {
+        const int tiles = keys.tiles;
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int row = (int)it.row0 + start_of<Lay::kKeys>(keys.sink_tiles, keys.first_tile, t);
+            const int head = it.head;
+            copy(kmap, head, row);
+            if (t == 0) {
+#pragma unroll
+                for (int g = 0; g < Lay::kGroups; ++g) {
+                    if (g * p.group >= it.tokens) break;
+                    ok = ok && warp_wait_for(&sh.q_empty[g], (q_copies[g] & 1) ^ 1, &sh.abort);
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(&sh.q_full[g], Lay::kHalves * p.group * p.G * 128);
+#pragma unroll
+                        for (int half = 0; half < Lay::kHalves; ++half)
+                            tma_load_3d(q_at + g * Lay::kQBytes + half * Lay::kQPanel, qmap, half * 64, head * p.G,
+                                        (int)it.row0 + it.at + g * p.group, &sh.q_full[g], stay);
+                    }
+                    __syncwarp();
+                    ++q_copies[g];
+                }
+            }
+            if (t == tiles - 1) {   // the next item is known before the last values are waited for
+                more = w.next(p, &it);
+                tell(more);
+            }
+            copy(vmap, head, row);
+        }
+    }
+    if (!ok) {   // gave up: whatever was copied must have arrived before the CTA's memory is given back
+        for (int s = 0; s < Lay::kSlots; ++s)
+            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
+#pragma unroll
+        for (int g = 0; g < Lay::kGroups; ++g)
+            for (int n = 0; q_copies[g] > 0 && n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.q_full[g], (q_copies[g] - 1) & 1); ++n) {}
+    }
+}
+
+// ---- warp 9: products -------------------------------------------------------------------------
+// The whole warp runs the loop, so that descriptors and addresses are uniform; one lane issues.
+template <int DP>
+__device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char* smem, PromptShared& sh) {
+    using Lay = PromptLayout<DP>;
+    constexpr int kGroups = Lay::kGroups;
+    const uint32_t q_at = smem_u32(smem), ring = q_at + kGroups * Lay::kQBytes;
+    const uint32_t tmem = __reduce_or_sync(0xffffffffu, sh.tmem);
+    const int ksteps = (p.a.D + 15) / 16;
+    // a negative scale is a negated Q (bit 13) and its magnitude
+    const uint32_t qk = mma_desc(Lay::kKeys, false) | (p.a.scale < 0.f ? 1u << 13 : 0u);
+    const uint32_t pv = mma_desc(ksteps * 16, true);   // as many columns of O as the head has
+    int items[2] = {0, 0};                             // of each group so far
+    unsigned k_at = 0, v_at = 1;                       // places in the ring, counted from the start: keys and values take turns
+    unsigned s_count = 0;                              // (one group) products S so far
+    unsigned p_count[2] = {0, 0};                      // waits for P of each buffer so far
+    auto full = [&](unsigned at) { return warp_wait_for(&sh.full[at % Lay::kSlots], (at / Lay::kSlots) & 1, &sh.abort); };
+    auto keys = [&](int g, int buf, bool last) {       // S of the tile at k_at
+        const uint32_t a = desc_lo(q_at + g * Lay::kQBytes, 1), b = desc_lo(ring + k_at % Lay::kSlots * Lay::kSlotBytes, 1);
+        tc_fence_after();
+        if (elected()) {
+#pragma unroll
+            for (int k = 0; k < Lay::kHalves * 4; ++k)
+                if (k < ksteps)
+                    mma_ss(tmem + buf * Lay::kKeys, desc(a + (k >> 2) * (Lay::kQPanel >> 4) + (k & 3) * 2, 1024 >> 4),
+                           desc(b + (k >> 2) * (Lay::kPanel >> 4) + (k & 3) * 2, 1024 >> 4), qk, k > 0);
+            mma_commit(&sh.s_full[buf]);
+            if (last) mma_commit(&sh.q_empty[g]);
+        }
+        __syncwarp();
+    };
+    auto values = [&](int g, int buf, bool add) {      // O += P V of the tile at v_at
+        const uint32_t v = desc_lo(ring + v_at % Lay::kSlots * Lay::kSlotBytes, Lay::kPanel >> 4);
+        tc_fence_after();
+        if (elected()) {
+#pragma unroll
+            for (int k = 0; k < Lay::kKeys / 16; ++k)
+                mma_ts(tmem + Lay::kOCol + g * DP, tmem + buf * Lay::kKeys + k * 8, desc(v + 2 * k * (1024 >> 4), 1024 >> 4), pv, add || k > 0);
+        }
+        __syncwarp();
+    };
+    auto release = [&](unsigned at) {
+        if (elected()) mma_commit(&sh.empty[at % Lay::kSlots]);
+        __syncwarp();
+    };
+    int at = 0, tiles = 0, n[2] = {0, 0};
+    auto next = [&](int* tiles_out, int* n_out) {      // the next item's tiles
+        const int place = at % kSegments;
+        if (!warp_wait_for(&sh.seg_full[place], (at / kSegments) & 1, &sh.abort)) return false;
+        *tiles_out = (int)__reduce_max_sync(0xffffffffu, (unsigned)sh.seg[place].tiles);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) n_out[g] = (int)__reduce_max_sync(0xffffffffu, (unsigned)sh.seg[place].group_tiles[g]);
+        if (elected()) mbar_arrive(&sh.seg_empty[place]);
+        __syncwarp();
+        ++at;
+        return true;
+    };
+    if (!next(&tiles, n)) return false;
+    if (tiles == 0) return true;
+    if (kGroups == 2) {
+        if (!full(k_at)) return false;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (n[g] == 0) continue;
+            if (!warp_wait_for(&sh.q_full[g], items[g] & 1, &sh.abort)) return false;
+            ++items[g];
+            keys(g, g, n[g] == 1);
+        }
+        release(k_at);
+        k_at += 2;
+        for (;;) {
+            int after = 0, m[2] = {0, 0};   // the next item
+            for (int t = 0; t < tiles; ++t) {
+                const bool last = t == tiles - 1;
+                if (last && !next(&after, m)) return false;
+                const bool more = !last || after > 0;   // tiles behind this one
+                bool ready = false;
+                if (!full(v_at)) return false;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (t < n[g]) {
+                        if (!warp_wait_for(&sh.p_full[g], p_count[g]++ & 1, &sh.abort)) return false;
+                        values(g, g, t > 0);
+                        if (t == n[g] - 1) {
+                            if (elected()) mma_commit(&sh.o_done[g]);
+                            __syncwarp();
+                        }
+                    }
+                    if (g == 1) release(v_at);
+                    if (more && (last ? m[g] > 0 : t + 1 < n[g])) {
+                        if (!ready && !full(k_at)) return false;
+                        ready = true;
+                        if (last) {
+                            if (!warp_wait_for(&sh.q_full[g], items[g] & 1, &sh.abort)) return false;
+                            ++items[g];
+                        }
+                        keys(g, g, last ? m[g] == 1 : t + 2 == n[g]);
+                    }
+                }
+                if (more) {
+                    release(k_at);
+                    k_at += 2;
+                }
+                v_at += 2;
+            }
+            if (after == 0) return true;
+            tiles = after;
+            n[0] = m[0], n[1] = m[1];
+        }
+    } else {
+        // S of tile t + 1 goes to the other buffer before O += P V of tile t
+        unsigned o_count = 0;
+        auto ahead = [&](bool begin, bool end) {
+            if (!full(k_at)) return false;
+            if (begin && !warp_wait_for(&sh.q_full[0], items[0]++ & 1, &sh.abort)) return false;
+            keys(0, s_count++ & 1, end);
+            release(k_at);
+            k_at += 2;
+            return true;
+        };
+        if (!ahead(true, tiles == 1)) return false;
+        for (;;) {
+            int after = 0, m[2] = {0, 0};
+            for (int t = 0; t < tiles; ++t) {
+                const bool last = t == tiles - 1;
+                if (last && !next(&after, m)) return false;
+                if ((!last || after > 0) && !ahead(last, last ? after == 1 : t + 2 == tiles)) return false;
+                const int buf = o_count++ & 1;
+                if (!full(v_at)) return false;
+                if (!warp_wait_for(&sh.p_full[buf], p_count[buf]++ & 1, &sh.abort)) return false;
+                values(0, buf, t > 0);
+                if (elected()) mma_commit(&sh.o_done[buf]);
+                __syncwarp();
+                release(v_at);
+                v_at += 2;
+            }
+            if (after == 0) return true;
+            tiles = after;
+        }
+    }
+}
+
+// ---- warps 0 to 3, 4 to 7: softmax, scaling, output ----------------------------------------------
+template <int DP>
+__device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char* smem, PromptShared& sh, int g) {
+    using Lay = PromptLayout<DP>;
+    constexpr int kKeys = Lay::kKeys, kGroups = Lay::kGroups;
+    const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t o_at = lanes + Lay::kOCol + g * DP;
+    const int token_in = p.by_G.of(tid), query = tid - token_in * p.G;
+    const bool wide = (((uint32_t)reinterpret_cast<uintptr_t>(p.a.out) | p.a.D * 2) & 31) == 0;   // 32-byte stores
+    unsigned n_all = 0, tiles_all = 0, items = 0;   // tiles of the group, of the CTA, and the group's items so far
+    for (int n_seg = 0;; ++n_seg) {
+        const int place = n_seg % kSegments;
+        if (!warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort)) return;
+        const PromptSegment w = sh.seg[place];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
+        if (w.tiles == 0) return;
+        const int n = kGroups == 1 ? w.tiles : w.group_tiles[g];
+        const int fixes_from = g == 0 ? 0 : w.group_tiles[0];   // the tiles whose values this group looks after
+        const int tokens = min(p.group, w.tokens - g * p.group);
+        const int at_first = w.at + g * p.group, at_last = at_first + tokens - 1;
+        const bool mine = token_in < tokens;
+        const int at = min(at_first + token_in, at_last);
+        const int low = p.a.window > 0 ? at + 1 - p.a.window : 0;   // the row sees [low, at] and [0, sinks)
+        float m = -kInf, l = 0.f;
+        for (int t = 0; t < n; ++t, ++n_all) {
+            const int buf = kGroups == 2 ? g : (int)(n_all & 1);
+            const unsigned uses = kGroups == 2 ? n_all : n_all >> 1;
+            const int j0 = start_of<kKeys>(w.sink_tiles, w.first_tile, t);
+            if (!warp_wait_for(&sh.s_full[buf], uses & 1, &sh.abort)) return;
+            tc_fence_after();
+            uint32_t s[kKeys];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) tmem_ld32(lanes + buf * kKeys + c, s + c);
+            tc_wait_ld();
+            // a tile that every row sees whole needs no mask
+            const bool clean = j0 + kKeys - 1 <= at_first && (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kKeys <= p.a.sinks);
+            if (!clean) {
+                const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c)
+                    if (!(c <= hi && (c >= lo || c < sk))) s[c] = 0xff800000u;
+            }
+            float x[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2)   // three-way maxima
+                x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;   // the scale is positive here
+            float scale_o = 1.f;
+            if (mine && top > m + 8.f) {   // lanes without a row never ask for the scaling of O
+                scale_o = m == -kInf ? 0.f : ex2(m - top);
+                m = top;
+                l *= scale_o;
+            }
+            const float base = m == -kInf ? 0.f : m;
+            const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t pk[kKeys / 2];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+                const float2 y = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, nb);
+                // P V takes both operands in one type, so the weights are rounded to bf16, and the sum takes them as rounded
+                pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
+                sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], make_float2(bf16_lo(pk[c / 2]), bf16_hi(pk[c / 2])));
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < kKeys / 2; c += 32) tmem_st32(lanes + buf * kKeys + c, pk + c);
+            if (t > 0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
+                // (two groups: S of this tile was issued behind the product before, so that is done)
+                if (kGroups == 1 && !warp_wait_for(&sh.o_done[buf ^ 1], ((n_all - 1) >> 1) & 1, &sh.abort)) return;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + c, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale_o);
+                    tmem_st32(o_at + c, o);
+                }
+            }
+            tc_wait_st();
+            tc_fence_before();
+            // values of positions that no row of the item sees (another prompt's, or what lies behind the last): zeros, whatever is
+            // there.  The first group that uses the tile sees to it, a position a thread, before its P is announced.
+            const int from = min(kKeys, w.high - j0), lo = min(kKeys, max(0, w.low - j0)), sk = max(0, w.sink - j0);
+            if (t >= fixes_from && (from < kKeys || sk < lo)) {
+                const unsigned in = 2 * (tiles_all + t) + 1;
+                if (!warp_wait_for(&sh.full[in % Lay::kSlots], (in / Lay::kSlots) & 1, &sh.abort)) return;
+                if (tid < kKeys && (tid >= from || (tid >= sk && tid < lo))) {
+                    char* const to = smem + kGroups * Lay::kQBytes + in % Lay::kSlots * Lay::kSlotBytes + tid * 128;
+#pragma unroll
+                    for (int c = 0; c < Lay::kHalves * 8; ++c)
+                        *reinterpret_cast<uint4*>(to + (c >> 3) * Lay::kPanel + (((c & 7) ^ (tid & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+        }
+        tiles_all += w.tiles;
+        if (n == 0) continue;
+        if (kGroups == 2 ? !warp_wait_for(&sh.o_done[g], items & 1, &sh.abort)
+                         : !warp_wait_for(&sh.o_done[(n_all - 1) & 1], ((n_all - 1) >> 1) & 1, &sh.abort))
+            return;
+        ++items;
+        tc_fence_after();
+        const float inv = 1.f / l;
+        unsigned short* const to = reinterpret_cast<unsigned short*>(p.a.out) +
+                                   ((w.row0 + at) * p.a.Hq + w.head * p.G + query) * (int64_t)p.a.D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < p.a.D; c0 += 64) {
+            uint32_t o[64];
+            __syncwarp();
+            tmem_ld32(o_at + c0, o);
+            tmem_ld32(o_at + c0 + 32, o + 32);
+            tc_wait_ld();
+            if (!mine) continue;
+            uint32_t y[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) y[c / 2] = pack_bf16(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                if (wide && c0 + c < p.a.D) {
+                    store32(to + c0 + c, y + c / 2);
+                } else {
+                    if (c0 + c < p.a.D) *reinterpret_cast<uint4*>(to + c0 + c) = make_uint4(y[c / 2], y[c / 2 + 1], y[c / 2 + 2], y[c / 2 + 3]);
+                    if (c0 + c + 8 < p.a.D)
+                        *reinterpret_cast<uint4*>(to + c0 + c + 8) = make_uint4(y[c / 2 + 4], y[c / 2 + 5], y[c / 2 + 6], y[c / 2 + 7]);
+                }
+            }
+        }
+        __syncwarp();
+        tc_fence_before();
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const PromptParams p, const __grid_constant__ CUtensorMap qmap,
+                                                                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using Lay = PromptLayout<DP>;
+    extern __shared__ __align__(1024) char smem[];
+    PromptShared& sh = *reinterpret_cast<PromptShared*>(smem + Lay::kBytes);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (warp == 8 && (tid & 31) < 3) {
+        const CUtensorMap* map = (tid & 31) == 0 ? &kmap : (tid & 31) == 1 ? &vmap : &qmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"((uint32_t)Lay::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        mbar_init(&sh.drain, 1);
+        for (int i = 0; i < Lay::kSlots; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+        }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_empty[i], 4 * Lay::kGroups + 1);   // softmax, products
+        }
+        mbar_init_fence();
+        sh.abort = 0;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp >= 8) {
+        if (Lay::kGroups == 2) registers_down<kRegsOthers>();
+        if (warp == 8) {
+            prompt_copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
+            prompt_statuses(p);   // while the last tiles are computed
+        } else if (warp == 9) {
+            if (!prompt_products_role<DP>(p, smem, sh)) drain(&sh.drain);
+        }
+    } else {
+        if (Lay::kGroups == 2) registers_up<kRegsRows>();
+        if (warp < 4 * Lay::kGroups) prompt_softmax_role<DP>(p, smem, sh, warp >> 2);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"((uint32_t)Lay::kCols));
+    }
+    if (warp == 8 && sh.abort) prompt_gave_up<unsigned short>(p, 0x7fff);
+}
+
+// ---------------------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------------------
+// [rows][heads][D] in boxes of 64 columns, some heads, some rows.
+static bool encode_rows(CUtensorMap* map, const void* base, const spec_prompt_args& a, int heads, int64_t stride, int box_heads, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)heads, (cuuint64_t)a.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 3, dims, strides, box);
+}
+
+template <int DP>
+static cudaError_t launch(PromptParams p, int sms, cudaStream_t s) {
+    using Lay = PromptLayout<DP>;
+    static std::atomic<int> ready[64];   // whether the device's kernel has its shared memory
+    constexpr int bytes = Lay::kBytes + (int)sizeof(PromptShared);
+    static_assert(bytes <= 232448, "shared memory of an SM");
+    p.piece = p.group * Lay::kGroups;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || ready[dev].load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes of;
+        e = cudaFuncGetAttributes(&of, prompt_tc_kernel<DP>);
+        if (e != cudaSuccess) return e;
+        if (Lay::kGroups == 2 && of.numRegs != kRegsStart) return cudaErrorInvalidConfiguration;   // the shares would not add up
+        e = cudaFuncSetAttribute(prompt_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_release);
+    }
+    CUtensorMap q, k, v;
+    if (!encode_rows(&q, p.a.q, p.a, p.a.Hq, p.a.q_row_stride, p.G, p.group) ||
+        !encode_rows(&k, p.a.k, p.a, p.a.Hkv, p.a.k_row_stride, 1, Lay::kKeys) ||
+        !encode_rows(&v, p.a.v, p.a, p.a.Hkv, p.a.v_row_stride, 1, Lay::kKeys))
+        return cudaErrorInvalidValue;
+    return launch_after(prompt_tc_kernel<DP>, dim3((unsigned)prompt_ctas(p, sms)), dim3(kPromptThreads), bytes, s, p, q, k, v);
+}
+
+cudaError_t launch_prompt_tc(const PromptParams& p, int sms, cudaStream_t s) {
+    if (p.a.D <= 64) return launch<64>(p, sms, s);
+    if (p.a.D <= 128) return launch<128>(p, sms, s);
+    return launch<256>(p, sms, s);
+}
+
+}  // namespace sv

@@ -1,0 +1,22 @@
+// Tiled copies (TMA): the map's encoding and the copy of a box.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace sv {
+
+// Element strides of 1, L2 sectors of 256 bytes, zeros outside the tensor; false where the map is refused (defined in attention_tc.cu).
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box);
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], "
+        "%6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+}  // namespace sv
