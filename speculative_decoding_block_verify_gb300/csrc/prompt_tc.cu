@@ -37,6 +37,7 @@ struct PromptLayout {
     static constexpr int kPanel = kKeys * 128;
     static constexpr int kSlotBytes = kHalves * kPanel;        // K or V of one tile
     static constexpr int kSlots = DP == 64 ? 10 : 5;
+    static constexpr int kPart = 64, kParts = kKeys / kPart;   // of P
     static constexpr int kBuffers = 2;                         // of S: a group's, or (one group) every other tile's
     static constexpr int kOCol = kBuffers * kKeys;
     static constexpr int kCols = 512;
@@ -53,7 +54,7 @@ struct PromptSegment {
 };
 
 struct PromptShared {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][4], o_done[2], drain;
     uint64_t full[10], empty[10];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     PromptSegment seg[kSegments];
@@ -167,7 +168,7 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
     int items[2] = {0, 0};                             // of each group so far
     unsigned k_at = 0, v_at = 1;                       // places in the ring, counted from the start: keys and values take turns
     unsigned s_count = 0;                              // (one group) products S so far
-    unsigned p_count[2] = {0, 0};                      // waits for P of each buffer so far
+    unsigned p_count[2] = {0, 0};                      // products of each buffer's P so far
     auto full = [&](unsigned at) { return warp_wait_for(&sh.full[at % Lay::kSlots], (at / Lay::kSlots) & 1, &sh.abort); };
     auto keys = [&](int g, int buf, bool last) {       // S of the tile at k_at
         const uint32_t a = desc_lo(q_at + g * Lay::kQBytes, 1), b = desc_lo(ring + k_at % Lay::kSlots * Lay::kSlotBytes, 1);
@@ -185,13 +186,19 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
     };
     auto values = [&](int g, int buf, bool add) {      // O += P V of the tile at v_at
         const uint32_t v = desc_lo(ring + v_at % Lay::kSlots * Lay::kSlotBytes, Lay::kPanel >> 4);
-        tc_fence_after();
-        if (elected()) {
+        const unsigned phase = p_count[buf]++ & 1;
 #pragma unroll
-            for (int k = 0; k < Lay::kKeys / 16; ++k)
-                mma_ts(tmem + Lay::kOCol + g * DP, tmem + buf * Lay::kKeys + k * 8, desc(v + 2 * k * (1024 >> 4), 1024 >> 4), pv, add || k > 0);
+        for (int part = 0; part < Lay::kParts; ++part) {
+            if (!warp_wait_for(&sh.p_full[buf][part], phase, &sh.abort)) return false;
+            tc_fence_after();
+            if (elected()) {
+#pragma unroll
+                for (int k = part * Lay::kPart / 16; k < (part + 1) * Lay::kPart / 16; ++k)
+                    mma_ts(tmem + Lay::kOCol + g * DP, tmem + buf * Lay::kKeys + k * 8, desc(v + 2 * k * (1024 >> 4), 1024 >> 4), pv, add || k > 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        return true;
     };
     auto release = [&](unsigned at) {
         if (elected()) mma_commit(&sh.empty[at % Lay::kSlots]);
@@ -233,8 +240,7 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (t < n[g]) {
-                        if (!warp_wait_for(&sh.p_full[g], p_count[g]++ & 1, &sh.abort)) return false;
-                        values(g, g, t > 0);
+                        if (!values(g, g, t > 0)) return false;
                         if (t == n[g] - 1) {
                             if (elected()) mma_commit(&sh.o_done[g]);
                             __syncwarp();
@@ -281,8 +287,7 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
                 if ((!last || after > 0) && !ahead(last, last ? after == 1 : t + 2 == tiles)) return false;
                 const int buf = o_count++ & 1;
                 if (!full(v_at)) return false;
-                if (!warp_wait_for(&sh.p_full[buf], p_count[buf]++ & 1, &sh.abort)) return false;
-                values(0, buf, t > 0);
+                if (!values(0, buf, t > 0)) return false;
                 if (elected()) mma_commit(&sh.o_done[buf]);
                 __syncwarp();
                 release(v_at);
@@ -293,6 +298,17 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
         }
     }
 }
+
+// Two sums and the bf16 pair w, each in one instruction.
+__device__ __forceinline__ void add_bf16(float2& sum, uint32_t w) {
+    asm("{\n\t.reg .b16 l, h, one;\n\tmov.b16 one, 0x3F80;\n\tmov.b32 {l, h}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, l, one, %0;\n\tfma.rn.f32.bf16 %1, h, one, %1;\n\t}"
+        : "+f"(sum.x), "+f"(sum.y)
+        : "r"(w));
+}
+
+// The lowest n bits of a word (none, or all, where n is outside 0 to 32).
+__device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // ---- warps 0 to 3, 4 to 7: softmax, scaling, output ----------------------------------------------
 template <int DP>
@@ -312,7 +328,7 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
         if (w.tiles == 0) return;
-        const int n = kGroups == 1 ? w.tiles : w.group_tiles[g];
+        const int n = kGroups == 1 ? w.tiles : g == 0 ? w.group_tiles[0] : w.group_tiles[1];
         const int fixes_from = g == 0 ? 0 : w.group_tiles[0];   // the tiles whose values this group looks after
         const int tokens = min(p.group, w.tokens - g * p.group);
         const int at_first = w.at + g * p.group, at_last = at_first + tokens - 1;
@@ -333,10 +349,12 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
             // a tile that every row sees whole needs no mask
             const bool clean = j0 + kKeys - 1 <= at_first && (p.a.window <= 0 || j0 > at_last - p.a.window || j0 + kKeys <= p.a.sinks);
             if (!clean) {
-                const int hi = at - j0, lo = low - j0, sk = p.a.sinks - j0;
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    if (!(c <= hi && (c >= lo || c < sk))) s[c] = 0xff800000u;
+                for (int c = 0; c < kKeys; c += 32) {   // a bit a column; a comparison each, as it comes from the compiler, takes 8,000 cycles
+                    const unsigned sees = below(at + 1 - j0 - c) & (~below(low - j0 - c) | below(p.a.sinks - j0 - c));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[c + i] = sees >> i & 1 ? s[c + i] : 0xff800000u;
+                }
             }
             float x[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
@@ -349,21 +367,6 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
                 m = top;
                 l *= scale_o;
             }
-            const float base = m == -kInf ? 0.f : m;
-            const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t pk[kKeys / 2];
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 2) {
-                const float2 y = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, nb);
-                // P V takes both operands in one type, so the weights are rounded to bf16, and the sum takes them as rounded
-                pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
-                sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], make_float2(bf16_lo(pk[c / 2]), bf16_hi(pk[c / 2])));
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < kKeys / 2; c += 32) tmem_st32(lanes + buf * kKeys + c, pk + c);
             if (t > 0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
                 // (two groups: S of this tile was issued behind the product before, so that is done)
                 if (kGroups == 1 && !warp_wait_for(&sh.o_done[buf ^ 1], ((n_all - 1) >> 1) & 1, &sh.abort)) return;
@@ -378,12 +381,10 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
                     tmem_st32(o_at + c, o);
                 }
             }
-            tc_wait_st();
-            tc_fence_before();
             // values of positions that no row of the item sees (another prompt's, or what lies behind the last): zeros, whatever is
             // there.  The first group that uses the tile sees to it, a position a thread, before its P is announced.
             const int from = min(kKeys, w.high - j0), lo = min(kKeys, max(0, w.low - j0)), sk = max(0, w.sink - j0);
-            if (t >= fixes_from && (from < kKeys || sk < lo)) {
+            if (!clean && t >= fixes_from && (from < kKeys || sk < lo)) {
                 const unsigned in = 2 * (tiles_all + t) + 1;
                 if (!warp_wait_for(&sh.full[in % Lay::kSlots], (in / Lay::kSlots) & 1, &sh.abort)) return;
                 if (tid < kKeys && (tid >= from || (tid >= sk && tid < lo))) {
@@ -393,9 +394,30 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
                         *reinterpret_cast<uint4*>(to + (c >> 3) * Lay::kPanel + (((c & 7) ^ (tid & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
+                __syncwarp();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+            const float base = m == -kInf ? 0.f : m;
+            const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int part = 0; part < Lay::kParts; ++part) {
+                uint32_t pk[Lay::kPart / 2];
+#pragma unroll
+                for (int c = 0; c < Lay::kPart; c += 2) {
+                    const int i = part * Lay::kPart + c;
+                    const float2 y = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc, nb);
+                    // P V takes both operands in one type, so the weights are rounded to bf16, and the sum takes them as rounded
+                    pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
+                    add_bf16(sum[(c >> 1) & 1], pk[c / 2]);
+                }
+                __syncwarp();
+                tmem_st32(lanes + buf * kKeys + part * 32, pk);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[buf][part]);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         tiles_all += w.tiles;
         if (n == 0) continue;
@@ -461,7 +483,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
             mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.o_done[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            for (int part = 0; part < Lay::kParts; ++part) mbar_init(&sh.p_full[i][part], 4);
         }
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);

@@ -105,7 +105,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
         SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24), "r"(addr)
         : "memory");
 }
-// ... eight, four columns
+// ... sixteen, eight, four columns
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::SV_W8(r, 0),
+        SV_W8(r, 8), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::SV_W8(r, 0), "r"(addr) : "memory");
 }
