@@ -50,6 +50,7 @@ extern "C" int spec_prompt_attention(const spec_prompt_args* a, void* stream) {
     p.by_G = divisor(p.G);
     p.group = 128 / p.G;
     p.piece = p.group;
+    p.rows_each = (int)(a->rows / a->B);
     // the kernels negate Q for a negative scale, and multiply masked scores of -inf by it
     p.scale_log2 = a->scale == 0.f ? 1e-30f : std::fabs((float)((double)a->scale * kLog2e));
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -18,6 +18,7 @@ struct PromptParams {
     int G;             // query heads per key head
     int group;         // tokens of a group of up to 128 rows
     int piece;         // tokens of a piece
+    int rows_each;     // without cu_rows: rows of a prompt
     Divisor by_G;
     float scale_log2;  // |scale| * log2(e)
 };
@@ -51,108 +52,102 @@ __device__ __forceinline__ int start_of(int sink_tiles, int first_tile, int t) {
     return (t < sink_tiles ? t : first_tile + t - sink_tiles) * kTile;
 }
 
-__device__ __forceinline__ int64_t prompt_row(const spec_prompt_args& a, int b) {
-    return a.cu_rows == nullptr ? (int64_t)b * (a.rows / a.B) : (int64_t)*(a.cu_rows + b);
-}
+// (there are fewer than 2^31 rows)
+__device__ __forceinline__ int prompt_row(const PromptParams& p, int b) { return p.a.cu_rows == nullptr ? b * p.rows_each : *(p.a.cu_rows + b); }
 // Offsets that break the packing at prompt b: it and the prompts behind it are not defined.
-__device__ __forceinline__ bool prompt_broken(const spec_prompt_args& a, int b, int64_t row0, int64_t end) {
-    return end < row0 || (b == 0 && row0 != 0) || end > a.rows;
+__device__ __forceinline__ bool prompt_broken(const PromptParams& p, int b, int row0, int end) {
+    return end < row0 || (b == 0 && row0 != 0) || end > (int)p.a.rows;
 }
 
 // The CTA's items, found by one warp together (all 32 lanes call, all know the result).  A batch of kBatch prompts at a time: ranks go
-// through the first batch's items, then the second's.
+// through the first batch's items, then the second's.  Ranks fit 32 bits: an item that is not a prompt's last has 64 rows of Q or more, 1 KB,
+// and there are at most 2^26 last ones.  The code is short on purpose: it runs once an item beside all the other roles, and what it
+// takes of the place where instructions are kept is theirs (54 KB of it, divided and unrolled without need, took a fifth of the time of prompts of 500 tokens).
 struct PromptWalk {
     static constexpr int kEach = 8, kBatch = 32 * kEach;
     int pieces[kEach];   // of prompt first + 32 i + lane
     int first;           // the batch's first prompt
-    int most, total;     // pieces of its longest prompt, and of all
-    int64_t base;        // items of the batches before
-    int64_t round;
+    unsigned total;      // pieces of the batch
+    unsigned base;       // items of the batches before
+    unsigned round;
     bool ended;          // no batch behind this one
 
-    __device__ __forceinline__ int above(int level) const {   // pieces of the batch with a number of `level` or more
+    __device__ __forceinline__ unsigned above(int level) const {   // pieces of the batch with a number of `level` or more
         int s = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) s += max(0, pieces[i] - level);
-        return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
+        return __reduce_add_sync(0xffffffffu, (unsigned)s);
     }
-    __device__ __forceinline__ void load(const PromptParams& p, int from) {
+    __device__ __forceinline__ void load(const PromptParams& p) {   // the batch at `first`
         const int lane = threadIdx.x & 31;
-        int bad = INT32_MAX, top = 0;
+        int bad = INT32_MAX;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int b = from + 32 * i + lane;
+            const int b = first + 32 * i + lane;
             pieces[i] = 0;
             if (b < p.a.B) {
-                const int64_t row0 = prompt_row(p.a, b), end = prompt_row(p.a, b + 1);
-                if (prompt_broken(p.a, b, row0, end))
+                const int row0 = prompt_row(p, b), end = prompt_row(p, b + 1);
+                if (prompt_broken(p, b, row0, end))
                     bad = min(bad, b);
                 else
-                    pieces[i] = (int)((end - row0 + p.piece - 1) / p.piece);
+                    pieces[i] = (unsigned)(end - row0 + p.piece - 1) / (unsigned)p.piece;
             }
         }
         bad = __reduce_min_sync(0xffffffffu, bad);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (from + 32 * i + lane >= bad) pieces[i] = 0;
-            top = max(top, pieces[i]);
-        }
-        first = from;
-        most = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+        for (int i = 0; i < kEach; ++i)
+            if (first + 32 * i + lane >= bad) pieces[i] = 0;
         total = above(0);
-        ended = bad != INT32_MAX || from + kBatch >= p.a.B;
+        ended = bad != INT32_MAX || first + kBatch >= p.a.B;
     }
-    __device__ __forceinline__ void start(const PromptParams& p) {
-        base = 0;
-        round = 0;
-        load(p, 0);
+    __device__ __forceinline__ void start() {
+        base = total = round = 0;
+        first = -kBatch;
+        ended = false;
     }
     // The next item; false: there are no more.
     __device__ __forceinline__ bool next(const PromptParams& p, Piece* out) {
         const int lane = threadIdx.x & 31;
-        const int64_t rank = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const unsigned rank = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         ++round;
-        while (rank >= base + (int64_t)total * p.a.Hkv) {
+        while (rank >= base + total * (unsigned)p.a.Hkv) {
             if (ended) return false;
-            base += (int64_t)total * p.a.Hkv;
-            load(p, first + kBatch);
+            base += total * (unsigned)p.a.Hkv;
+            first += kBatch;
+            load(p);
         }
-        const int64_t at = rank - base;
-        int r;
-        if (at >> 32)
-            r = (int)(at / p.a.Hkv);
-        else
-            r = (int)((uint32_t)at / (uint32_t)p.a.Hkv);
-        out->head = (int)(at - (int64_t)r * p.a.Hkv);
+        const unsigned at = rank - base, r = at / (unsigned)p.a.Hkv;
+        out->head = (int)(at - r * (unsigned)p.a.Hkv);
         // the lowest level above which lie no more than r pieces
-        int lo = 0, hi = most - 1;
+        int top = pieces[0];
+#pragma unroll
+        for (int i = 1; i < kEach; ++i) top = max(top, pieces[i]);
+        int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)top) - 1;
+        unsigned over = 0;   // pieces above level hi
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (above(mid + 1) <= r)
+            const unsigned n = above(mid + 1);
+            if (n <= r) {
                 hi = mid;
-            else
+                over = n;
+            } else {
                 lo = mid + 1;
-        }
-        int nth = r - above(lo + 1), b = 0;
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const unsigned has = __ballot_sync(0xffffffffu, pieces[i] > lo);
-            if (!found) {
-                const int n = __popc(has);
-                if (nth < n) {
-                    // the lane whose bit is number nth: the one that has nth bits below its own
-                    const bool me = ((has >> lane) & 1) && __popc(has & ((1u << lane) - 1)) == nth;
-                    b = first + 32 * i + __ffs((int)__ballot_sync(0xffffffffu, me)) - 1;
-                    found = true;
-                } else {
-                    nth -= n;
-                }
             }
         }
+        // the prompts with a piece of that level, in order: number r - over of them
+        int nth = (int)(r - over), b = -1;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const unsigned has = __ballot_sync(0xffffffffu, pieces[i] > lo), me = 1u << lane;
+            // the lane whose bit is there and has nth bits below its own
+            if ((has & me) != 0 && __popc(has & (me - 1)) == nth) b = first + 32 * i + lane;
+            nth -= __popc(has);
+        }
+        b = __reduce_max_sync(0xffffffffu, b);
         out->b = b;
-        out->row0 = prompt_row(p.a, b);
-        out->n = (int)(prompt_row(p.a, b + 1) - out->row0);
+        const int row0 = prompt_row(p, b);
+        out->row0 = row0;
+        out->n = prompt_row(p, b + 1) - row0;
         out->at = lo * p.piece;
         out->tokens = min(p.piece, out->n - out->at);
         return true;
@@ -166,7 +161,7 @@ __device__ __forceinline__ void prompt_statuses(const PromptParams& p) {
     int bad = INT32_MAX;
     for (int b0 = 0; b0 < p.a.B && bad == INT32_MAX; b0 += 32) {
         const int b = b0 + lane;
-        if (b < p.a.B && prompt_broken(p.a, b, prompt_row(p.a, b), prompt_row(p.a, b + 1))) bad = b;
+        if (b < p.a.B && prompt_broken(p, b, prompt_row(p, b), prompt_row(p, b + 1))) bad = b;
         bad = __reduce_min_sync(0xffffffffu, bad);
     }
     for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.a.B; b += (int64_t)gridDim.x * 32)
@@ -175,11 +170,11 @@ __device__ __forceinline__ void prompt_statuses(const PromptParams& p) {
 
 // A wait of this CTA gave up: one warp leaves NaN in the rows of all its items.
 template <typename T>
-__device__ __forceinline__ void prompt_gave_up(const PromptParams& p, T nan) {
+__device__ __noinline__ void prompt_gave_up(const PromptParams& p, T nan) {
     const int lane = threadIdx.x & 31;
     PromptWalk w;
     Piece it;
-    w.start(p);
+    w.start();
     while (w.next(p, &it)) {
         const int per = p.G * p.a.D;
         for (int t = 0; t < it.tokens; ++t) {

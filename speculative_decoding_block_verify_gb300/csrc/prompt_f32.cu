@@ -53,7 +53,7 @@ __device__ __forceinline__ void prompt_f32_copy_role(const PromptParams& p, cons
             phase ^= 1;
         }
     };
-    w.start(p);
+    w.start();
     bool more = w.next(p, &it);
     tell(more);
     while (more && ok) {

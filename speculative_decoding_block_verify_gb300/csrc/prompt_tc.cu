@@ -10,7 +10,7 @@
 //
 // Warps 0 to 3 and 4 to 7 are a group's softmax, a row per thread (TMEM lane = row): the row's running maximum and sum in registers, O scaled in
 // tensor memory when the maximum has risen by more than 8 (2^8 of headroom is nothing to float32, and most tiles then leave O alone).
-// Warp 8 finds the items and copies by TMA, warp 9 issues the products.
+// Warp 11 finds the items, warp 8 copies keys and values by TMA, warp 10 the rows of Q, warp 9 issues the products.
 
 #include <atomic>
 
@@ -37,7 +37,7 @@ struct PromptLayout {
     static constexpr int kPanel = kKeys * 128;
     static constexpr int kSlotBytes = kHalves * kPanel;        // K or V of one tile
     static constexpr int kSlots = DP == 64 ? 10 : 5;
-    static constexpr int kPart = 64, kParts = kKeys / kPart;   // of P
+    static constexpr int kHalf = kKeys / 2;                    // P comes in two halves
     static constexpr int kBuffers = 2;                         // of S: a group's, or (one group) every other tile's
     static constexpr int kOCol = kBuffers * kKeys;
     static constexpr int kCols = 512;
@@ -54,7 +54,7 @@ struct PromptSegment {
 };
 
 struct PromptShared {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][4], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2], drain;
     uint64_t full[10], empty[10];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     PromptSegment seg[kSegments];
@@ -62,27 +62,23 @@ struct PromptShared {
     int abort;
 };
 
-// ---- warp 8: the walk over the CTA's items, and the copies ------------------------------------
+// ---- warp 11: the walk over the CTA's items ------------------------------------------------------
 template <int DP>
-__device__ __forceinline__ void prompt_copy_role(const PromptParams& p, const CUtensorMap* qmap, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                                 char* smem, PromptShared& sh) {
+__device__ __forceinline__ void prompt_walk_role(const PromptParams& p, PromptShared& sh) {
     using Lay = PromptLayout<DP>;
     const int lane = threadIdx.x & 31;
-    const uint32_t q_at = smem_u32(smem), ring = q_at + Lay::kGroups * Lay::kQBytes;
-    const uint64_t stay = l2_evict_normal_policy();
     PromptWalk w;
     Piece it = {};
-    Keys keys = {};
-    int told = 0, slot = 0, q_copies[2] = {0, 0};
-    unsigned phase = 1;   // a fresh barrier: the phase before its first is done
-    bool ok = true;
-    auto tell = [&](bool any) {   // the next item, or that there is none
+    w.start();
+    for (int told = 0;; ++told) {
+        const bool any = w.next(p, &it);
         PromptSegment& seg = sh.seg[told % kSegments];
-        ok = ok && warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort);
-        if (any) keys = keys_of<Lay::kKeys>(p, it.at, it.tokens);
-        if (ok && lane == 0) {
-            seg.tiles = any ? keys.tiles : 0;
+        if (!warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort)) return;
+        if (lane == 0) {
+            seg.tiles = 0;
             if (any) {
+                const Keys keys = keys_of<Lay::kKeys>(p, it.at, it.tokens);
+                seg.tiles = keys.tiles;
 #pragma unroll
                 for (int g = 0; g < Lay::kGroups; ++g) {
                     const int mine = min(p.group, it.tokens - g * p.group), last = it.at + g * p.group + mine - 1;
@@ -95,8 +91,20 @@ __device__ __forceinline__ void prompt_copy_role(const PromptParams& p, const CU
             mbar_arrive(&sh.seg_full[told % kSegments]);
         }
         __syncwarp();
-        ++told;
-    };
+        if (!any) return;
+    }
+}
+
+// ---- warp 8: keys and values ------------------------------------------------------------------
+template <int DP>
+__device__ __forceinline__ void prompt_copy_role(const CUtensorMap* kmap, const CUtensorMap* vmap, char* smem, PromptShared& sh) {
+    using Lay = PromptLayout<DP>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(smem) + Lay::kGroups * Lay::kQBytes;
+    const uint64_t stay = l2_evict_normal_policy();
+    int slot = 0;
+    unsigned phase = 1;   // a fresh barrier: the phase before its first is done
+    bool ok = true;
     auto copy = [&](const CUtensorMap* map, int head, int row) {
         ok = ok && warp_wait_for(&sh.empty[slot], phase, &sh.abort);
         if (!ok) return;
@@ -112,45 +120,66 @@ __device__ __forceinline__ void prompt_copy_role(const PromptParams& p, const CU
             phase ^= 1;
         }
     };
-    w.start(p);
-    bool more = w.next(p, &it);
-    tell(more);
-    while (more && ok) {
-        const int tiles = keys.tiles;
+    for (int n_seg = 0; ok; ++n_seg) {
+        const int place = n_seg % kSegments;
+        ok = warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort);
+        if (!ok) break;
+        const int tiles = sh.seg[place].tiles, head = sh.seg[place].head, row0 = (int)sh.seg[place].row0;
+        const int sink_tiles = sh.seg[place].sink_tiles, first_tile = sh.seg[place].first_tile;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
+        if (tiles == 0) return;
         for (int t = 0; t < tiles && ok; ++t) {
-            const int row = (int)it.row0 + start_of<Lay::kKeys>(keys.sink_tiles, keys.first_tile, t);
-            const int head = it.head;
+            const int row = row0 + start_of<Lay::kKeys>(sink_tiles, first_tile, t);
             copy(kmap, head, row);
-            if (t == 0) {
-#pragma unroll
-                for (int g = 0; g < Lay::kGroups; ++g) {
-                    if (g * p.group >= it.tokens) break;
-                    ok = ok && warp_wait_for(&sh.q_empty[g], (q_copies[g] & 1) ^ 1, &sh.abort);
-                    if (ok && lane == 0) {
-                        mbar_expect_tx(&sh.q_full[g], Lay::kHalves * p.group * p.G * 128);
-#pragma unroll
-                        for (int half = 0; half < Lay::kHalves; ++half)
-                            tma_load_3d(q_at + g * Lay::kQBytes + half * Lay::kQPanel, qmap, half * 64, head * p.G,
-                                        (int)it.row0 + it.at + g * p.group, &sh.q_full[g], stay);
-                    }
-                    __syncwarp();
-                    ++q_copies[g];
-                }
-            }
-            if (t == tiles - 1) {   // the next item is known before the last values are waited for
-                more = w.next(p, &it);
-                tell(more);
-            }
             copy(vmap, head, row);
         }
     }
-    if (!ok) {   // gave up: whatever was copied must have arrived before the CTA's memory is given back
-        for (int s = 0; s < Lay::kSlots; ++s)
-            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
+    // gave up: whatever was copied must have arrived before the CTA's memory is given back
+    for (int s = 0; s < Lay::kSlots; ++s)
+        for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
+}
+
+// ---- warp 10: the rows of Q ----------------------------------------------------------------------
+// An item's rows are on their way to L2 as soon as it is known, and to shared memory when the item before has no more use of its own.
+template <int DP>
+__device__ __forceinline__ void prompt_queries_role(const PromptParams& p, const CUtensorMap* qmap, char* smem, PromptShared& sh) {
+    using Lay = PromptLayout<DP>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t q_at = smem_u32(smem);
+    const uint64_t stay = l2_evict_normal_policy();
+    unsigned copies[2] = {0, 0};
+    bool ok = true;
+    for (int n_seg = 0; ok; ++n_seg) {
+        const int place = n_seg % kSegments;
+        ok = warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort);
+        if (!ok) break;
+        const int tiles = sh.seg[place].tiles, tokens = sh.seg[place].tokens, head = sh.seg[place].head * p.G;
+        const int row = (int)sh.seg[place].row0 + sh.seg[place].at;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
+        if (tiles == 0) break;
+        if (lane < Lay::kHalves * Lay::kGroups && lane / Lay::kHalves * p.group < tokens)
+            tma_prefetch_3d(qmap, lane % Lay::kHalves * 64, head, row + lane / Lay::kHalves * p.group);
+#pragma unroll
+        for (int g = 0; g < Lay::kGroups; ++g) {
+            if (g * p.group >= tokens) break;
+            ok = ok && warp_wait_for(&sh.q_empty[g], (copies[g] & 1) ^ 1, &sh.abort);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_expect_tx(&sh.q_full[g], Lay::kHalves * p.group * p.G * 128);
+#pragma unroll
+                for (int half = 0; half < Lay::kHalves; ++half)
+                    tma_load_3d(q_at + g * Lay::kQBytes + half * Lay::kQPanel, qmap, half * 64, head, row + g * p.group, &sh.q_full[g], stay);
+            }
+            __syncwarp();
+            ++copies[g];
+        }
+    }
+    if (!ok)
 #pragma unroll
         for (int g = 0; g < Lay::kGroups; ++g)
-            for (int n = 0; q_copies[g] > 0 && n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.q_full[g], (q_copies[g] - 1) & 1); ++n) {}
-    }
+            for (int n = 0; copies[g] > 0 && n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.q_full[g], (copies[g] - 1) & 1); ++n) {}
 }
 
 // ---- warp 9: products -------------------------------------------------------------------------
@@ -188,12 +217,12 @@ __device__ __forceinline__ bool prompt_products_role(const PromptParams& p, char
         const uint32_t v = desc_lo(ring + v_at % Lay::kSlots * Lay::kSlotBytes, Lay::kPanel >> 4);
         const unsigned phase = p_count[buf]++ & 1;
 #pragma unroll
-        for (int part = 0; part < Lay::kParts; ++part) {
+        for (int part = 0; part < 2; ++part) {
             if (!warp_wait_for(&sh.p_full[buf][part], phase, &sh.abort)) return false;
             tc_fence_after();
             if (elected()) {
 #pragma unroll
-                for (int k = part * Lay::kPart / 16; k < (part + 1) * Lay::kPart / 16; ++k)
+                for (int k = part * Lay::kHalf / 16; k < (part + 1) * Lay::kHalf / 16; ++k)
                     mma_ts(tmem + Lay::kOCol + g * DP, tmem + buf * Lay::kKeys + k * 8, desc(v + 2 * k * (1024 >> 4), 1024 >> 4), pv, add || k > 0);
             }
             __syncwarp();
@@ -310,11 +339,59 @@ __device__ __forceinline__ void add_bf16(float2& sum, uint32_t w) {
 // The lowest n bits of a word (none, or all, where n is outside 0 to 32).
 __device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
+// Maxima of n scores, in four chains of three-way maxima.
+template <int n>
+__device__ __forceinline__ void tops(const uint32_t* s, float (&x)[4]) {
+#pragma unroll
+    for (int c = 0; c < n; c += 2) x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+}
+// Weights 2^(s scale - base) as bf16 pairs, and their sums.  P V takes both operands in one type, so the weights are rounded to bf16, and the
+// sum takes them as rounded.
+template <int n>
+__device__ __forceinline__ void weights(const uint32_t* s, float2 scale, float2 minus_base, uint32_t* pk, float2 (&sum)[2]) {
+#pragma unroll
+    for (int c = 0; c < n; c += 2) {
+        const float2 y = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale, minus_base);
+        pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
+        add_bf16(sum[(c >> 1) & 1], pk[c / 2]);
+    }
+}
+// Lanes l and l ^ mask exchange: of pieces i and i | mask (8 words each) the lane whose bit is 0 keeps i and gives the other, and
+// so on.  With masks 1 and 2 lane l ends up with piece l & 3 of the four lanes' rows, in their order.
+__device__ __forceinline__ void swap_pieces(uint32_t (&y)[32], int mask) {
+    const bool up = (threadIdx.x & mask) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i & mask) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t& a = y[8 * i + c];
+            uint32_t& b = y[8 * (i | mask) + c];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, mask);
+            a = up ? got : a;
+            b = up ? b : got;
+        }
+    }
+}
+// Half of a tile's P to tensor memory, and the products' warp told.
+template <int n>
+__device__ __forceinline__ void announce(uint32_t at, const uint32_t* pk, uint64_t* bar) {
+    __syncwarp();
+    if constexpr (n == 64)
+        tmem_st32(at, pk);
+    else
+        tmem_st16(at, pk);
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // ---- warps 0 to 3, 4 to 7: softmax, scaling, output ----------------------------------------------
 template <int DP>
 __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char* smem, PromptShared& sh, int g) {
     using Lay = PromptLayout<DP>;
-    constexpr int kKeys = Lay::kKeys, kGroups = Lay::kGroups;
+    constexpr int kKeys = Lay::kKeys, kGroups = Lay::kGroups, kHalf = Lay::kHalf;
     const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
     const uint32_t lanes = sh.tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t o_at = lanes + Lay::kOCol + g * DP;
@@ -352,14 +429,14 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {   // a bit a column; a comparison each, as it comes from the compiler, takes 8,000 cycles
                     const unsigned sees = below(at + 1 - j0 - c) & (~below(low - j0 - c) | below(p.a.sinks - j0 - c));
+                    if (__any_sync(0xffffffffu, sees != ~0u)) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[c + i] = sees >> i & 1 ? s[c + i] : 0xff800000u;
+                        for (int i = 0; i < 32; ++i) s[c + i] = sees >> i & 1 ? s[c + i] : 0xff800000u;
+                    }
                 }
             }
             float x[4] = {-kInf, -kInf, -kInf, -kInf};
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 2)   // three-way maxima
-                x[(c >> 1) & 3] = fmaxf(fmaxf(x[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+            tops<kKeys>(s, x);
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;   // the scale is positive here
             float scale_o = 1.f;
             if (mine && top > m + 8.f) {   // lanes without a row never ask for the scaling of O
@@ -400,22 +477,10 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
             const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int part = 0; part < Lay::kParts; ++part) {
-                uint32_t pk[Lay::kPart / 2];
-#pragma unroll
-                for (int c = 0; c < Lay::kPart; c += 2) {
-                    const int i = part * Lay::kPart + c;
-                    const float2 y = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc, nb);
-                    // P V takes both operands in one type, so the weights are rounded to bf16, and the sum takes them as rounded
-                    pk[c / 2] = pack_bf16(ex2(y.x), ex2(y.y));
-                    add_bf16(sum[(c >> 1) & 1], pk[c / 2]);
-                }
-                __syncwarp();
-                tmem_st32(lanes + buf * kKeys + part * 32, pk);
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[buf][part]);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[kHalf / 2];
+                weights<kHalf>(s + half * kHalf, sc, nb, pk, sum);
+                announce<kHalf>(lanes + buf * kKeys + half * (kHalf / 2), pk, &sh.p_full[buf][half]);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
@@ -427,28 +492,30 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
         ++items;
         tc_fence_after();
         const float inv = 1.f / l;
-        unsigned short* const to = reinterpret_cast<unsigned short*>(p.a.out) +
-                                   ((w.row0 + at) * p.a.Hq + w.head * p.G + query) * (int64_t)p.a.D;
+        unsigned short* const first = reinterpret_cast<unsigned short*>(p.a.out) + ((w.row0 + at_first) * p.a.Hq + w.head * p.G) * (int64_t)p.a.D;
 #pragma unroll 1
         for (int c0 = 0; c0 < p.a.D; c0 += 64) {
-            uint32_t o[64];
+            uint32_t o[64], y[32];
             __syncwarp();
             tmem_ld32(o_at + c0, o);
             tmem_ld32(o_at + c0 + 32, o + 32);
             tc_wait_ld();
-            if (!mine) continue;
-            uint32_t y[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 2) y[c / 2] = pack_bf16(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
+            if (wide && p.a.D - c0 >= 64) {
+                // four lanes swap pieces of 32 bytes, so that a store writes whole lines of eight rows instead of pieces of 32
+                swap_pieces(y, 1);
+                swap_pieces(y, 2);
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-                if (wide && c0 + c < p.a.D) {
-                    store32(to + c0 + c, y + c / 2);
-                } else {
-                    if (c0 + c < p.a.D) *reinterpret_cast<uint4*>(to + c0 + c) = make_uint4(y[c / 2], y[c / 2 + 1], y[c / 2 + 2], y[c / 2 + 3]);
-                    if (c0 + c + 8 < p.a.D)
-                        *reinterpret_cast<uint4*>(to + c0 + c + 8) = make_uint4(y[c / 2 + 4], y[c / 2 + 5], y[c / 2 + 6], y[c / 2 + 7]);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (tid & ~3) + i, token = p.by_G.of(row);
+                    if (token < tokens) store32(first + (int64_t)token * p.a.Hq * p.a.D + (row - token * p.G) * p.a.D + c0 + (tid & 3) * 16, y + 8 * i);
                 }
+            } else if (mine) {
+                unsigned short* const to = first + (int64_t)token_in * p.a.Hq * p.a.D + query * p.a.D + c0;
+#pragma unroll
+                for (int c = 0; c < 64; c += 8)
+                    if (c0 + c < p.a.D) *reinterpret_cast<uint4*>(to + c) = make_uint4(y[c / 2], y[c / 2 + 1], y[c / 2 + 2], y[c / 2 + 3]);
             }
         }
         __syncwarp();
@@ -483,11 +550,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
             mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.o_done[i], 1);
-            for (int part = 0; part < Lay::kParts; ++part) mbar_init(&sh.p_full[i][part], 4);
+            for (int half = 0; half < 2; ++half) mbar_init(&sh.p_full[i][half], 4);
         }
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 4 * Lay::kGroups + 1);   // softmax, products
+            mbar_init(&sh.seg_empty[i], 4 * Lay::kGroups + 3);   // softmax, copies of keys and values, of queries, products
         }
         mbar_init_fence();
         sh.abort = 0;
@@ -500,10 +567,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
     if (warp >= 8) {
         if (Lay::kGroups == 2) registers_down<kRegsOthers>();
         if (warp == 8) {
-            prompt_copy_role<DP>(p, &qmap, &kmap, &vmap, smem, sh);
-            prompt_statuses(p);   // while the last tiles are computed
+            prompt_copy_role<DP>(&kmap, &vmap, smem, sh);
         } else if (warp == 9) {
             if (!prompt_products_role<DP>(p, smem, sh)) drain(&sh.drain);
+        } else if (warp == 10) {
+            prompt_queries_role<DP>(p, &qmap, smem, sh);
+        } else {
+            prompt_walk_role<DP>(p, sh);
+            prompt_statuses(p);   // while the last tiles are computed
         }
     } else {
         if (Lay::kGroups == 2) registers_up<kRegsRows>();
