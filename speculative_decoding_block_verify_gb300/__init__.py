@@ -677,17 +677,28 @@ def _on(t, name, device, dtype, shape):
 def _rows_of(t, name, device, dtype, heads, D):
     """(pointer, row stride) of [rows, heads, D] with dense rows (a slice of a wider projection)."""
     shape = t.shape
+    if t.get_device() == device and t.dtype is dtype and len(shape) == 3:
+        rows, h, d = shape
+        row, head, one = t.stride()
+        dense = heads * D
+        if h == heads and d == D and one == 1 and (head == D or heads == 1) and (row >= dense or rows <= 1):
+            return t.data_ptr(), row if row > dense else dense
     if t.get_device() != device:
         raise TypeError(f"{name} must be a CUDA tensor on the cache's device")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
     if len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{name} must be [rows, {heads}, {D}], got {list(shape)}")
-    row, head, one = t.stride()
-    dense = heads * D
-    if one != 1 or (head != D and heads > 1) or (row < dense and shape[0] > 1):
-        raise ValueError(f"{name} must have dense rows of heads * D elements")
-    return t.data_ptr(), row if row > dense else dense
+    raise ValueError(f"{name} must have dense rows of heads * D elements")
+
+
+def _rows_into(t, name, device, dtype, rows, heads, D):
+    """(pointer, row stride) of an output [rows, heads, D] with dense rows."""
+    if t.is_contiguous() and t.dtype is dtype and t.get_device() == device and t.shape == (rows, heads, D):
+        return t.data_ptr(), heads * D
+    if len(t.shape) == 3 and t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
+    return _rows_of(t, name, device, dtype, heads, D)
 
 
 def _layer_of(k_pages, v_pages):
@@ -974,9 +985,7 @@ def spec_rotate(x, positions, rotary, out=None, stream=None):
     if out is None:
         with _made_on(stream):
             out = torch.empty(shape, dtype=dtype, device=x.device)
-    op, os_ = _rows_of(out, "out", device, dtype, heads, D)
-    if out.shape[0] != rows:
-        raise ValueError("out must have x's rows")
+    op, os_ = _rows_into(out, "out", device, dtype, rows, heads, D)
     rc = (_lib or lib()).spec_rotate(_ROTATE.pack(
         heads, D, rotary.dim, rotary.interleaved, code, rotary.magnitude, rows, rotary._on(device),
         _on(positions, "positions", device, _I32, (rows,)), xp, xs, op, os_), _raw_stream(stream, device))
@@ -1034,13 +1043,9 @@ def spec_cache_append_rotated(q, k, v, k_pages, v_pages, page_table, length, rot
                    "status": torch.empty(B, dtype=torch.int32, device=k.device)}
     oq = oqs = ok = oks = 0
     if q is not None:
-        oq, oqs = _rows_of(out["q"], "out['q']", device, dtype, Hq, D)
-        if out["q"].shape[0] != rows:
-            raise ValueError("out['q'] must have q's rows")
+        oq, oqs = _rows_into(out["q"], "out['q']", device, dtype, rows, Hq, D)
     if keep_keys:
-        ok, oks = _rows_of(out["k"], "out['k']", device, dtype, Hkv, D)
-        if out["k"].shape[0] != rows:
-            raise ValueError("out['k'] must have k's rows")
+        ok, oks = _rows_into(out["k"], "out['k']", device, dtype, rows, Hkv, D)
     rc = (_lib or lib()).spec_cache_append_rotated(_APPEND_ROTATED.pack(
         B, most, extra, Hq, Hkv, D, page_size, num_pages, shape[1], code, rotary.dim, rotary.interleaved, rotary.magnitude,
         rotary._on(device), cu, _on(length, "length", device, _I32, (B,)), _on(page_table, "page_table", device, _I32, shape),
