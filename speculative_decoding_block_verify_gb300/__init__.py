@@ -674,15 +674,15 @@ def _on(t, name, device, dtype, shape):
     return t.data_ptr()
 
 
-def _rows_of(t, name, device, dtype, heads, D):
-    """(pointer, row stride) of [rows, heads, D] with dense rows (a slice of a wider projection)."""
+def _packed(t, name, device, dtype, heads, D):
+    """(pointer, row stride, rows) of [rows, heads, D] with dense rows (a slice of a wider projection)."""
     shape = t.shape
     if t.get_device() == device and t.dtype is dtype and len(shape) == 3:
         rows, h, d = shape
         row, head, one = t.stride()
         dense = heads * D
         if h == heads and d == D and one == 1 and (head == D or heads == 1) and (row >= dense or rows <= 1):
-            return t.data_ptr(), row if row > dense else dense
+            return t.data_ptr(), row if row > dense else dense, rows
     if t.get_device() != device:
         raise TypeError(f"{name} must be a CUDA tensor on the cache's device")
     if t.dtype is not dtype:
@@ -690,6 +690,11 @@ def _rows_of(t, name, device, dtype, heads, D):
     if len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{name} must be [rows, {heads}, {D}], got {list(shape)}")
     raise ValueError(f"{name} must have dense rows of heads * D elements")
+
+
+def _rows_of(t, name, device, dtype, heads, D):
+    """(pointer, row stride) of such a tensor."""
+    return _packed(t, name, device, dtype, heads, D)[:2]
 
 
 def _rows_into(t, name, device, dtype, rows, heads, D):
@@ -899,14 +904,14 @@ def spec_prompt_attention(q, k, v, cu_rows, scale, window=0, sinks=0, out=None, 
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    if len(shape) != 3 or len(k.shape) != 3:
+    if len(shape) != 3 or k.dim() != 3:
         raise ValueError("q must be [rows, Hq, D] and k [rows, Hkv, D]")
     rows, Hq, D = shape
-    Hkv = k.shape[1]
+    Hkv = k.size(1)
     qp, qs = _rows_of(q, "q", device, dtype, Hq, D)
-    kp, ks = _rows_of(k, "k", device, dtype, Hkv, D)
-    vp, vs = _rows_of(v, "v", device, dtype, Hkv, D)
-    if k.shape[0] != rows or v.shape[0] != rows:
+    kp, ks, k_rows = _packed(k, "k", device, dtype, Hkv, D)
+    vp, vs, v_rows = _packed(v, "v", device, dtype, Hkv, D)
+    if k_rows != rows or v_rows != rows:
         raise ValueError("q, k and v must have the same rows")
     if cu_rows is None:
         B, cu = 1, 0
@@ -1007,17 +1012,17 @@ def spec_cache_append_rotated(q, k, v, k_pages, v_pages, page_table, length, rot
     torch = _T or _cache_torch()
     device, code, kpp, vpp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
     dtype = k_pages.dtype
-    nk, ks = _rows_of(k, "k", device, dtype, Hkv, D)
-    nv, vs = _rows_of(v, "v", device, dtype, Hkv, D)
-    rows = k.shape[0]
-    if v.shape[0] != rows or (q is not None and q.shape[0] != rows):
-        raise ValueError("q, k and v must have the same rows")
+    nk, ks, rows = _packed(k, "k", device, dtype, Hkv, D)
+    nv, vs, v_rows = _packed(v, "v", device, dtype, Hkv, D)
     Hq = nq = qs = 0
+    q_rows = rows
     if q is not None:
-        if len(q.shape) != 3:
+        if q.dim() != 3:
             raise ValueError("q must be [rows, Hq, D]")
-        Hq = q.shape[1]
-        nq, qs = _rows_of(q, "q", device, dtype, Hq, D)
+        Hq = q.size(1)
+        nq, qs, q_rows = _packed(q, "q", device, dtype, Hq, D)
+    if v_rows != rows or q_rows != rows:
+        raise ValueError("q, k and v must have the same rows")
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
