@@ -57,15 +57,13 @@ __device__ __forceinline__ void prepare_row(const Turn& t, int p, float2* cs) {
 
 __device__ __forceinline__ float2 turned(float a, float b, float2 cs) { return make_float2(a * cs.x - b * cs.y, b * cs.x + a * cs.y); }
 
-// What a thread moves in one step.
+// 16 bytes as floats and back.
 template <typename T>
 struct Wide;
 template <>
 struct Wide<unsigned short> {
     static constexpr int kPer = 8;
-    float x[8];
-    __device__ __forceinline__ void load(const unsigned short* p) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
+    static __device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -73,7 +71,7 @@ struct Wide<unsigned short> {
             x[2 * i + 1] = bf16_hi(u[i]);
         }
     }
-    __device__ __forceinline__ uint4 pack() const {
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
@@ -83,12 +81,10 @@ struct Wide<unsigned short> {
 template <>
 struct Wide<float> {
     static constexpr int kPer = 4;
-    float x[4];
-    __device__ __forceinline__ void load(const float* p) {
-        const float4 w = *reinterpret_cast<const float4*>(p);
-        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    static __device__ __forceinline__ void unpack(uint4 w, float (&x)[4]) {
+        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
     }
-    __device__ __forceinline__ uint4 pack() const {
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
 };
@@ -97,89 +93,134 @@ __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ void store(unsigned short* p, float x) { *p = __bfloat16_as_ushort(__float2bfloat16(x)); }
 __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 
-// Unit u of a head, to one place or two (also == nullptr: one).  `from` may be a destination: what a thread writes is what it read.
+// A unit of a head, as it was read.  The next one is read before this one is turned and written (what is written may be the place that
+// was read, but a unit is one thread's alone), and the first one before the row's sines are there.
 template <typename T, bool kWide, bool kPairs>
-__device__ __forceinline__ void turn_unit(const Turn& t, const float2* cs, int u, const T* from, T* to, T* also) {
-    if constexpr (kWide) {
-        constexpr int per = Wide<T>::kPer;
+struct Held;
+template <typename T, bool kPairs>
+struct Held<T, true, kPairs> {
+    static constexpr int per = Wide<T>::kPer;
+    uint4 a, b;
+    __device__ __forceinline__ void load(const Turn& t, int u, const T* from) {
         if (u < t.turning) {
-            if constexpr (kPairs) {
-                Wide<T> w;
-                w.load(from + u * per);
-#pragma unroll
-                for (int i = 0; i < per; i += 2) {
-                    const float2 y = turned(w.x[i], w.x[i + 1], cs[(u * per + i) / 2]);
-                    w.x[i] = y.x;
-                    w.x[i + 1] = y.y;
-                }
-                const uint4 y = w.pack();
-                *reinterpret_cast<uint4*>(to + u * per) = y;
-                if (also != nullptr) *reinterpret_cast<uint4*>(also + u * per) = y;
-            } else {
-                Wide<T> a, b;
-                a.load(from + u * per);
-                b.load(from + t.pairs + u * per);
-#pragma unroll
-                for (int i = 0; i < per; ++i) {
-                    const float2 y = turned(a.x[i], b.x[i], cs[u * per + i]);
-                    a.x[i] = y.x;
-                    b.x[i] = y.y;
-                }
-                const uint4 y = a.pack(), z = b.pack();
-                *reinterpret_cast<uint4*>(to + u * per) = y;
-                *reinterpret_cast<uint4*>(to + t.pairs + u * per) = z;
-                if (also != nullptr) {
-                    *reinterpret_cast<uint4*>(also + u * per) = y;
-                    *reinterpret_cast<uint4*>(also + t.pairs + u * per) = z;
-                }
-            }
+            a = *reinterpret_cast<const uint4*>(from + u * per);
+            if constexpr (!kPairs) b = *reinterpret_cast<const uint4*>(from + t.pairs + u * per);
         } else {
-            const int at = 2 * t.pairs + (u - t.turning) * per;
-            const uint4 y = *reinterpret_cast<const uint4*>(from + at);
-            *reinterpret_cast<uint4*>(to + at) = y;
-            if (also != nullptr) *reinterpret_cast<uint4*>(also + at) = y;
+            a = *reinterpret_cast<const uint4*>(from + 2 * t.pairs + (u - t.turning) * per);
         }
-    } else if (u < t.turning) {
+    }
+    __device__ __forceinline__ void load_copy(int u, const T* from) { a = *(reinterpret_cast<const uint4*>(from) + u); }
+    __device__ __forceinline__ void store_copy(int u, T* to) const { *(reinterpret_cast<uint4*>(to) + u) = a; }
+    // ... to one place or two (also == nullptr: one)
+    __device__ __forceinline__ void finish(const Turn& t, const float2* cs, int u, T* to, T* also) const {
+        int at = u * per;
+        uint4 y = a, z = b;
+        if (u >= t.turning) {
+            at = 2 * t.pairs + (u - t.turning) * per;
+        } else if constexpr (kPairs) {
+            float x[per];
+            Wide<T>::unpack(a, x);
+#pragma unroll
+            for (int i = 0; i < per; i += 2) {
+                const float2 w = turned(x[i], x[i + 1], cs[(at + i) / 2]);
+                x[i] = w.x;
+                x[i + 1] = w.y;
+            }
+            y = Wide<T>::pack(x);
+        } else {
+            float x[per], v[per];
+            Wide<T>::unpack(a, x);
+            Wide<T>::unpack(b, v);
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const float2 w = turned(x[i], v[i], cs[at + i]);
+                x[i] = w.x;
+                v[i] = w.y;
+            }
+            y = Wide<T>::pack(x);
+            z = Wide<T>::pack(v);
+            *reinterpret_cast<uint4*>(to + t.pairs + at) = z;
+            if (also != nullptr) *reinterpret_cast<uint4*>(also + t.pairs + at) = z;
+        }
+        *reinterpret_cast<uint4*>(to + at) = y;
+        if (also != nullptr) *reinterpret_cast<uint4*>(also + at) = y;
+    }
+};
+template <typename T, bool kPairs>
+struct Held<T, false, kPairs> {   // a pair, or an element that does not turn
+    T a, b;
+    __device__ __forceinline__ void load(const Turn& t, int u, const T* from) {
+        if (u < t.turning) {
+            a = from[kPairs ? 2 * u : u];
+            b = from[kPairs ? 2 * u + 1 : u + t.pairs];
+        } else {
+            a = from[t.pairs + u];
+        }
+    }
+    __device__ __forceinline__ void load_copy(int u, const T* from) { a = from[u]; }
+    __device__ __forceinline__ void store_copy(int u, T* to) const { to[u] = a; }
+    __device__ __forceinline__ void finish(const Turn& t, const float2* cs, int u, T* to, T* also) const {
+        if (u >= t.turning) {
+            to[t.pairs + u] = a;
+            if (also != nullptr) also[t.pairs + u] = a;
+            return;
+        }
         const int i = kPairs ? 2 * u : u, j = kPairs ? 2 * u + 1 : u + t.pairs;
-        const float2 y = turned(value(from[i]), value(from[j]), cs[u]);
+        const float2 y = turned(value(a), value(b), cs[u]);
         store(to + i, y.x);
         store(to + j, y.y);
         if (also != nullptr) {
             store(also + i, y.x);
             store(also + j, y.y);
         }
-    } else {
-        const int at = t.pairs + u;
-        const T y = from[at];
-        to[at] = y;
-        if (also != nullptr) also[at] = y;
     }
-}
+};
+
+// The units of a CTA's rows, row by row, kTurnThreads apart.
+struct Place {
+    int r, u;   // row, unit of the CTA's share of it
+    __device__ __forceinline__ Place(int tid, int n, int rows) : r(0), u(tid) { wrap(n, rows); }
+    __device__ __forceinline__ void wrap(int n, int rows) {
+        while (u >= n && r < rows) {
+            u -= n;
+            ++r;
+        }
+    }
+    __device__ __forceinline__ void next(int n, int rows) {
+        u += kTurnThreads;
+        wrap(n, rows);
+    }
+};
 
 // ---------------------------------------------------------------------------------------
 // rows at given positions
 // ---------------------------------------------------------------------------------------
 template <typename T, bool kWide, bool kPairs>
-__global__ void __launch_bounds__(kTurnThreads) rotate_kernel(const spec_rotate_args a, const Turn t, int rows_each, int units_each) {
+__global__ void __launch_bounds__(kTurnThreads, 6) rotate_kernel(const spec_rotate_args a, const Turn t, int rows_each, int units_each) {
     __shared__ float2 s_cs[kTurnRows][kTurnPairs];
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int rows = (int)min((int64_t)rows_each, a.rows - row0);
+    const int first = blockIdx.y * units_each, n = min(units_each, a.heads * t.units - first);
+    Held<T, kWide, kPairs> held = {};
+    auto load = [&](const Place& at) {
+        const int head = t.by_units.of(first + at.u);
+        held.load(t, first + at.u - head * t.units, reinterpret_cast<const T*>(a.x) + (row0 + at.r) * a.x_row_stride + head * t.D);
+    };
+    Place at(tid, n, rows);
+    if (at.r < rows) load(at);
     if (warp < rows) prepare_row(t, *(a.positions + row0 + warp), s_cs[warp]);
     __syncthreads();
-    const int first = blockIdx.y * units_each, n = min(units_each, a.heads * t.units - first);
-    for (int r = 0, u = tid;; u += kTurnThreads) {
-        while (u >= n && r < rows) {
-            u -= n;
-            ++r;
-        }
-        if (r >= rows) return;
-        const int head = t.by_units.of(first + u), c = first + u - head * t.units;
-        const T* from = reinterpret_cast<const T*>(a.x) + (row0 + r) * a.x_row_stride + head * t.D;
-        T* to = reinterpret_cast<T*>(a.out) + (row0 + r) * a.out_row_stride + head * t.D;
-        turn_unit<T, kWide, kPairs>(t, s_cs[r], c, from, to, (T*)nullptr);
+    while (at.r < rows) {
+        const Place now = at;
+        const Held<T, kWide, kPairs> mine = held;
+        at.next(n, rows);
+        if (at.r < rows) load(at);
+        const int head = t.by_units.of(first + now.u);
+        mine.finish(t, s_cs[now.r], first + now.u - head * t.units,
+                    reinterpret_cast<T*>(a.out) + (row0 + now.r) * a.out_row_stride + head * t.D, (T*)nullptr);
     }
 }
 
@@ -223,7 +264,7 @@ __device__ __forceinline__ int append_refusal(const spec_append_rotated_args& a,
 }
 
 template <typename T, bool kWide, bool kPairs>
-__global__ void __launch_bounds__(kTurnThreads) append_rotated_kernel(const spec_append_rotated_args a, const Turn t, int rows_each, int units_each) {
+__global__ void __launch_bounds__(kTurnThreads, 6) append_rotated_kernel(const spec_append_rotated_args a, const Turn t, int rows_each, int units_each) {
     __shared__ float2 s_cs[kTurnRows][kTurnPairs];
     __shared__ int s_stream[kTurnRows], s_page[kTurnRows], s_offset[kTurnRows];   // page -2: the row is left alone
     __shared__ int s_first;
@@ -236,6 +277,27 @@ __global__ void __launch_bounds__(kTurnThreads) append_rotated_kernel(const spec
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int rows = (int)max((int64_t)0, min((int64_t)rows_each, a.rows - row0));
     const bool reports = blockIdx.y == 0 && (int64_t)blockIdx.x * kTurnRows < a.B;   // this CTA writes statuses: it looks at all offsets
+    const int first = blockIdx.y * units_each, turn_q = a.Hq * t.units, turn = turn_q + a.Hkv * t.units;
+    const int n = min(units_each, turn + a.Hkv * t.copies - first);
+    Held<T, kWide, kPairs> held = {};
+    auto load = [&](const Place& at) {
+        const int64_t row = row0 + at.r;
+        int x = first + at.u;
+        if (x < turn_q) {
+            const int head = t.by_units.of(x);
+            held.load(t, x - head * t.units, reinterpret_cast<const T*>(a.q) + row * a.q_row_stride + head * t.D);
+        } else if (x < turn) {
+            x -= turn_q;
+            const int head = t.by_units.of(x);
+            held.load(t, x - head * t.units, reinterpret_cast<const T*>(a.k) + row * a.k_row_stride + head * t.D);
+        } else {
+            x -= turn;
+            const int head = t.by_copies.of(x);
+            held.load_copy(x - head * t.copies, reinterpret_cast<const T*>(a.v) + row * a.v_row_stride + head * t.D);
+        }
+    };
+    Place at(tid, n, rows);
+    if (at.r < rows) load(at);   // on its way while the rows' streams are found
     // a stream's rows lie behind those of the streams before it, so a thread whose stream begins past the CTA's rows is done
     for (int b = tid; b < a.B; b += kTurnThreads) {
         const int64_t at = stream_row(a, b), n = stream_rows(a, b);
@@ -267,39 +329,29 @@ __global__ void __launch_bounds__(kTurnThreads) append_rotated_kernel(const spec
         }
     }
     __syncthreads();
-    const int first = blockIdx.y * units_each, turn_q = a.Hq * t.units, turn = turn_q + a.Hkv * t.units;
-    const int n = min(units_each, turn + a.Hkv * t.copies - first);
-    for (int r = 0, u = tid;; u += kTurnThreads) {
-        while (u >= n && r < rows) {
-            u -= n;
-            ++r;
-        }
-        if (r >= rows) break;
-        const int page = s_page[r];
+    while (at.r < rows) {
+        const Place now = at;
+        const Held<T, kWide, kPairs> mine = held;
+        at.next(n, rows);
+        if (at.r < rows) load(at);
+        const int page = s_page[now.r];
         if (page == -2) continue;
-        const int64_t row = row0 + r;
-        int x = first + u;
+        const int64_t row = row0 + now.r;
+        int x = first + now.u;
         if (x < turn_q) {
             const int head = t.by_units.of(x);
-            turn_unit<T, kWide, kPairs>(t, s_cs[r], x - head * t.units, reinterpret_cast<const T*>(a.q) + row * a.q_row_stride + head * t.D,
-                                        reinterpret_cast<T*>(a.q_out) + row * a.q_out_row_stride + head * t.D, (T*)nullptr);
+            mine.finish(t, s_cs[now.r], x - head * t.units, reinterpret_cast<T*>(a.q_out) + row * a.q_out_row_stride + head * t.D, (T*)nullptr);
         } else if (x < turn) {
             x -= turn_q;
             const int head = t.by_units.of(x);
             T* kept = a.k_out == nullptr ? (T*)nullptr : reinterpret_cast<T*>(a.k_out) + row * a.k_out_row_stride + head * t.D;
-            T* to = page < 0 ? kept : reinterpret_cast<T*>(a.k_pages) + (((int64_t)page * a.Hkv + head) * a.page_size + s_offset[r]) * t.D;
-            if (to != nullptr)
-                turn_unit<T, kWide, kPairs>(t, s_cs[r], x - head * t.units, reinterpret_cast<const T*>(a.k) + row * a.k_row_stride + head * t.D, to,
-                                            page < 0 ? (T*)nullptr : kept);
+            T* to = page < 0 ? kept : reinterpret_cast<T*>(a.k_pages) + (((int64_t)page * a.Hkv + head) * a.page_size + s_offset[now.r]) * t.D;
+            if (to != nullptr) mine.finish(t, s_cs[now.r], x - head * t.units, to, page < 0 ? (T*)nullptr : kept);
         } else if (page >= 0) {
             x -= turn;
-            const int head = t.by_copies.of(x), c = x - head * t.copies;
-            const T* from = reinterpret_cast<const T*>(a.v) + row * a.v_row_stride + head * t.D;
-            T* to = reinterpret_cast<T*>(a.v_pages) + (((int64_t)page * a.Hkv + head) * a.page_size + s_offset[r]) * t.D;
-            if constexpr (kWide)
-                *(reinterpret_cast<uint4*>(to) + c) = *(reinterpret_cast<const uint4*>(from) + c);
-            else
-                to[c] = from[c];
+            const int head = t.by_copies.of(x);
+            mine.store_copy(x - head * t.copies,
+                            reinterpret_cast<T*>(a.v_pages) + (((int64_t)page * a.Hkv + head) * a.page_size + s_offset[now.r]) * t.D);
         }
     }
     if (!reports) return;
@@ -342,11 +394,14 @@ static Turn plan(int D, int dim, int interleaved, int dtype, float magnitude, co
     return t;
 }
 
-// Rows and units of a CTA.
+// Rows and units of a CTA: what fills the resident CTAs (six an SM) once, from one to eight units a thread, and in whole rows where a thread has
+// more than one: a row's sines, and an append's search for its stream, are every CTA's that has a part of it.  8,191 rows of 72 heads of 128 take 47.7 us with eight units, 52.0
+// with six and 55.2 with sixteen; 900 float32 rows of 48 heads appended 6.9 us a row a CTA and 10.2 in three parts.
 static void share(int64_t rows, int64_t per_row, int* rows_each, int* units_each, dim3* grid) {
-    const int64_t want = rows * per_row >= 152 * 16 * kTurnThreads ? 8 * kTurnThreads : kTurnThreads;
+    const int64_t fill = rows * per_row / (152 * 6);
+    const int64_t want = fill < kTurnThreads ? kTurnThreads : fill > 8 * kTurnThreads ? 8 * kTurnThreads : fill;
     const int64_t each = want / per_row < 1 ? 1 : want / per_row > kTurnRows ? kTurnRows : want / per_row;
-    const int64_t splits = each > 1 ? 1 : (per_row + want - 1) / want;
+    const int64_t splits = each > 1 ? 1 : want == kTurnThreads ? (per_row + want - 1) / want : per_row < 2 * want ? 1 : per_row / want;
     *rows_each = (int)each;
     *units_each = (int)((per_row + splits - 1) / splits);
     const int64_t x = (rows + each - 1) / each;
