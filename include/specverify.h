@@ -529,12 +529,13 @@ size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
  * window > 0 only those with j > i - window or j < sinks (as in spec_paged_attention, which carries on behind the prompt):
  *   out[i, h] = sum_j e_j v[j, g] / sum_j e_j,   e_j = exp(scale q[i, h] . k[j, g]),   g = h / (Hq / Hkv).
  * q [rows, Hq, D], k and v [rows, Hkv, D] with row strides in elements (slices of a wider projection), out [rows, Hq, D] dense, one dtype.
- * cu_rows [B + 1] int32 (NULL: B prompts of rows / B).  Rows behind the last prompt's are neither read nor written.
+ * cu_rows [B + 1] int32 (NULL: B prompts of rows / B).  out overlaps none of them.  Rows behind the last prompt's are not written, and what they hold
+ * does not matter.
  * status [B]: SPEC_ST_OK, or BAD_OFFSETS for the first prompt whose offsets are broken (cu_rows[0] not 0, a negative count, rows
- * beyond `rows`) and all behind it, whose rows are not written.  Rows that a bounded wait left unfinished are NaN.
- * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before they meet the values, and the same
- * rounded weights are summed.  A value that is not finite reaches the rows that see it and may reach earlier rows of its prompt, up to 255
- * tokens before it; it reaches no other prompt.  In float32 infinite queries, keys and values count as NaN.  Results are the same from run to run.
+ * beyond `rows`) and all behind it, whose rows are not written.  Where a bounded wait gives up rows are NaN.
+ * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before they meet the values, and the
+ * same rounded weights are summed.  A value that is not finite reaches the rows that see it, and may reach rows of its prompt up to 255 tokens
+ * before it, or behind the last that sees it; it reaches no other prompt.  In float32 infinite queries, keys and values count as NaN.  Results are the same from run to run.
  * Errors: SPEC_ERR_ARG (NULL pointer, scale or scale * log2(e) not finite, q, k, v, out or a row stride not a multiple of 16 bytes),
  * SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (B outside [0, SPEC_MAX_STREAMS], Hq not a multiple of Hkv or more than 128 times it, D not a
  * multiple of 8 up to SPEC_MAX_HEAD, in float32 up to 128, a row stride below heads * D, rows outside [0, 2^31), without cu_rows not a multiple of B, window or sinks

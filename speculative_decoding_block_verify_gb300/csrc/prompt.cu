@@ -10,7 +10,9 @@ namespace sv {
 __global__ void __launch_bounds__(32) no_rows_kernel(const PromptParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    prompt_statuses(p);
+    PromptWalk w;
+    w.start();
+    prompt_statuses(p, w);
 }
 
 }  // namespace sv

@@ -70,6 +70,7 @@ struct PromptWalk {
     unsigned total;      // pieces of the batch
     unsigned base;       // items of the batches before
     unsigned round;
+    int broken;          // the first prompt whose offsets are broken, as far as is known
     bool ended;          // no batch behind this one
 
     __device__ __forceinline__ unsigned above(int level) const {   // pieces of the batch with a number of `level` or more
@@ -90,7 +91,7 @@ struct PromptWalk {
                 if (prompt_broken(p, b, row0, end))
                     bad = min(bad, b);
                 else
-                    pieces[i] = (unsigned)(end - row0 + p.piece - 1) / (unsigned)p.piece;
+                    pieces[i] = (int)(((unsigned)(end - row0) + p.piece - 1) / (unsigned)p.piece);
             }
         }
         bad = __reduce_min_sync(0xffffffffu, bad);
@@ -98,11 +99,13 @@ struct PromptWalk {
         for (int i = 0; i < kEach; ++i)
             if (first + 32 * i + lane >= bad) pieces[i] = 0;
         total = above(0);
+        broken = bad;
         ended = bad != INT32_MAX || first + kBatch >= p.a.B;
     }
     __device__ __forceinline__ void start() {
         base = total = round = 0;
         first = -kBatch;
+        broken = INT32_MAX;
         ended = false;
     }
     // The next item; false: there are no more.
@@ -154,18 +157,16 @@ struct PromptWalk {
     }
 };
 
-// The statuses, by one warp of every CTA: CTA c has those of batches c, c + gridDim.x, .. of 32 prompts.
-__device__ __forceinline__ void prompt_statuses(const PromptParams& p) {
+// The statuses, by the warp of every CTA that walked: CTA c has those of batches c, c + gridDim.x, .. of 32 prompts.
+__device__ __forceinline__ void prompt_statuses(const PromptParams& p, PromptWalk& w) {
     const int lane = threadIdx.x & 31;
     if ((int64_t)blockIdx.x * 32 >= p.a.B) return;
-    int bad = INT32_MAX;
-    for (int b0 = 0; b0 < p.a.B && bad == INT32_MAX; b0 += 32) {
-        const int b = b0 + lane;
-        if (b < p.a.B && prompt_broken(p, b, prompt_row(p, b), prompt_row(p, b + 1))) bad = b;
-        bad = __reduce_min_sync(0xffffffffu, bad);
+    while (!w.ended) {   // (a walk that was broken off, or had no item)
+        w.first += PromptWalk::kBatch;
+        w.load(p);
     }
     for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.a.B; b += (int64_t)gridDim.x * 32)
-        p.a.status[b] = b < bad ? SPEC_ST_OK : SPEC_ST_BAD_OFFSETS;
+        p.a.status[b] = b < w.broken ? SPEC_ST_OK : SPEC_ST_BAD_OFFSETS;
 }
 
 // A wait of this CTA gave up: one warp leaves NaN in the rows of all its items.

@@ -11,13 +11,12 @@ namespace sv {
 // ---- warp 15: the walk over the CTA's items, and the copies --------------------------------
 template <int DP>
 __device__ __forceinline__ void prompt_f32_copy_role(const PromptParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, char* raw,
-                                                     F32Shared& sh) {
+                                                     F32Shared& sh, PromptWalk& w) {
     using Lay = F32Layout<DP>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(raw);
     const unsigned bytes = kTile * p.a.D * 4;
     const uint64_t stay = l2_evict_normal_policy();
-    PromptWalk w;
     Piece it = {};
     Keys keys = {};
     int told = 0, slot = 0;
@@ -91,8 +90,9 @@ __global__ void __launch_bounds__(kF32Threads, 1) prompt_f32_kernel(const Prompt
     if (warp >= 12) {
         registers_down<kRegsRest>();
         if (warp == 15) {
-            prompt_f32_copy_role<DP>(pp, &kmap, &vmap, raw, sh);
-            prompt_statuses(pp);
+            PromptWalk w;
+            prompt_f32_copy_role<DP>(pp, &kmap, &vmap, raw, sh, w);
+            prompt_statuses(pp, w);
         } else if (warp == 14) {
             if (!f32_keys_role<DP>(p, planes, sh)) drain(&sh.drain[0]);
         } else if (warp == 13) {

@@ -72,10 +72,9 @@ struct PromptShared {
 
 // ---- warp 11: the walk over the CTA's items ------------------------------------------------------
 template <int DP, bool kWindow>
-__device__ __forceinline__ void prompt_walk_role(const PromptParams& p, PromptShared& sh) {
+__device__ __forceinline__ void prompt_walk_role(const PromptParams& p, PromptShared& sh, PromptWalk& w) {
     using Lay = PromptLayout<DP>;
     const int lane = threadIdx.x & 31;
-    PromptWalk w;
     Piece it = {};
     w.start();
     for (int told = 0;; ++told) {
@@ -618,8 +617,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
         } else if (warp == 10) {
             prompt_queries_role<DP>(p, &qmap, smem, sh);
         } else {
-            prompt_walk_role<DP, kWindow>(p, sh);
-            prompt_statuses(p);   // while the last tiles are computed
+            PromptWalk w;
+            prompt_walk_role<DP, kWindow>(p, sh, w);
+            prompt_statuses(p, w);   // while the last tiles are computed
         }
     } else {
         if (Lay::kGroups == 2) registers_up<kRegsRows>();

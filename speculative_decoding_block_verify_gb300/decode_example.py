@@ -9,6 +9,8 @@ written into).  Each step then
      (spec_cache_append) and the block attends over the whole context (spec_paged_attention),
   3. verifies the block (spec_verify_block), and
   4. keeps the emitted tokens' pages and reserves room for the next block (spec_cache_resize).
+With ``--rotary`` the target has rotary positions instead of learned ones: every step's append turns keys and queries on the way
+(spec_cache_append_rotated), and the prompt goes through in one piece (the same call, and spec_prompt_attention over its packed rows).
 Nothing is read back to the host inside a step: what a call reports for a stream goes into the next one on the device.  A
 stream that finds no page in step 4 is passed over by the next step's append, keeps nothing of that step and asks again.  The target is a small random transformer whose projections
 are plain torch products: it stands for a user's model.
@@ -24,11 +26,12 @@ class Target:
     low-rank table of the token before (the part that the drafter knows, and most of them)."""
 
     def __init__(self, torch, V=512, width=256, layers=2, q_heads=8, kv_heads=2, head=64, positions=4096, seed=0,
-                 dtype=None, device="cuda"):
+                 dtype=None, device="cuda", rotary=False):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.dtype = torch.float32 if dtype is None else dtype
         r = lambda *s: torch.randn(s, generator=g, device=device)  # noqa: E731
+        self.rotary = sv.RotaryTable(head, device=device) if rotary else None
         self.V, self.layers, self.q_heads, self.kv_heads, self.head = V, layers, q_heads, kv_heads, head
         self.embedding = r(V, width).to(self.dtype)
         self.position = (0.3 * r(positions, width)).to(self.dtype)
@@ -76,10 +79,22 @@ def first_of(torch, *statuses):
 def forward(torch, target, cache, tokens, cu, kmax, state):
     """Logits [rows, V] of the packed block rows ``tokens``; their keys and values are appended.  ``state["status"]`` is
     what the block's calls report for each stream, that of the resize before them included."""
-    if cache.table.shape[1] * cache.page > target.position.shape[0]:
+    if target.rotary is None and cache.table.shape[1] * cache.page > target.position.shape[0]:
         raise ValueError(f"the cache has room for {cache.table.shape[1] * cache.page} tokens a stream, the model for "
                          f"{target.position.shape[0]}")
     rows = tokens.numel()
+    if target.rotary is not None:
+        def block(i, qkv):
+            H, G = target.q_heads, target.kv_heads
+            turn = ("append", rows)
+            state[turn] = a = sv.spec_cache_append_rotated(
+                qkv[:, :H], qkv[:, H:H + G], qkv[:, H + G:], cache.k[i], cache.v[i], cache.table, cache.length, target.rotary, cu_drafts=cu,
+                kmax=kmax, reserved=cache.reserved, out=state.get(turn))
+            key = ("attention", rows, kmax)
+            state[key] = o = sv.spec_paged_attention(a["q"], cache.k[i], cache.v[i], cache.table, cache.length, cu, kmax, target.head ** -0.5,
+                                                     out=state.get(key))
+            return o["out"], a["status"], o["status"]
+        return layers(torch, target, tokens, target.embedding[tokens.long()], cache.reserved, block, state)
     stream = torch.searchsorted(cu + torch.arange(cu.numel(), device=cu.device), torch.arange(rows, device=cu.device), right=True) - 1
     at = cache.length[stream] + torch.arange(rows, device=cu.device) - cu[stream] - stream
     # a block that does not fit its stream's table row is refused by the calls below, and its rows stand for nothing
@@ -100,6 +115,39 @@ def forward(torch, target, cache, tokens, cu, kmax, state):
     state["status"] = status
     W1, W2 = target.table
     return (x @ target.logits).float() + W1[tokens.long()] @ W2
+
+
+def layers(torch, target, tokens, x, status, attend, state):
+    """Logits of the rows ``x``; ``attend(layer, projections)`` returns the layer's attention and what its calls report."""
+    rows, H, G, D = tokens.numel(), target.q_heads, target.kv_heads, target.head
+    for i in range(target.layers):
+        out, *seen = attend(i, (x @ target.qkv[i]).view(rows, H + 2 * G, D))
+        status = first_of(torch, status, *seen)
+        x = x + out.view(rows, H * D) @ target.o[i]
+        x = x * torch.rsqrt((x.float() ** 2).mean(dim=1, keepdim=True)).to(x.dtype)
+    state["status"] = status
+    W1, W2 = target.table
+    return (x @ target.logits).float() + W1[tokens.long()] @ W2
+
+
+def prefill_whole(torch, target, cache, tokens, counts, state):
+    """Whole prompts into a cache that holds none of their streams yet: ``tokens`` [rows] packed, counts[b] of them for stream b (0 for
+    one that takes no part).  Returns the logits [rows, V]; ``state["status"]`` [B] is what the calls report."""
+    H, G, dev = target.q_heads, target.kv_heads, tokens.device
+    counts = torch.as_tensor(counts, dtype=torch.int32, device=dev)
+    cu = torch.zeros(counts.numel() + 1, dtype=torch.int32, device=dev)
+    cu[1:] = torch.cumsum(counts, 0)
+    reserved = cache.resize(room=counts)
+
+    def whole(i, qkv):
+        a = sv.spec_cache_append_rotated(qkv[:, :H], qkv[:, H:H + G], qkv[:, H + G:], cache.k[i], cache.v[i], cache.table, cache.length,
+                                         target.rotary, cu_rows=cu, keep_keys=True, reserved=reserved)
+        o = sv.spec_prompt_attention(a["q"], a["k"], qkv[:, H + G:], cu, target.head ** -0.5)
+        return o["out"], a["status"], o["status"]
+
+    logits = layers(torch, target, tokens, target.embedding[tokens.long()], reserved, whole, state)
+    cache.resize(advance=torch.where(state["status"] == 0, counts, 0))
+    return logits
 
 
 def prefill(torch, target, cache, prompt, state, kmax=sv.MAX_DRAFTS):
@@ -184,14 +232,20 @@ def main():
     ap.add_argument("--drafts", type=int, default=5)
     ap.add_argument("--prompt", type=int, default=100)
     ap.add_argument("--temperature", type=float, default=0.8)
+    ap.add_argument("--rotary", action="store_true", help="rotary positions, and the prompt in one piece")
     a = ap.parse_args()
     tokens = a.prompt + (a.steps + 1) * (a.drafts + 1)
-    target = Target(torch, positions=-(-tokens // 16) * 16)
+    target = Target(torch, positions=-(-tokens // 16) * 16, rotary=a.rotary)
     cache = Cache(torch, target, a.streams, tokens)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     prompt = torch.randint(0, target.V, (a.prompt,), generator=g, device="cuda", dtype=torch.int32)
-    seen = [prefill(torch, target, cache, prompt, {})]
+    if a.rotary:
+        state = {}
+        prefill_whole(torch, target, cache, prompt[:-1], [a.prompt - 1] + [0] * (a.streams - 1), state)
+        seen = [state["status"]]
+    else:
+        seen = [prefill(torch, target, cache, prompt, {})]
     if a.streams > 1:
         others = torch.arange(1, a.streams, dtype=torch.int32, device="cuda")
         seen.append(cache.fork(torch.zeros_like(others), others))
