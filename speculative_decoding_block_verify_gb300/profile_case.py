@@ -101,12 +101,14 @@ def main(argv=None):
                 pl.launch()
             torch.cuda.synchronize()
             pl.close()
-    elif a.case.startswith("cache_"):
-        spec = importlib.util.spec_from_file_location("operators", Path(__file__).parents[1] / "perf" / "operators.py")
+    elif a.case.startswith(("cache_", "path_")):
+        kind, name = a.case.split("_", 1)
+        file = {"cache": "operators.py", "path": "more_operators.py"}[kind]
+        spec = importlib.util.spec_from_file_location("operators", Path(__file__).parents[1] / "perf" / file)
         operators = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(operators)
         operators.own = True
-        case = [c for c in operators.listed() if c["name"] == a.case[len("cache_"):]]
+        case = [c for c in operators.listed() if c["name"] == name]
         if not case:
             print(f"unknown case {a.case}", file=sys.stderr)
             return 2
