@@ -23,14 +23,18 @@ constexpr int kTurnThreads = 256;
 constexpr int kTurnRows = kTurnThreads / 32;       // rows of a CTA: a warp prepares one
 // A row's sines and cosines in shared memory, one place free behind every eight: threads of neighbouring units read eight (or four) of them each, which
 // without that are in the same banks (24 prompts appended 93.5 us against 97.2, 64 blocks 4.5 against 5.2; rows alone as before).
-constexpr int kTurnPairs = SPEC_MAX_HEAD / 2 / 8 * 9;
+constexpr int kTurnPairs = (SPEC_MAX_HEAD / 2 + 8) / 8 * 9;   // (a ragged unit reads up to seven past the last)
 __device__ __forceinline__ int place(int j) { return j + (j >> 3); }
 
-// How a head is cut: units of 16 bytes (halves: 16 bytes of either half), or of one pair or element.
+// How a head is cut.  kWide: units of 16 bytes (halves: 16 bytes of either half).  kRagged: the same where what turns does not end on, or a half
+// does not begin on, a 16-byte boundary; the second half and the rest of the head then move in pieces of what alignment they have.  kScalar: units
+// of one pair or element, for rows that are not on 16-byte boundaries.
+enum { kScalar, kWide, kRagged };
 struct Turn {
     const uint64_t* turns;
     int D, pairs;
     int turning;        // units of a head that turn; the others are copied
+    int half_align, rest_align;   // kRagged: bytes to whose multiples the second half and the rest of a head lie
     int units, copies;  // units of a head that turns, and of one that is copied as it is (values)
     Divisor by_units, by_copies;
     float magnitude;
@@ -99,10 +103,10 @@ __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 
 // A unit of a head, as it was read.  The next one is read before this one is turned and written (what is written may be the place that
 // was read, but a unit is one thread's alone), and the first one before the row's sines are there.
-template <typename T, bool kWide, bool kPairs>
+template <typename T, int kMode, bool kPairs>
 struct Held;
 template <typename T, bool kPairs>
-struct Held<T, true, kPairs> {
+struct Held<T, kWide, kPairs> {
     static constexpr int per = Wide<T>::kPer;
     uint4 a, b;
     __device__ __forceinline__ void load(const Turn& t, int u, const T* from) {
@@ -153,7 +157,7 @@ struct Held<T, true, kPairs> {
     }
 };
 template <typename T, bool kPairs>
-struct Held<T, false, kPairs> {   // a pair, or an element that does not turn
+struct Held<T, kScalar, kPairs> {   // a pair, or an element that does not turn
     T a, b;
     __device__ __forceinline__ void load(const Turn& t, int u, const T* from) {
         if (u < t.turning) {
@@ -182,6 +186,128 @@ struct Held<T, false, kPairs> {   // a pair, or an element that does not turn
     }
 };
 
+// n elements (16 bytes, or fewer at the end of a part) of a place that lies on a multiple of `align` bytes.
+__device__ __forceinline__ uint4 fetch(const unsigned short* p, int n, int align) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (n == 8 && align == 16) return *reinterpret_cast<const uint4*>(p);
+    if (n == 8 && align >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else if (n == 8) {   // the words from the element before on (it is the head's too), and the last element
+        uint32_t x[5];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = reinterpret_cast<const uint32_t*>(p - 1)[i];
+        x[4] = p[7];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) w[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 fetch(const float* p, int n, int align) {
+    if (n == 4 && align == 16) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put(unsigned short* p, uint4 x, int n, int align) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (n == 8 && align == 16) {
+        *reinterpret_cast<uint4*>(p) = x;
+    } else if (n == 8 && align >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    } else if (n == 8) {
+        p[0] = (unsigned short)w[0];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(p + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        p[7] = (unsigned short)(w[3] >> 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = (unsigned short)(w[i / 2] >> (i % 2 * 16));
+    }
+}
+__device__ __forceinline__ void put(float* p, uint4 x, int n, int align) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (n == 4 && align == 16) {
+        *reinterpret_cast<uint4*>(p) = x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    }
+}
+template <typename T, bool kPairs>
+struct Held<T, kRagged, kPairs> {
+    static constexpr int per = Wide<T>::kPer;
+    uint4 a, b;
+    // where unit u lies (halves: its first element of the first half), its elements there, and whether it turns
+    __device__ __forceinline__ static bool span(const Turn& t, int u, int* at, int* n) {
+        if (kPairs) {
+            *at = u * per;
+            *n = per;
+            return u < t.turning;
+        }
+        const bool turns = u < t.turning;
+        const int first = turns ? 0 : 2 * t.pairs, end = turns ? t.pairs : t.D;
+        *at = first + (turns ? u : u - t.turning) * per;
+        *n = min(per, end - *at);
+        return turns;
+    }
+    __device__ __forceinline__ void load(const Turn& t, int u, const T* from) {
+        int at, n;
+        const bool turns = span(t, u, &at, &n);
+        a = fetch(from + at, n, kPairs || turns ? 16 : t.rest_align);
+        if (!kPairs && turns) b = fetch(from + t.pairs + at, n, t.half_align);
+    }
+    __device__ __forceinline__ void load_copy(int u, const T* from) { a = *(reinterpret_cast<const uint4*>(from) + u); }
+    __device__ __forceinline__ void store_copy(int u, T* to) const { *(reinterpret_cast<uint4*>(to) + u) = a; }
+    __device__ __forceinline__ void finish(const Turn& t, const float2* cs, int u, T* to, T* also) const {
+        int at, n;
+        const bool turns = span(t, u, &at, &n);
+        uint4 y = a;
+        if (turns) {
+            float x[per], v[per];
+            Wide<T>::unpack(a, x);
+            if constexpr (kPairs) {
+#pragma unroll
+                for (int i = 0; i < per; i += 2) {
+                    const float2 w = turned(x[i], x[i + 1], cs[place(at / 2) + i / 2]);
+                    x[i] = w.x;
+                    x[i + 1] = w.y;
+                }
+            } else {
+                Wide<T>::unpack(b, v);
+#pragma unroll
+                for (int i = 0; i < per; ++i) {
+                    const float2 w = turned(x[i], v[i], cs[place(at) + i]);
+                    x[i] = w.x;
+                    v[i] = w.y;
+                }
+                const uint4 z = Wide<T>::pack(v);
+                put(to + t.pairs + at, z, n, t.half_align);
+                if (also != nullptr) put(also + t.pairs + at, z, n, t.half_align);
+            }
+            y = Wide<T>::pack(x);
+            if constexpr (kPairs) {   // the unit's pairs behind the last that turns stay as they are
+                const int left = (t.pairs - at / 2) * 2 * (int)sizeof(T) / 4;
+                y.y = left > 1 ? y.y : a.y;
+                y.z = left > 2 ? y.z : a.z;
+                y.w = left > 3 ? y.w : a.w;
+            }
+        }
+        const int align = kPairs || turns ? 16 : t.rest_align;
+        put(to + at, y, n, align);
+        if (also != nullptr) put(also + at, y, n, align);
+    }
+};
+
 // The units of a CTA's rows, row by row, kTurnThreads apart.
 struct Place {
     int r, u;   // row, unit of the CTA's share of it
@@ -201,7 +327,7 @@ struct Place {
 // ---------------------------------------------------------------------------------------
 // rows at given positions
 // ---------------------------------------------------------------------------------------
-template <typename T, bool kWide, bool kPairs>
+template <typename T, int kMode, bool kPairs>
 __global__ void __launch_bounds__(kTurnThreads, 6) rotate_kernel(const spec_rotate_args a, const Turn t, int rows_each, int units_each) {
     __shared__ float2 s_cs[kTurnRows][kTurnPairs];
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -210,7 +336,7 @@ __global__ void __launch_bounds__(kTurnThreads, 6) rotate_kernel(const spec_rota
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int rows = (int)min((int64_t)rows_each, a.rows - row0);
     const int first = blockIdx.y * units_each, n = min(units_each, a.heads * t.units - first);
-    Held<T, kWide, kPairs> held = {};
+    Held<T, kMode, kPairs> held = {};
     auto load = [&](const Place& at) {
         const int head = t.by_units.of(first + at.u);
         held.load(t, first + at.u - head * t.units, reinterpret_cast<const T*>(a.x) + (row0 + at.r) * a.x_row_stride + head * t.D);
@@ -221,7 +347,7 @@ __global__ void __launch_bounds__(kTurnThreads, 6) rotate_kernel(const spec_rota
     __syncthreads();
     while (at.r < rows) {
         const Place now = at;
-        const Held<T, kWide, kPairs> mine = held;
+        const Held<T, kMode, kPairs> mine = held;
         at.next(n, rows);
         if (at.r < rows) load(at);
         const int head = t.by_units.of(first + now.u);
@@ -269,7 +395,7 @@ __device__ __forceinline__ int append_refusal(const spec_append_rotated_args& a,
     return SPEC_ST_OK;
 }
 
-template <typename T, bool kWide, bool kPairs>
+template <typename T, int kMode, bool kPairs>
 __global__ void __launch_bounds__(kTurnThreads, 6) append_rotated_kernel(const spec_append_rotated_args a, const Turn t, int rows_each, int units_each) {
     __shared__ float2 s_cs[kTurnRows][kTurnPairs];
     __shared__ int s_stream[kTurnRows], s_page[kTurnRows], s_offset[kTurnRows];   // page -2: the row is left alone
@@ -285,7 +411,7 @@ __global__ void __launch_bounds__(kTurnThreads, 6) append_rotated_kernel(const s
     const bool reports = blockIdx.y == 0 && (int64_t)blockIdx.x * kTurnRows < a.B;   // this CTA writes statuses: it looks at all offsets
     const int first = blockIdx.y * units_each, turn_q = a.Hq * t.units, turn = turn_q + a.Hkv * t.units;
     const int n = min(units_each, turn + a.Hkv * t.copies - first);
-    Held<T, kWide, kPairs> held = {};
+    Held<T, kMode, kPairs> held = {};
     auto load = [&](const Place& at) {
         const int64_t row = row0 + at.r;
         int x = first + at.u;
@@ -337,7 +463,7 @@ __global__ void __launch_bounds__(kTurnThreads, 6) append_rotated_kernel(const s
     __syncthreads();
     while (at.r < rows) {
         const Place now = at;
-        const Held<T, kWide, kPairs> mine = held;
+        const Held<T, kMode, kPairs> mine = held;
         at.next(n, rows);
         if (at.r < rows) load(at);
         const int page = s_page[now.r];
@@ -383,18 +509,22 @@ __global__ void __launch_bounds__(kTurnThreads, 6) append_rotated_kernel(const s
 // ---------------------------------------------------------------------------------------
 static int element(int dtype) { return dtype == SPEC_DTYPE_F32 ? 4 : 2; }
 
-// `wide`: every pointer and stride lets 16 bytes be moved at a time.
-static Turn plan(int D, int dim, int interleaved, int dtype, float magnitude, const uint64_t* turns, bool* wide) {
-    const int per = 16 / element(dtype);
+// `even`: every pointer and row stride is a multiple of 16 bytes.  Whole 16-byte units are what most heads are.  Of 4,000 rows of 40 heads of 128 in bf16
+// the ragged form takes 18.7 us with 122 elements turned in pairs and 38.3 with halves of 33; one pair a thread takes 40.6 and 52.3.
+static Turn plan(int D, int dim, int interleaved, int dtype, float magnitude, const uint64_t* turns, bool even, int* mode) {
+    const int es = element(dtype), per = 16 / es, pairs = dim / 2, turning = interleaved ? dim : pairs;
     Turn t = {};
-    *wide = *wide && (interleaved ? dim : dim / 2) % per == 0;
+    *mode = !even ? kScalar : turning % per == 0 ? kWide : kRagged;
     t.turns = turns;
     t.D = D;
-    t.pairs = dim / 2;
+    t.pairs = pairs;
     t.magnitude = magnitude;
-    t.turning = *wide ? (interleaved ? dim / per : dim / 2 / per) : dim / 2;
-    t.units = t.turning + (*wide ? (D - dim) / per : D - dim);
-    t.copies = *wide ? D / per : D;
+    auto align = [&](int elements) { return (elements * es) % 16 == 0 ? 16 : (elements * es) & -(elements * es); };
+    t.half_align = align(pairs);
+    t.rest_align = align(dim);
+    t.turning = *mode == kScalar ? pairs : (turning + per - 1) / per;
+    t.units = *mode == kScalar ? pairs + D - dim : interleaved ? D / per : t.turning + (D - dim + per - 1) / per;
+    t.copies = *mode == kScalar ? D : D / per;
     t.by_units = divisor(t.units);
     t.by_copies = divisor(t.copies);
     return t;
@@ -423,18 +553,20 @@ static int check_turn(const char* who, int dtype, int D, int dim, float magnitud
     return SPEC_OK;
 }
 
-template <typename T, typename A, template <typename, bool, bool> class K>
-static cudaError_t pick(const A& a, const Turn& t, bool wide, bool pairs, int rows_each, int units_each, dim3 grid, cudaStream_t s) {
-    auto* f = wide ? (pairs ? K<T, true, true>::kernel : K<T, true, false>::kernel) : pairs ? K<T, false, true>::kernel : K<T, false, false>::kernel;
+template <typename T, typename A, template <typename, int, bool> class K>
+static cudaError_t pick(const A& a, const Turn& t, int mode, bool pairs, int rows_each, int units_each, dim3 grid, cudaStream_t s) {
+    auto* f = mode == kWide     ? (pairs ? K<T, kWide, true>::kernel : K<T, kWide, false>::kernel)
+              : mode == kRagged ? (pairs ? K<T, kRagged, true>::kernel : K<T, kRagged, false>::kernel)
+                                : (pairs ? K<T, kScalar, true>::kernel : K<T, kScalar, false>::kernel);
     return launch_after(f, grid, dim3(kTurnThreads), 0, s, a, t, rows_each, units_each);
 }
-template <typename T, bool kWide, bool kPairs>
+template <typename T, int kMode, bool kPairs>
 struct Rotates {
-    static constexpr auto kernel = rotate_kernel<T, kWide, kPairs>;
+    static constexpr auto kernel = rotate_kernel<T, kMode, kPairs>;
 };
-template <typename T, bool kWide, bool kPairs>
+template <typename T, int kMode, bool kPairs>
 struct Appends {
-    static constexpr auto kernel = append_rotated_kernel<T, kWide, kPairs>;
+    static constexpr auto kernel = append_rotated_kernel<T, kMode, kPairs>;
 };
 
 }  // namespace sv
@@ -500,14 +632,15 @@ extern "C" int spec_rotate(const spec_rotate_args* a, void* stream) {
     if (a->turns == nullptr || a->positions == nullptr || a->x == nullptr || a->out == nullptr)
         return set_error(SPEC_ERR_ARG, "spec_rotate: a required pointer is NULL");
     const int es = element(a->dtype);
-    bool wide = (((uintptr_t)a->x | (uintptr_t)a->out | (uintptr_t)(a->x_row_stride * es) | (uintptr_t)(a->out_row_stride * es)) & 15) == 0;
-    const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, &wide);
+    const bool even = (((uintptr_t)a->x | (uintptr_t)a->out | (uintptr_t)(a->x_row_stride * es) | (uintptr_t)(a->out_row_stride * es)) & 15) == 0;
+    int mode;
+    const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, even, &mode);
     int rows_each, units_each;
     dim3 grid;
     share(a->rows, (int64_t)a->heads * t.units, &rows_each, &units_each, &grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = es == 4 ? pick<float, spec_rotate_args, Rotates>(*a, t, wide, a->interleaved != 0, rows_each, units_each, grid, s)
-                                  : pick<unsigned short, spec_rotate_args, Rotates>(*a, t, wide, a->interleaved != 0, rows_each, units_each, grid, s);
+    const cudaError_t e = es == 4 ? pick<float, spec_rotate_args, Rotates>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s)
+                                  : pick<unsigned short, spec_rotate_args, Rotates>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_rotate");
 }
 
@@ -541,14 +674,14 @@ extern "C" int spec_cache_append_rotated(const spec_append_rotated_args* a, void
     uintptr_t low = (uintptr_t)a->k | (uintptr_t)a->v | (uintptr_t)(a->k_row_stride * es) | (uintptr_t)(a->v_row_stride * es);
     if (a->Hq > 0) low |= (uintptr_t)a->q | (uintptr_t)a->q_out | (uintptr_t)(a->q_row_stride * es) | (uintptr_t)(a->q_out_row_stride * es);
     if (a->k_out != nullptr) low |= (uintptr_t)a->k_out | (uintptr_t)(a->k_out_row_stride * es);
-    bool wide = (low & 15) == 0;
-    const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, &wide);
+    int mode;
+    const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, (low & 15) == 0, &mode);
     int rows_each, units_each;
     dim3 grid;
     share(a->rows, (int64_t)(a->Hq + a->Hkv) * t.units + (int64_t)a->Hkv * t.copies, &rows_each, &units_each, &grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = es == 4
-                              ? pick<float, spec_append_rotated_args, Appends>(*a, t, wide, a->interleaved != 0, rows_each, units_each, grid, s)
-                              : pick<unsigned short, spec_append_rotated_args, Appends>(*a, t, wide, a->interleaved != 0, rows_each, units_each, grid, s);
+                              ? pick<float, spec_append_rotated_args, Appends>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s)
+                              : pick<unsigned short, spec_append_rotated_args, Appends>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, who);
 }
