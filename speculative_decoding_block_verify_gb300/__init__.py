@@ -692,18 +692,13 @@ def _packed(t, name, device, dtype, heads, D):
     raise ValueError(f"{name} must have dense rows of heads * D elements")
 
 
-def _rows_of(t, name, device, dtype, heads, D):
-    """(pointer, row stride) of such a tensor."""
-    return _packed(t, name, device, dtype, heads, D)[:2]
-
-
 def _rows_into(t, name, device, dtype, rows, heads, D):
     """(pointer, row stride) of an output [rows, heads, D] with dense rows."""
     if t.is_contiguous() and t.dtype is dtype and t.get_device() == device and t.shape == (rows, heads, D):
         return t.data_ptr(), heads * D
     if len(t.shape) == 3 and t.shape[0] != rows:
         raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
-    return _rows_of(t, name, device, dtype, heads, D)
+    return _packed(t, name, device, dtype, heads, D)[:2]
 
 
 def _layer_of(k_pages, v_pages):
@@ -770,7 +765,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, length, cu_drafts, kma
     if len(shape) != 3 or shape[1] % Hkv != 0:
         raise ValueError("q must be [rows, Hq, D] with Hq a multiple of Hkv")
     rows, Hq, _ = shape
-    qp, stride = _rows_of(q, "q", device, k_pages.dtype, Hq, D)
+    qp, stride, _ = _packed(q, "q", device, k_pages.dtype, Hq, D)
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     L = _lib or lib()
     if out is None:
@@ -801,10 +796,9 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, length, cu_drafts, kma
     torch = _T or _cache_torch()
     device, code, kp, vp, (num_pages, Hkv, page_size, D) = _layer_of(k_pages, v_pages)
     dtype = k_pages.dtype
-    nk, ks = _rows_of(k, "k", device, dtype, Hkv, D)
-    nv, vs = _rows_of(v, "v", device, dtype, Hkv, D)
-    rows = k.shape[0]
-    if v.shape[0] != rows:
+    nk, ks, rows = _packed(k, "k", device, dtype, Hkv, D)
+    nv, vs, v_rows = _packed(v, "v", device, dtype, Hkv, D)
+    if v_rows != rows:
         raise ValueError("k and v must have the same rows")
     B, max_pages, cu, lp, tp = _blocks_of(device, page_table, length, cu_drafts, rows, kmax)
     if out is None:
@@ -908,7 +902,7 @@ def spec_prompt_attention(q, k, v, cu_rows, scale, window=0, sinks=0, out=None, 
         raise ValueError("q must be [rows, Hq, D] and k [rows, Hkv, D]")
     rows, Hq, D = shape
     Hkv = k.size(1)
-    qp, qs = _rows_of(q, "q", device, dtype, Hq, D)
+    qp, qs, _ = _packed(q, "q", device, dtype, Hq, D)
     kp, ks, k_rows = _packed(k, "k", device, dtype, Hkv, D)
     vp, vs, v_rows = _packed(v, "v", device, dtype, Hkv, D)
     if k_rows != rows or v_rows != rows:
@@ -986,7 +980,7 @@ def spec_rotate(x, positions, rotary, out=None, stream=None):
     if len(shape) != 3:
         raise ValueError("x must be [rows, heads, D]")
     rows, heads, D = shape
-    xp, xs = _rows_of(x, "x", device, dtype, heads, D)
+    xp, xs, _ = _packed(x, "x", device, dtype, heads, D)
     if out is None:
         with _made_on(stream):
             out = torch.empty(shape, dtype=dtype, device=x.device)
