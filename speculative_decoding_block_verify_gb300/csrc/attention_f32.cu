@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) attention_f32_kernel(const Att
     char* const raw = smem + 2 * kPlanes * Lay::kPlane;
     F32Shared& sh = *reinterpret_cast<F32Shared*>(smem + Lay::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
-    f32_begin<DP>(sh);
+    f32_begin<DP>(sh, 22);   // softmax 4, keys 8, values 8, products 2
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join, which waits for the whole grid
     if (tid == 0) p.desc[cta].rows = 0;

@@ -440,9 +440,9 @@ __device__ __forceinline__ void f32_softmax_role(const AttnParams& p, F32Shared&
     }
 }
 
-// Tensor memory and barriers, before the CTA's first __syncthreads.
+// Tensor memory and barriers, before the CTA's first __syncthreads.  `listeners`: warps that a segment is told.
 template <int DP>
-__device__ __forceinline__ void f32_begin(F32Shared& sh) {
+__device__ __forceinline__ void f32_begin(F32Shared& sh, int listeners) {
     using Lay = F32Layout<DP>;
     const int tid = threadIdx.x, warp = tid >> 5;
     if (warp == 13) {
@@ -463,7 +463,7 @@ __device__ __forceinline__ void f32_begin(F32Shared& sh) {
         for (int i = 0; i < 6; ++i) mbar_init(one[i], 1);
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 22);   // softmax 4, keys 8, values 8, products 2
+            mbar_init(&sh.seg_empty[i], listeners);
         }
         mbar_init_fence();
         sh.abort = 0;

@@ -2,44 +2,50 @@
 //
 // The kernel of the paged attention (attention_f32.cuh) with another source: tiles of 64 keys and values come from packed rows
 // by one tiled copy each, and the items are pieces of prompts (prompt.cuh), whole ones, so nothing is joined.  Five prompts of 100 to 1,500
-// tokens, 32/8 heads of 128: 280 us, 195 TFLOP/s, with six bf16 products for each float32 one 0.62 of the measured bf16 rate; the tensor cores
-// are busy for 53 % of the cycles, and the softmax with its split into three parts is what they wait for.
+// tokens, 32/8 heads of 128: 276 us, 197 TFLOP/s, with six bf16 products for each float32 one 0.63 of the measured bf16 rate (282 us with the walk and
+// the copies in one warp); the tensor cores are busy for 53 % of the cycles, and the softmax with its split into three parts is what they wait for.
 #include "attention_f32.cuh"
 #include "prompt.cuh"
 #include "tensor_map.h"
 
 namespace sv {
 
-// ---- warp 15: the walk over the CTA's items, and the copies --------------------------------
+// ---- warp 12: the walk over the CTA's items ------------------------------------------------
+__device__ __forceinline__ void prompt_f32_walk_role(const PromptParams& p, F32Shared& sh, PromptWalk& w) {
+    Piece it = {};
+    w.start();
+    for (int told = 0;; ++told) {
+        const bool any = w.next(p, &it);
+        Segment& seg = sh.seg[told % kSegments];
+        if (!warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort)) return;
+        if ((threadIdx.x & 31) == 0) {
+            // the piece's first token is the block's
+            if (any) {
+                const Keys keys = keys_of<kTile>(p, it.at, it.tokens);
+                seg = {0, keys.tiles, keys.sink_tiles, keys.first_tile, keys.low, keys.high, keys.sink, it.at, 0, it.tokens * p.G, it.head, 1, 0,
+                       it.row0 + it.at};
+            } else {
+                seg.t0 = seg.t1 = 0;
+            }
+            mbar_arrive(&sh.seg_full[told % kSegments]);
+        }
+        __syncwarp();
+        if (!any) return;
+    }
+}
+
+// ---- warp 15: keys and values --------------------------------------------------------------
 template <int DP>
 __device__ __forceinline__ void prompt_f32_copy_role(const PromptParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, char* raw,
-                                                     F32Shared& sh, PromptWalk& w) {
+                                                     F32Shared& sh) {
     using Lay = F32Layout<DP>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(raw);
     const unsigned bytes = kTile * p.a.D * 4;
     const uint64_t stay = l2_evict_normal_policy();
-    Piece it = {};
-    Keys keys = {};
-    int told = 0, slot = 0;
+    int slot = 0;
     unsigned phase = 1;
     bool ok = true;
-    auto tell = [&](bool any) {
-        Segment& seg = sh.seg[told % kSegments];
-        ok = ok && warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort);
-        if (any) keys = keys_of<kTile>(p, it.at, it.tokens);
-        if (ok && lane == 0) {
-            // the piece's first token is the block's
-            if (any)
-                seg = {0, keys.tiles, keys.sink_tiles, keys.first_tile, keys.low, keys.high, keys.sink, it.at, 0, it.tokens * p.G, it.head, 1, 0,
-                       it.row0 + it.at};
-            else
-                seg.t0 = seg.t1 = 0;
-            mbar_arrive(&sh.seg_full[told % kSegments]);
-        }
-        __syncwarp();
-        ++told;
-    };
     auto copy = [&](const CUtensorMap* map, int head, int row) {
         ok = ok && warp_wait_for(&sh.raw_empty[slot], phase, &sh.abort);
         if (!ok) return;
@@ -54,24 +60,23 @@ __device__ __forceinline__ void prompt_f32_copy_role(const PromptParams& p, cons
             phase ^= 1;
         }
     };
-    w.start();
-    bool more = w.next(p, &it);
-    tell(more);
-    while (more && ok) {
-        const int tiles = keys.tiles;
-        for (int t = 0; t < tiles && ok; ++t) {
-            const int row = (int)it.row0 + start_of<kTile>(keys.sink_tiles, keys.first_tile, t), head = it.head;
-            copy(kmap, head, row);
-            if (t == tiles - 1) {
-                more = w.next(p, &it);
-                tell(more);
-            }
-            copy(vmap, head, row);
+    for (int n_seg = 0; ok; ++n_seg) {
+        const int place = n_seg % kSegments;
+        ok = warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort);
+        if (!ok) break;
+        const Segment w = sh.seg[place];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
+        if (w.t0 == w.t1) return;
+        const int row0 = (int)w.row0 - w.len;   // the prompt's first row
+        for (int t = 0; t < w.t1 && ok; ++t) {
+            copy(kmap, w.head, row0 + w.start(t));
+            copy(vmap, w.head, row0 + w.start(t));
         }
     }
-    if (!ok)   // gave up: whatever was copied must have arrived before the CTA's memory is given back
-        for (int s = 0; s < Lay::kRaws; ++s)
-            for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.raw_full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
+    // gave up: whatever was copied must have arrived before the CTA's memory is given back
+    for (int s = 0; s < Lay::kRaws; ++s)
+        for (int n = 0; n < kTcSpinLimit / 64 && !mbar_try_wait(&sh.raw_full[s], (s < slot ? phase : phase ^ 1) ^ 1); ++n) {}
 }
 
 template <int DP>
@@ -83,7 +88,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) prompt_f32_kernel(const Prompt
     char* const raw = smem + 2 * kPlanes * Lay::kPlane;
     F32Shared& sh = *reinterpret_cast<F32Shared*>(smem + Lay::kBytes);
     const int warp = threadIdx.x >> 5;
-    f32_begin<DP>(sh);
+    f32_begin<DP>(sh, 23);   // softmax 4, keys 8, values 8, products 2, copies
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
@@ -92,13 +97,15 @@ __global__ void __launch_bounds__(kF32Threads, 1) prompt_f32_kernel(const Prompt
     if (warp >= 12) {
         registers_down<kRegsRest>();
         if (warp == 15) {
-            PromptWalk w;
-            prompt_f32_copy_role<DP>(pp, &kmap, &vmap, raw, sh, w);
-            prompt_statuses(pp, w);
+            prompt_f32_copy_role<DP>(pp, &kmap, &vmap, raw, sh);
         } else if (warp == 14) {
             if (!f32_keys_role<DP>(p, planes, sh)) drain(&sh.drain[0]);
         } else if (warp == 13) {
             if (!f32_values_role<DP>(planes, sh)) drain(&sh.drain[1]);
+        } else {
+            PromptWalk w;
+            prompt_f32_walk_role(pp, sh, w);
+            prompt_statuses(pp, w);
         }
     } else if (warp >= 4) {
         registers_up<kRegsSplit>();
