@@ -446,7 +446,7 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
         const int at_first = w.at + g * p.group, at_last = at_first + tokens - 1;
         const bool mine = token_in < tokens;
         const int at = min(at_first + token_in, at_last);
-        const int low = kWindow ? at + 1 - p.a.window : 0;   // the row sees [low, at] and [0, sinks)
+        const int low = kWindow ? max(0, at + 1 - p.a.window) : 0;   // the row sees [low, at] and [0, sinks)
         float m = -kInf, l = 0.f;
         for (int t = 0; t < n; ++t, ++n_all) {
             const int buf = kGroups == 2 ? g : (int)(n_all & 1);
@@ -460,13 +460,16 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
             if (kWindow && !clean) {
                 // A bit a column (a comparison each, as it comes from the compiler, takes 8,000 cycles), 32 columns at a time and in
                 // place: unrolled, the longer masks take 2,000, of which most is waiting for instructions.
+                // A first tile that begins in front of the prompt (at -15 or behind) holds no position of kKeys or more: what is near 2^31, less
+                // a negative position, does not fit 32 bits.
+                const int far = j0 < 0 ? kKeys : INT32_MAX;
 #pragma unroll 1
                 for (int c = 0; c < kKeys; c += 32) {
                     const int j = j0 + c;
-                    unsigned sees = below(at + 1 - j);
+                    unsigned sees = below(min(at + 1, far) - j);
                     if (kWindow) {
                         const unsigned leads = below(lead - c);
-                        sees = first ? below(w.sink - j) : (sees & (~below(low - j) | below(p.a.sinks - j)) & ~leads) | (below(w.sink - c) & leads);
+                        sees = first ? below(w.sink - j) : (sees & (~below(low - j) | below(min(p.a.sinks, far) - j)) & ~leads) | (below(w.sink - c) & leads);
                     }
                     if (!__any_sync(0xffffffffu, sees != ~0u)) continue;
                     uint32_t s[32];
