@@ -623,7 +623,7 @@ int spec_rotary_turns(const double* frequency, int32_t n, uint64_t* turns);
 
 /*
  * spec_rotate - rows [rows, heads, D] turned by their positions [rows] int32 (any values).
- * x and out have row strides in elements (slices of a wider projection); out may be x itself (with the same stride), and overlaps it in no
+ * x and out have row strides in elements (slices of a wider projection); out may be x itself (with the same stride, if there is more than one row), and overlaps it in no
  * other way.  Queries and keys that lie beside each other are one call with the heads of both.
  * Errors: SPEC_ERR_ARG (NULL pointer, turns not 8-byte aligned, magnitude not finite), SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (heads outside [1, 4096], D not a multiple of 8 up to
  * SPEC_MAX_HEAD, dim odd or outside [2, D], rows outside [0, 2^31), a row stride below heads * D, in place with two strides),
@@ -652,7 +652,7 @@ int spec_rotate(const spec_rotate_args* args, void* stream);
  *     extra_rows = 0: cu is the rows' own prefix sum, and a stream may have none; extra_rows = 1: cu is cu_drafts, a block being one
  *     token more than its drafts, any number of them.  cu NULL: max_rows each.  Rows behind the last stream's are left alone.
  *   - reserved [B] (or NULL): the status of the spec_cache_resize that made the room, as in spec_cache_append_reserved.
- *   - Hq = 0: no queries.  q_out may be q, and k_out may be k (with the same strides); otherwise nothing overlaps.
+ *   - Hq = 0: no queries.  q_out may be q, and k_out may be k (with the same strides, if there is more than one row); otherwise nothing overlaps.
  * status [B]: SPEC_ST_OK, BAD_OFFSETS, the entry of reserved, BAD_LENGTH, NO_PAGES as in spec_cache_append_reserved (nothing of
  * the stream is written, its rows of q_out and k_out neither), BAD_PAGE (rows whose page is not in the pool are written to q_out and k_out only).
  * Errors: SPEC_ERR_ARG (NULL pointer, a pool that is not 16-byte aligned, turns not 8-byte aligned, magnitude not finite), SPEC_ERR_DTYPE, SPEC_ERR_SHAPE (as in spec_cache_append and

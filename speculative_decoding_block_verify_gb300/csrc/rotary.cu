@@ -626,7 +626,7 @@ extern "C" int spec_rotate(const spec_rotate_args* a, void* stream) {
     if (a->rows < 0 || a->rows > INT32_MAX) return set_error(SPEC_ERR_SHAPE, "spec_rotate: rows = %lld", (long long)a->rows);
     const int64_t dense = (int64_t)a->heads * a->D;
     if (a->x_row_stride < dense || a->out_row_stride < dense) return set_error(SPEC_ERR_SHAPE, "spec_rotate: a row stride is below heads * D");
-    if (a->rows > 0 && a->x == a->out && a->x_row_stride != a->out_row_stride)
+    if (a->rows > 1 && a->x == a->out && a->x_row_stride != a->out_row_stride)
         return set_error(SPEC_ERR_SHAPE, "spec_rotate: in place with different row strides");
     if (a->rows == 0) return SPEC_OK;
     if (a->turns == nullptr || a->positions == nullptr || a->x == nullptr || a->out == nullptr)
@@ -660,7 +660,7 @@ extern "C" int spec_cache_append_rotated(const spec_append_rotated_args* a, void
     if (a->k_row_stride < dk || a->v_row_stride < dk || (a->Hq > 0 && (a->q_row_stride < dq || a->q_out_row_stride < dq)) ||
         (a->k_out != nullptr && a->k_out_row_stride < dk))
         return set_error(SPEC_ERR_SHAPE, "%s: a row stride is below its heads * D", who);
-    if (a->rows > 0 && ((a->Hq > 0 && a->q_out == a->q && a->q_out_row_stride != a->q_row_stride) ||
+    if (a->rows > 1 && ((a->Hq > 0 && a->q_out == a->q && a->q_out_row_stride != a->q_row_stride) ||
         (a->k_out != nullptr && a->k_out == a->k && a->k_out_row_stride != a->k_row_stride)))
         return set_error(SPEC_ERR_SHAPE, "%s: in place with different row strides", who);
     if (a->rows < 0 || a->rows > INT32_MAX || (a->cu == nullptr && a->rows < (int64_t)a->B * a->max_rows))
