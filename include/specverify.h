@@ -531,8 +531,10 @@ size_t spec_paged_attention_workspace_bytes(const spec_attention_args* args);
  * q [rows, Hq, D], k and v [rows, Hkv, D] with row strides in elements (slices of a wider projection), out [rows, Hq, D] dense, one dtype.
  * cu_rows [B + 1] int32 (NULL: B prompts of rows / B).  out overlaps none of them.  Rows behind the last prompt's are not written, and what they hold
  * does not matter.
- * status [B]: SPEC_ST_OK, or BAD_OFFSETS for the first prompt whose offsets are broken (cu_rows[0] not 0, a negative count, rows
- * beyond `rows`) and all behind it, whose rows are not written.  Where a bounded wait gives up rows are NaN.
+ * status [B]: SPEC_ST_OK, BAD_OFFSETS for the first prompt whose offsets are broken (cu_rows[0] not 0, a negative count, rows
+ * beyond `rows`) and all behind it, whose rows are not written, or TIMEOUT: a bounded wait gave up, in this call or in an earlier one that had rows of
+ * this type on this device (the mark that it leaves stays set, see spec_prompt_mark_timeout).  Rows of a TIMEOUT are undefined; those that
+ * were waited for are NaN.
  * Sums and softmax statistics are float32.  With bf16 the weights e_j are rounded to bf16 before they meet the values, and the
  * same rounded weights are summed.  A value that is not finite reaches the rows that see it, and may reach rows of its prompt up to 255 tokens
  * before it, or behind the last that sees it; it reaches no other prompt.  In float32 infinite queries, keys and values count as NaN.  Results are the same from run to run.
@@ -557,6 +559,11 @@ typedef struct {
 } spec_prompt_args;
 
 int spec_prompt_attention(const spec_prompt_args* args, void* stream);
+
+/* spec_prompt_mark_timeout - clears (marked = 0) the current device's marks of waits that gave up, in the stream's order, once the cause is dealt
+ * with; or sets them (1), so that spec_prompt_attention reports TIMEOUT and a caller's handling of it can be tried.  Errors: SPEC_ERR_ARG (marked not
+ * 0 or 1), SPEC_ERR_CUDA. */
+int spec_prompt_mark_timeout(int32_t marked, void* stream);
 
 /*
  * spec_cache_append - the block's new keys and values into their pages.

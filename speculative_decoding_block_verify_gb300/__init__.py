@@ -22,6 +22,7 @@ Entry points (same names as the C ABI):
 * ``spec_cache_resize``      - pages reserved before a block and given back after its verify
 * ``spec_cache_fork``        - a stream's pages shared with other streams
 * ``spec_prompt_attention``  - causal attention over whole prompts, packed one behind the other
+* ``spec_prompt_mark_timeout`` - what a wait that gave up has left there is cleared
 * ``spec_rotate``            - rotary positions of packed rows (``RotaryTable``: their frequencies)
 * ``spec_cache_append_rotated`` - a block's or a whole prompt's keys rotated into their pages, its queries rotated on the way
 * ``spec_philox_uniforms``   - the verify calls' uniforms (for checking)
@@ -45,7 +46,7 @@ __all__ = [
     "spec_philox_uniforms", "spec_verify_launch_info",
     "spec_verify_workspace_bytes", "spec_verify_block_static",
     "spec_paged_attention", "spec_cache_append", "spec_cache_resize", "spec_cache_fork", "spec_prompt_attention",
-    "RotaryTable", "spec_rotate", "spec_cache_append_rotated", "lib", "lib_path", "SpecError",
+    "spec_prompt_mark_timeout", "RotaryTable", "spec_rotate", "spec_cache_append_rotated", "lib", "lib_path", "SpecError",
     "DTYPE_F32", "DTYPE_BF16", "STATUS_NAMES", "DIAG_COLS",
 ]
 
@@ -67,7 +68,7 @@ EXPORTED = ["dspark_markov_bias", "dspark_markov_walk", "dspark_markov_walk_work
             "spec_cost_curve_table", "spec_cost_curve_upload", "spec_cost_curve_destroy",
             "spec_paged_attention", "spec_paged_attention_workspace_bytes", "spec_cache_append",
             "spec_cache_append_reserved", "spec_cache_resize", "spec_cache_resize_workspace_bytes", "spec_cache_fork",
-            "spec_prompt_attention", "spec_rotary_frequencies", "spec_rotary_turns", "spec_rotate", "spec_cache_append_rotated",
+            "spec_prompt_attention", "spec_prompt_mark_timeout", "spec_rotary_frequencies", "spec_rotary_turns", "spec_rotate", "spec_cache_append_rotated",
             "spec_last_error", "spec_version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -174,6 +175,7 @@ def lib():
     L.spec_cache_fork.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     f64 = ctypes.c_double
     L.spec_prompt_attention.argtypes = [vp, vp]
+    L.spec_prompt_mark_timeout.argtypes = [i32, vp]
     L.spec_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
     L.spec_rotary_turns.argtypes = [vp, i32, vp]
     L.spec_rotate.argtypes = [vp, vp]
@@ -187,7 +189,7 @@ def lib():
                  "spec_pipeline_destroy", "spec_cost_curve_begin", "spec_cost_curve_end",
                  "spec_cost_curve_poll", "spec_cost_curve_observe", "spec_cost_curve_table",
                  "spec_cost_curve_upload", "spec_paged_attention", "spec_cache_append", "spec_cache_append_reserved",
-                 "spec_cache_resize", "spec_cache_fork", "spec_prompt_attention", "spec_rotary_frequencies",
+                 "spec_cache_resize", "spec_cache_fork", "spec_prompt_attention", "spec_prompt_mark_timeout", "spec_rotary_frequencies",
                  "spec_rotary_turns", "spec_rotate", "spec_cache_append_rotated"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -890,7 +892,8 @@ def spec_prompt_attention(q, k, v, cu_rows, scale, window=0, sinks=0, out=None, 
 
     q [rows, Hq, D], k and v [rows, Hkv, D] of one dtype (float32/bf16; rows may be slices of a wider projection, on 16-byte
     boundaries); prompt b has rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows [B + 1] int32; None: one prompt of all rows).
-    window and sinks as in spec_paged_attention.  Returns (and reuses) ``out`` with out [rows, Hq, D], status [B]."""
+    window and sinks as in spec_paged_attention.  Returns (and reuses) ``out`` with out [rows, Hq, D], status [B].  A call that reports TIMEOUT leaves
+    a mark on the device: the calls after it report TIMEOUT as well until spec_prompt_mark_timeout clears it."""
     torch = _T or _cache_torch()
     shape, device, dtype = q.shape, q.get_device(), q.dtype
     if device < 0:
@@ -924,6 +927,13 @@ def spec_prompt_attention(q, k, v, cu_rows, scale, window=0, sinks=0, out=None, 
     if rc != 0:
         _check(rc)
     return out
+
+
+def spec_prompt_mark_timeout(marked=False, stream=None):
+    """Clears what a wait of spec_prompt_attention that gave up has left on the current device; or sets it (True), so that the calls
+    behind this one in the stream report TIMEOUT and a program's handling of that can be tried."""
+    torch = _T or _cache_torch()
+    _check((_lib or lib()).spec_prompt_mark_timeout(int(marked), _raw_stream(stream, torch.cuda.current_device())))
 
 
 class RotaryTable:

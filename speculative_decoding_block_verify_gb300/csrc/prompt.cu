@@ -1,4 +1,4 @@
-// spec_prompt_attention: the entry point.
+// spec_prompt_attention: the entry points.
 #include "prompt.cuh"
 
 #include <cmath>
@@ -12,7 +12,7 @@ __global__ void __launch_bounds__(32) no_rows_kernel(const PromptParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     PromptWalk w;
     w.start();
-    prompt_statuses(p, w);
+    prompt_statuses(p, w, nullptr);   // no rows, no waits
 }
 
 }  // namespace sv
@@ -60,4 +60,13 @@ extern "C" int spec_prompt_attention(const spec_prompt_args* a, void* stream) {
                           : a->dtype == SPEC_DTYPE_BF16 ? launch_prompt_tc(p, sms, s)
                                                         : launch_prompt_f32(p, sms, s);
     return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, who);
+}
+
+extern "C" int spec_prompt_mark_timeout(int32_t marked, void* stream) {
+    clear_error();
+    if ((marked & ~1) != 0) return set_error(SPEC_ERR_ARG, "spec_prompt_mark_timeout: marked = %d", marked);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = mark_prompt_tc(marked, s);
+    if (e == cudaSuccess) e = mark_prompt_f32(marked, s);
+    return e == cudaSuccess ? SPEC_OK : set_cuda_error(e, "spec_prompt_mark_timeout");
 }

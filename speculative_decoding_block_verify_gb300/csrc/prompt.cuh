@@ -158,22 +158,31 @@ struct PromptWalk {
     }
 };
 
-// The statuses, by the warp of every CTA that walked: CTA c has those of batches c, c + gridDim.x, .. of 32 prompts.
-__device__ __forceinline__ void prompt_statuses(const PromptParams& p, PromptWalk& w) {
+// The statuses, by the warp of every CTA that walked: CTA c has those of batches c, c + gridDim.x, .. of 32 prompts.  `mark` (or nullptr) is set
+// where a wait has given up, which may be in another CTA and later: whoever sets it writes statuses behind that (prompt_gave_up), and whoever
+// writes one looks at it behind that.
+__device__ __forceinline__ void prompt_statuses(const PromptParams& p, PromptWalk& w, const int32_t* mark) {
     const int lane = threadIdx.x & 31;
     if ((int64_t)blockIdx.x * 32 >= p.a.B) return;
     while (!w.ended) {   // (a walk that was broken off, or had no item)
         w.first += PromptWalk::kBatch;
         w.load(p);
     }
-    for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.a.B; b += (int64_t)gridDim.x * 32)
+    for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.a.B; b += (int64_t)gridDim.x * 32) {
         p.a.status[b] = b < w.broken ? SPEC_ST_OK : SPEC_ST_BAD_OFFSETS;
+        if (mark == nullptr || b >= w.broken) continue;
+        __threadfence();
+        if (*reinterpret_cast<const volatile int32_t*>(mark) != 0) p.a.status[b] = SPEC_ST_TIMEOUT;
+    }
 }
 
-// A wait of this CTA gave up: one warp leaves NaN in the rows of all its items.
+// A wait of this CTA gave up: one warp sets the mark, leaves NaN in the rows of all its items, and has every prompt report it.
 template <typename T>
-__device__ __noinline__ void prompt_gave_up(const PromptParams& p, T nan) {
+__device__ __noinline__ void prompt_gave_up(const PromptParams& p, T nan, int32_t* mark) {
     const int lane = threadIdx.x & 31;
+    if (lane == 0) atomicExch(mark, 1);
+    __syncwarp();
+    __threadfence();
     PromptWalk w;
     Piece it;
     w.start();
@@ -184,10 +193,13 @@ __device__ __noinline__ void prompt_gave_up(const PromptParams& p, T nan) {
             for (int i = lane; i < per; i += 32) to[i] = nan;
         }
     }
+    for (int b = lane; b < p.a.B && b < w.broken; b += 32) p.a.status[b] = SPEC_ST_TIMEOUT;
 }
 
 cudaError_t launch_prompt_tc(const PromptParams& p, int sms, cudaStream_t s);    // bf16 (prompt_tc.cu)
 cudaError_t launch_prompt_f32(const PromptParams& p, int sms, cudaStream_t s);   // float32 heads up to 128 (prompt_f32.cu)
+cudaError_t mark_prompt_tc(int32_t marked, cudaStream_t s);    // each kernel's mark of a wait that gave up, on the current device
+cudaError_t mark_prompt_f32(int32_t marked, cudaStream_t s);
 // CTAs of a grid: what is resident, or fewer where there cannot be as many items.
 inline int prompt_ctas(const PromptParams& p, int resident) {
     const int64_t items = (p.a.rows / p.piece + p.a.B) * p.a.Hkv;

@@ -10,6 +10,13 @@
 
 namespace sv {
 
+static __device__ int32_t g_mark;   // a wait gave up since it was last cleared
+static __global__ void mark_kernel(int32_t marked) { g_mark = marked; }
+cudaError_t mark_prompt_f32(int32_t marked, cudaStream_t s) {
+    mark_kernel<<<1, 1, 0, s>>>(marked);
+    return cudaGetLastError();
+}
+
 // ---- warp 12: the walk over the CTA's items ------------------------------------------------
 __device__ __forceinline__ void prompt_f32_walk_role(const PromptParams& p, F32Shared& sh, PromptWalk& w) {
     Piece it = {};
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) prompt_f32_kernel(const Prompt
         } else {
             PromptWalk w;
             prompt_f32_walk_role(pp, sh, w);
-            prompt_statuses(pp, w);
+            prompt_statuses(pp, w, &g_mark);
         }
     } else if (warp >= 4) {
         registers_up<kRegsSplit>();
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) prompt_f32_kernel(const Prompt
         f32_softmax_role<DP>(p, sh);
     }
     f32_end<DP>(sh);
-    if (warp == 15 && sh.abort) prompt_gave_up<float>(pp, __int_as_float(0x7fffffff));
+    if (warp == 15 && sh.abort) prompt_gave_up<float>(pp, __int_as_float(0x7fffffff), &g_mark);
 }
 
 // [rows][Hkv][D] in boxes of a head and 64 rows.

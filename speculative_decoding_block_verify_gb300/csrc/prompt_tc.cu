@@ -36,6 +36,13 @@
 
 namespace sv {
 
+static __device__ int32_t g_mark;   // a wait gave up since it was last cleared
+static __global__ void mark_kernel(int32_t marked) { g_mark = marked; }
+cudaError_t mark_prompt_tc(int32_t marked, cudaStream_t s) {
+    mark_kernel<<<1, 1, 0, s>>>(marked);
+    return cudaGetLastError();
+}
+
 constexpr int kPromptThreads = 384;
 // registers of a thread of the softmax's two warpgroups and of the last one, where the CTA was launched with kRegsStart each
 constexpr int kRegsRows = 208, kRegsOthers = 88, kRegsStart = 168;
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
         } else {
             PromptWalk w;
             prompt_walk_role<DP, kWindow>(p, sh, w);
-            prompt_statuses(p, w);   // while the last tiles are computed
+            prompt_statuses(p, w, &g_mark);   // while the last tiles are computed
         }
     } else {
         if (Lay::kGroups == 2) registers_up<kRegsRows>();
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"((uint32_t)Lay::kCols));
     }
-    if (warp == 8 && sh.abort) prompt_gave_up<unsigned short>(p, 0x7fff);
+    if (warp == 8 && sh.abort) prompt_gave_up<unsigned short>(p, 0x7fff, &g_mark);
 }
 
 // ---------------------------------------------------------------------------------------
