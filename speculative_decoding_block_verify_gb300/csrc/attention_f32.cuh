@@ -69,6 +69,7 @@ struct F32Shared {
     int scratch;
     uint32_t tmem;
     int abort;
+    int moved;   // tiles copied so far (prompts)
 };
 
 // x less the bf16 pair w, exact for the roundings below
@@ -466,7 +467,7 @@ __device__ __forceinline__ void f32_begin(F32Shared& sh, int listeners) {
             mbar_init(&sh.seg_empty[i], listeners);
         }
         mbar_init_fence();
-        sh.abort = 0;
+        sh.abort = sh.moved = 0;
     }
 }
 template <int DP>

@@ -24,7 +24,7 @@ __device__ __forceinline__ void prompt_f32_walk_role(const PromptParams& p, F32S
     for (int told = 0;; ++told) {
         const bool any = w.next(p, &it);
         Segment& seg = sh.seg[told % kSegments];
-        if (!warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort)) return;
+        if (!warp_wait_moving(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort, &sh.moved)) return;
         if ((threadIdx.x & 31) == 0) {
             // the piece's first token is the block's
             if (any) {
@@ -79,6 +79,7 @@ __device__ __forceinline__ void prompt_f32_copy_role(const PromptParams& p, cons
         for (int t = 0; t < w.t1 && ok; ++t) {
             copy(kmap, w.head, row0 + w.start(t));
             copy(vmap, w.head, row0 + w.start(t));
+            if (lane == 0) *reinterpret_cast<volatile int*>(&sh.moved) += 1;
         }
     }
     // gave up: whatever was copied must have arrived before the CTA's memory is given back

@@ -90,6 +90,7 @@ struct PromptShared {
     PromptSegment seg[kSegments];
     uint32_t tmem;
     int abort;
+    int moved;   // tiles copied so far
 };
 
 // ---- warp 11: the walk over the CTA's items ------------------------------------------------------
@@ -102,7 +103,7 @@ __device__ __forceinline__ void prompt_walk_role(const PromptParams& p, PromptSh
     for (int told = 0;; ++told) {
         const bool any = w.next(p, &it);
         PromptSegment& seg = sh.seg[told % kSegments];
-        if (!warp_wait_for(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort)) return;
+        if (!warp_wait_moving(&sh.seg_empty[told % kSegments], ((told / kSegments) & 1) ^ 1, &sh.abort, &sh.moved)) return;
         if (lane == 0) {
             seg.tiles = 0;
             if (any) {
@@ -175,6 +176,7 @@ __device__ __forceinline__ void prompt_copy_role(const CUtensorMap* kmap, const 
             const int row0 = (int)w.row0, row = row0 + w.start<Lay::kKeys, kWindow>(t), lead = t == 0 ? w.lead : 0;
             copy(kmap, kmap16, w.head, row0, row, lead);
             copy(vmap, vmap16, w.head, row0, row, lead);
+            if (lane == 0) *reinterpret_cast<volatile int*>(&sh.moved) += 1;
         }
     }
     // gave up: whatever was copied must have arrived before the CTA's memory is given back
@@ -194,7 +196,7 @@ __device__ __forceinline__ void prompt_queries_role(const PromptParams& p, const
     bool ok = true;
     for (int n_seg = 0; ok; ++n_seg) {
         const int place = n_seg % kSegments;
-        ok = warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort);
+        ok = warp_wait_moving(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort, &sh.moved);
         if (!ok) break;
         const int tiles = sh.seg[place].tiles, tokens = sh.seg[place].tokens, head = sh.seg[place].head * p.G;
         const int row = (int)sh.seg[place].row0 + sh.seg[place].at;
@@ -206,7 +208,7 @@ __device__ __forceinline__ void prompt_queries_role(const PromptParams& p, const
 #pragma unroll
         for (int g = 0; g < Lay::kGroups; ++g) {
             if (g * p.group >= tokens) break;
-            ok = ok && warp_wait_for(&sh.q_empty[g], (copies[g] & 1) ^ 1, &sh.abort);
+            ok = ok && warp_wait_moving(&sh.q_empty[g], (copies[g] & 1) ^ 1, &sh.abort, &sh.moved);
             if (!ok) break;
             if (lane == 0) {
                 mbar_expect_tx(&sh.q_full[g], Lay::kHalves * p.group * p.G * 128);
@@ -442,7 +444,7 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
     unsigned n_all = 0, tiles_all = 0, items = 0;   // tiles of the group, of the CTA, and the group's items so far
     for (int n_seg = 0;; ++n_seg) {
         const int place = n_seg % kSegments;
-        if (!warp_wait_for(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort)) return;
+        if (!warp_wait_moving(&sh.seg_full[place], (n_seg / kSegments) & 1, &sh.abort, &sh.moved)) return;
         const PromptSegment w = sh.seg[place];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[place]);
@@ -459,7 +461,7 @@ __device__ __forceinline__ void prompt_softmax_role(const PromptParams& p, char*
             const int buf = kGroups == 2 ? g : (int)(n_all & 1);
             const unsigned uses = kGroups == 2 ? n_all : n_all >> 1;
             const int j0 = w.start<kKeys, kWindow>(t), lead = kWindow && t == 0 ? w.lead : 0;
-            if (!warp_wait_for(&sh.s_full[buf], uses & 1, &sh.abort)) return;
+            if (!warp_wait_moving(&sh.s_full[buf], uses & 1, &sh.abort, &sh.moved)) return;   // (the other group's items may have no rows of this one)
             tc_fence_after();
             // a tile that every row sees whole needs no mask
             const bool first = kWindow && t < w.sink_tiles;   // of the first tokens alone
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_tc_kernel(const Prom
             mbar_init(&sh.seg_empty[i], 4 * Lay::kGroups + 3);   // softmax, copies of keys and values, of queries, products
         }
         mbar_init_fence();
-        sh.abort = 0;
+        sh.abort = sh.moved = 0;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

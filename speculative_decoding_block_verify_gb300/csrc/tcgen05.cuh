@@ -50,6 +50,21 @@ __device__ __forceinline__ bool warp_wait_for(uint64_t* bar, unsigned parity, in
     }
     return true;
 }
+// ... where a whole item may pass before the phase: the polls count from the last tile that was copied (`moved` tells), so that the limit
+// is as far away for any length of an item.  (What moves the tiles waits with the limit above.)
+__device__ __forceinline__ bool warp_wait_moving(uint64_t* bar, unsigned parity, int* abort, const int* moved) {
+    int was = 0;
+    for (int n = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++n) {
+        if ((n & 15) == 0) {
+            const int now = __shfl_sync(0xffffffffu, *reinterpret_cast<const volatile int*>(moved), 0);   // one count for the warp
+            if (now != was) n = 0;
+            was = now;
+            if (n > kTcSpinLimit) *reinterpret_cast<volatile int*>(abort) = 1;
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort) != 0)) return false;
+        }
+    }
+    return true;
+}
 
 // Shared-memory matrix descriptors, 128-byte swizzle, strides in units of 16 bytes.  K-major (Q, K): 8 rows of 128
 // bytes are an atom of 1,024 bytes, the next 8 rows begin `group` further on.  MN-major (V, whose rows are the
