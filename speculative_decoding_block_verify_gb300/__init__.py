@@ -942,8 +942,8 @@ class RotaryTable:
     Pair j of dim / 2 turns by base^(-2 j / dim) radians a position; ``scaling`` stretches that for contexts ``factor``
     times as long: "none", "linear" (position interpolation), "ntk" (a larger base), "yarn" (pairs that turn fewer than
     ``slow`` times in the ``original`` context are stretched, those that turn more than ``fast`` times are not).
-    ``frequencies`` gives them (dim / 2 numbers, radians a position) instead.  ``magnitude`` multiplies what is turned
-    (None: 0.1 ln(factor) + 1 for "yarn", otherwise 1).  A pair is (j, j + dim / 2), or with ``interleaved`` (2 j, 2 j + 1)."""
+    ``frequencies`` gives them (dim / 2 numbers, radians a position) instead, as they are: no scaling stretches them.  ``magnitude``
+    multiplies what is turned (None: 0.1 ln(factor) + 1 for "yarn", of given frequencies too, otherwise 1).  A pair is (j, j + dim / 2), or with ``interleaved`` (2 j, 2 j + 1)."""
 
     SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -956,9 +956,9 @@ class RotaryTable:
             raise ValueError(f"dim must be even and at least 2, got {dim}")
         n = dim // 2
         freq, mag = (ctypes.c_double * n)(), ctypes.c_float(1.0)
-        if frequencies is None:
+        if frequencies is None or (scaling == "yarn" and magnitude is None):
             _check(lib().spec_rotary_frequencies(dim, base, self.SCALINGS[scaling], factor, original, slow, fast, freq, ctypes.byref(mag)))
-        else:
+        if frequencies is not None:
             if len(frequencies) != n:
                 raise ValueError(f"frequencies must be {n} numbers")
             freq[:] = [float(f) for f in frequencies]
