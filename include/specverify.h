@@ -618,10 +618,13 @@ int spec_cache_append_reserved(const spec_append_args* args, const int32_t* rese
  *   SPEC_ROTARY_NTK     with base factor^(dim / (dim - 2)) instead of base;
  *   SPEC_ROTARY_YARN    g f_j + (1 - g) f_j / factor, g = (r - slow) / (fast - slow) cut off at 0 and 1, where r = original
  *                       f_j / 2 pi is how often the pair turns in the original context (Peng et al. 2023, with slow 1 and fast 32).
+ *                       The ramp is linear in r, as that paper defines it.  Common implementations make it linear in the pair's index between two
+ *                       rounded borders, which gives other frequencies between them (by up to a factor of 3 of the same scaling): a model
+ *                       that was tuned so wants its own frequencies, see spec_rotary_turns.
  * magnitude (host): 0.1 ln(factor) + 1 for YARN, otherwise 1.  Errors: SPEC_ERR_ARG (NULL, an unknown scaling, base not
  * finite and above 1, and of what the scaling uses factor below 1, original below 1, fast not above slow, or one not finite),
  * SPEC_ERR_SHAPE (dim odd or outside [2, SPEC_MAX_HEAD]).
- * spec_rotary_turns - turns [n] (host) of any finite frequencies [n] (host).  Errors: SPEC_ERR_ARG, SPEC_ERR_SHAPE (n outside
+ * spec_rotary_turns - turns [n] (host) of any finite frequencies [n] (host), those of another scaling among them.  Errors: SPEC_ERR_ARG, SPEC_ERR_SHAPE (n outside
  * [1, SPEC_MAX_HEAD / 2]).  Neither call touches a device.
  */
 int spec_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor, double original, double slow, double fast,

@@ -941,7 +941,9 @@ class RotaryTable:
 
     Pair j of dim / 2 turns by base^(-2 j / dim) radians a position; ``scaling`` stretches that for contexts ``factor``
     times as long: "none", "linear" (position interpolation), "ntk" (a larger base), "yarn" (pairs that turn fewer than
-    ``slow`` times in the ``original`` context are stretched, those that turn more than ``fast`` times are not).
+    ``slow`` times in the ``original`` context are stretched, those that turn more than ``fast`` times are not, and between them
+    the ramp is linear in the number of turns, as in the method's paper; models that were tuned with a ramp over the pairs'
+    indices, or with another scaling, give their ``frequencies``).
     ``frequencies`` gives them (dim / 2 numbers, radians a position) instead, as they are: no scaling stretches them.  ``magnitude``
     multiplies what is turned (None: 0.1 ln(factor) + 1 for "yarn", of given frequencies too, otherwise 1).  A pair is (j, j + dim / 2), or with ``interleaved`` (2 j, 2 j + 1)."""
 
