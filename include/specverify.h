@@ -609,8 +609,9 @@ int spec_cache_append_reserved(const spec_append_args* args, const int32_t* rese
  * At position p pair j turns by the angle p f_j and is multiplied by `magnitude`:
  *   a' = magnitude (a cos(p f_j) - b sin(p f_j)),   b' = magnitude (b cos(p f_j) + a sin(p f_j));
  * the rest of the head stays as it is.  The calls take the frequencies as turns [dim / 2] in device memory: 2^64 f_j / 2 pi
- * modulo 2^64, so that position times turns modulo 2^64 is the exact fraction of a turn.  Angles are therefore as good at far positions as at near ones,
- * and negative positions turn back.  Arithmetic is float32, rounded once to the output's type.
+ * modulo 2^64, so that position times turns modulo 2^64 is the fraction of a turn with nothing lost in the product.  What an angle is off by is the position
+ * times the rounding of its turns (spec_rotary_turns: up to |f_j / 2 pi| 2^-52 + 2^-54 of a turn; 2^-55 for f_j up to 1, which float32 does not
+ * see below positions of 2^27), and negative positions turn back.  Arithmetic is float32, rounded once to the output's type.
  *
  * spec_rotary_frequencies - f_j = base^(-2 j / dim), scaled for contexts `factor` times as long, into frequency [dim / 2] (host):
  *   SPEC_ROTARY_PLAIN   as they are;

@@ -4,7 +4,8 @@
 //   a' = m (a cos - b sin),   b' = m (b cos + a sin).
 // The angle is kept in turns, as a 64-bit fraction: with T_j = 2^64 f_j / 2 pi the product p T_j modulo 2^64 is the
 // fraction of the turn, so whole turns fall away exactly, in two integer multiplications, at any position.  (In float32 an angle of
-// 131,072 radians is known to 0.008; the product here is off by p 2^-56 turns, the rounding of T_j.)  The nearest quarter
+// 131,072 radians is known to 0.008; the product here is off by p times what T_j is: it comes from double arithmetic, within |f_j / 2 pi| 2^-52 + 2^-54
+// turns, for frequencies up to 1 within 2^-55.  At position 131,072 that is 2^-38 turns, at 2^31 2^-24.)  The nearest quarter
 // turn is taken off in integers as well, and what is left, at most an eighth, goes to sincospif.
 //
 // Bound by memory: a row's sines and cosines are computed once, by a warp, into shared memory and serve all its heads; every element
