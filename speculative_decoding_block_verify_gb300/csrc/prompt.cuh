@@ -47,10 +47,6 @@ __device__ __forceinline__ Keys keys_of(const PromptParams& p, int at, int token
     k.tiles = k.sink_tiles + (int)(((unsigned)k.high + kTile - 1) / kTile) - k.first_tile;
     return k;
 }
-template <int kTile>
-__device__ __forceinline__ int start_of(int sink_tiles, int first_tile, int t) {
-    return (t < sink_tiles ? t : first_tile + t - sink_tiles) * kTile;
-}
 
 // (there are fewer than 2^31 rows)
 __device__ __forceinline__ int prompt_row(const PromptParams& p, int b) { return p.a.cu_rows == nullptr ? b * p.rows_each : *(p.a.cu_rows + b); }
