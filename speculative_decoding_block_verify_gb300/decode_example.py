@@ -82,39 +82,30 @@ def forward(torch, target, cache, tokens, cu, kmax, state):
     if target.rotary is None and cache.table.shape[1] * cache.page > target.position.shape[0]:
         raise ValueError(f"the cache has room for {cache.table.shape[1] * cache.page} tokens a stream, the model for "
                          f"{target.position.shape[0]}")
-    rows = tokens.numel()
-    if target.rotary is not None:
-        def block(i, qkv):
-            H, G = target.q_heads, target.kv_heads
-            turn = ("append", rows)
-            state[turn] = a = sv.spec_cache_append_rotated(
-                qkv[:, :H], qkv[:, H:H + G], qkv[:, H + G:], cache.k[i], cache.v[i], cache.table, cache.length, target.rotary, cu_drafts=cu,
-                kmax=kmax, reserved=cache.reserved, out=state.get(turn))
-            key = ("attention", rows, kmax)
-            state[key] = o = sv.spec_paged_attention(a["q"], cache.k[i], cache.v[i], cache.table, cache.length, cu, kmax, target.head ** -0.5,
-                                                     out=state.get(key))
-            return o["out"], a["status"], o["status"]
-        return layers(torch, target, tokens, target.embedding[tokens.long()], cache.reserved, block, state)
-    stream = torch.searchsorted(cu + torch.arange(cu.numel(), device=cu.device), torch.arange(rows, device=cu.device), right=True) - 1
-    at = cache.length[stream] + torch.arange(rows, device=cu.device) - cu[stream] - stream
-    # a block that does not fit its stream's table row is refused by the calls below, and its rows stand for nothing
-    x = target.embedding[tokens.long()] + target.position[at.clamp(max=target.position.shape[0] - 1)]
-    H, G, D = target.q_heads, target.kv_heads, target.head
-    status = cache.reserved
-    for i in range(target.layers):
-        qkv = (x @ target.qkv[i]).view(rows, H + 2 * G, D)
+    rows, H, G = tokens.numel(), target.q_heads, target.kv_heads
+    x = target.embedding[tokens.long()]
+    if target.rotary is None:
+        stream = torch.searchsorted(cu + torch.arange(cu.numel(), device=cu.device), torch.arange(rows, device=cu.device), right=True) - 1
+        at = cache.length[stream] + torch.arange(rows, device=cu.device) - cu[stream] - stream
+        # a block that does not fit its stream's table row is refused by the calls below, and its rows stand for nothing
+        x = x + target.position[at.clamp(max=target.position.shape[0] - 1)]
+
+    def block(i, qkv):
         # slices of the projection go in as they lie
-        state["append"] = sv.spec_cache_append(qkv[:, H:H + G], qkv[:, H + G:], cache.k[i], cache.v[i], cache.table,
-                                               cache.length, cu, kmax, out=state.get("append"), reserved=cache.reserved)
+        q, k, v = qkv[:, :H], qkv[:, H:H + G], qkv[:, H + G:]
+        pool = (cache.k[i], cache.v[i], cache.table, cache.length)
+        turn = ("append", rows)
+        if target.rotary is None:
+            a = sv.spec_cache_append(k, v, *pool, cu, kmax, out=state.get(turn), reserved=cache.reserved)
+        else:
+            a = sv.spec_cache_append_rotated(q, k, v, *pool, target.rotary, cu_drafts=cu, kmax=kmax, out=state.get(turn), reserved=cache.reserved)
+            q = a["q"]
+        state[turn] = a
         key = ("attention", rows, kmax)
-        state[key] = sv.spec_paged_attention(qkv[:, :H], cache.k[i], cache.v[i], cache.table, cache.length, cu, kmax,
-                                             D ** -0.5, out=state.get(key))
-        status = first_of(torch, status, state["append"]["status"], state[key]["status"])
-        x = x + state[key]["out"].view(rows, H * D) @ target.o[i]
-        x = x * torch.rsqrt((x.float() ** 2).mean(dim=1, keepdim=True)).to(x.dtype)
-    state["status"] = status
-    W1, W2 = target.table
-    return (x @ target.logits).float() + W1[tokens.long()] @ W2
+        state[key] = o = sv.spec_paged_attention(q, *pool, cu, kmax, target.head ** -0.5, out=state.get(key))
+        return o["out"], a["status"], o["status"]
+
+    return layers(torch, target, tokens, x, cache.reserved, block, state)
 
 
 def layers(torch, target, tokens, x, status, attend, state):
