@@ -534,8 +534,8 @@ static Turn plan(int D, int dim, int interleaved, int dtype, float magnitude, co
 // Rows and units of a CTA: what fills the resident CTAs (six an SM) once, from one to eight units a thread, and in whole rows where a thread has
 // more than one: a row's sines, and an append's search for its stream, are every CTA's that has a part of it.  8,191 rows of 72 heads of 128 take 47.7 us with eight units, 52.0
 // with six and 55.2 with sixteen; 900 float32 rows of 48 heads appended 6.9 us a row a CTA and 10.2 in three parts.
-static void share(int64_t rows, int64_t per_row, int* rows_each, int* units_each, dim3* grid) {
-    const int64_t fill = rows * per_row / (152 * 6);
+static void share(int64_t rows, int64_t per_row, int sms, int* rows_each, int* units_each, dim3* grid) {
+    const int64_t fill = rows * per_row / (sms * 6);
     const int64_t want = fill < kTurnThreads ? kTurnThreads : fill > 8 * kTurnThreads ? 8 * kTurnThreads : fill;
     const int64_t each = want / per_row < 1 ? 1 : want / per_row > kTurnRows ? kTurnRows : want / per_row;
     const int64_t splits = each > 1 ? 1 : want == kTurnThreads ? (per_row + want - 1) / want : per_row < 2 * want ? 1 : per_row / want;
@@ -634,11 +634,13 @@ extern "C" int spec_rotate(const spec_rotate_args* a, void* stream) {
         return set_error(SPEC_ERR_ARG, "spec_rotate: a required pointer is NULL");
     const int es = element(a->dtype);
     const bool even = (((uintptr_t)a->x | (uintptr_t)a->out | (uintptr_t)(a->x_row_stride * es) | (uintptr_t)(a->out_row_stride * es)) & 15) == 0;
-    int mode;
+    int mode, sms = 0;
+    const int count = sm_count(&sms, "spec_rotate");
+    if (count != SPEC_OK) return count;
     const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, even, &mode);
     int rows_each, units_each;
     dim3 grid;
-    share(a->rows, (int64_t)a->heads * t.units, &rows_each, &units_each, &grid);
+    share(a->rows, (int64_t)a->heads * t.units, sms, &rows_each, &units_each, &grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = es == 4 ? pick<float, spec_rotate_args, Rotates>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s)
                                   : pick<unsigned short, spec_rotate_args, Rotates>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s);
@@ -675,11 +677,13 @@ extern "C" int spec_cache_append_rotated(const spec_append_rotated_args* a, void
     uintptr_t low = (uintptr_t)a->k | (uintptr_t)a->v | (uintptr_t)(a->k_row_stride * es) | (uintptr_t)(a->v_row_stride * es);
     if (a->Hq > 0) low |= (uintptr_t)a->q | (uintptr_t)a->q_out | (uintptr_t)(a->q_row_stride * es) | (uintptr_t)(a->q_out_row_stride * es);
     if (a->k_out != nullptr) low |= (uintptr_t)a->k_out | (uintptr_t)(a->k_out_row_stride * es);
-    int mode;
+    int mode, sms = 0;
+    const int count = sm_count(&sms, who);
+    if (count != SPEC_OK) return count;
     const Turn t = plan(a->D, a->dim, a->interleaved, a->dtype, a->magnitude, a->turns, (low & 15) == 0, &mode);
     int rows_each, units_each;
     dim3 grid;
-    share(a->rows, (int64_t)(a->Hq + a->Hkv) * t.units + (int64_t)a->Hkv * t.copies, &rows_each, &units_each, &grid);
+    share(a->rows, (int64_t)(a->Hq + a->Hkv) * t.units + (int64_t)a->Hkv * t.copies, sms, &rows_each, &units_each, &grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = es == 4
                               ? pick<float, spec_append_rotated_args, Appends>(*a, t, mode, a->interleaved != 0, rows_each, units_each, grid, s)
