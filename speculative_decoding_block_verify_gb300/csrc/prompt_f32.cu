@@ -2,8 +2,8 @@
 //
 // The kernel of the paged attention (attention_f32.cuh) with another source: tiles of 64 keys and values come from packed rows
 // by one tiled copy each, and the items are pieces of prompts (prompt.cuh), whole ones, so nothing is joined.  Five prompts of 100 to 1,500
-// tokens, 32/8 heads of 128: 276 us, 197 TFLOP/s, with six bf16 products for each float32 one 0.63 of the measured bf16 rate (282 us with the walk and
-// the copies in one warp); the tensor cores are busy for 53 % of the cycles, and the softmax with its split into three parts is what they wait for.
+// tokens, 32/8 heads of 128: 279 to 289 us, 188 to 195 TFLOP/s, with six bf16 products for each float32 one 0.60 to 0.62 of the measured bf16 rate (the walk and
+// the copies in one warp: 282 us where this took 276); the tensor cores are busy for 53 % of the cycles, and the softmax with its split into three parts is what they wait for.
 #include "attention_f32.cuh"
 #include "prompt.cuh"
 #include "tensor_map.h"

@@ -12,10 +12,10 @@
 // tensor memory when the maximum has risen by more than 8 (2^8 of headroom is nothing to float32, and most tiles then leave O alone).
 // Warp 11 finds the items, warp 8 copies keys and values by TMA, warp 10 the rows of Q, warp 9 issues the products.
 //
-// What it measured (one GB300; a graph of 20 calls on two inputs by turns): one prompt of 16,001 tokens, 64/8 heads of 128, 2.63 ms, 1,596
-// TFLOP/s, 0.85 of what the library's largest bf16 product reaches; 24 prompts of 17 to 2,000 tokens 173 us (0.57: a quarter of the tiles'
-// scores lie above the diagonal or past a prompt's end, and an item's beginning and end take two tiles' time); six prompts of 2,000 to 9,000
-// with a window of 1,024 and 4 first tokens 605 us (0.60); 333 tokens 9.0 us, 17 tokens 7.2 (latency).
+// What it measured (one GB300; a graph of 20 calls on two inputs by turns): one prompt of 16,001 tokens, 64/8 heads of 128, 2.55 to 2.64 ms, 1,589 to
+// 1,642 TFLOP/s, 0.84 to 0.87 of what the library's largest bf16 product reaches (2.69 ms as calls from Python, 2.86 on a slower card); 24 prompts of 17
+// to 2,000 tokens 169 us (0.59: an item's beginning and end take two tiles' time, and it has five; 12 % of the tiles' scores are unseen); six prompts of
+// 2,000 to 9,000 with a window of 1,024 and 4 first tokens 575 us (0.63); 333 tokens 9.0 us, 17 tokens 7.3 (latency).
 // What bounds it: a tile of both groups takes about 3,000 cycles, 2,048 of them products.  The softmax of a group takes about 1,500 (a warp alone on
 // its quarter of the SM, 600 instructions one behind the other), then its products have to run before it has scores again: neither the tensor cores
 // (about two thirds of the cycles) nor the function units (a third) are full, the chain is.  What did not shorten it:
